@@ -266,6 +266,71 @@ W4A16_API w4a16_status_t w4a16_swiglu_mlp_static(const void* x, w4a16_dtype_t xt
                                                  const w4a16_weight_t* down, float* y, hipStream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection.  A projection
+ * W [K -> N] is served with num_adapters adapters; a row m with adapter
+ * id = adapter_ids[m] takes
+ *   y[m] = x[m] W + scale[id] * (x[m] a[id]^T) b[id]^T,
+ * and a row whose id is outside [0, num_adapters) (-1 by convention) takes
+ * x[m] W alone.  a and b are bf16 in the layouts adapters are trained and
+ * saved in, k and the rank contiguous.  Adapters of smaller ranks share a
+ * stack through `ranks`: adapter id uses its first ranks[id] ranks (clamped to
+ * [0, rank]; the rest of its slots is not used, whatever it holds), so
+ * `rank` is the largest.
+ */
+typedef struct {
+  const void* a;         /* device: bf16 [num_adapters][rank][K] */
+  const void* b;         /* device: bf16 [num_adapters][N][rank] */
+  const float* scale;    /* device: float32 [num_adapters] (alpha / rank) */
+  const int32_t* ranks;  /* device: int32 [num_adapters], or NULL: `rank` for every adapter */
+  int32_t rank;          /* a multiple of 8, 8 .. 256 */
+  int32_t num_adapters;  /* at least 1 */
+} w4a16_lora_t;
+
+/* Bytes of workspace w4a16_gemm_lora needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_gemm_lora_workspace_bytes(int32_t M, const w4a16_weight_t* w, w4a16_dtype_t xt,
+                                                 const w4a16_lora_t* lora);
+
+/*
+ * w4a16_gemm with an adapter for each row: y[M][N] as above, of type yt
+ * (float32, or bf16 rounded once, to nearest even).  x, W and the first term
+ * are as in w4a16_gemm.  The adapters' products run on bf16 matrix-core
+ * operands with float32 sums; a float32 x, and x a^T, enter as three bf16
+ * pieces (24 significant bits).  adapter_ids is int32 [M], in any order;
+ * rows of one adapter that stand together share its reads.  Rows do not
+ * affect one another: an infinity or NaN in x[m] or in one adapter reaches
+ * the rows that use it only.  Deterministic.
+ * Errors: as w4a16_gemm, plus INVALID_ARG for a null lora, a, b, scale or
+ * adapter_ids, misaligned pointers, rank < 1, num_adapters < 1 or an unknown
+ * yt, and UNSUPPORTED for a rank that is not a multiple of 8 or above 256.
+ */
+W4A16_API w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_weight_t* w,
+                                         const w4a16_lora_t* lora, const int32_t* adapter_ids, void* y,
+                                         w4a16_dtype_t yt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_swiglu_mlp_lora needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_weight_t* gate,
+                                                       const w4a16_weight_t* up, const w4a16_weight_t* down,
+                                                       const w4a16_lora_t* lora_gate, const w4a16_lora_t* lora_up,
+                                                       const w4a16_lora_t* lora_down);
+
+/*
+ * w4a16_swiglu_mlp with an adapter for each row on any of its projections:
+ * gate and up are x Wg and x Wu each with its adapter term, h = silu(gate) *
+ * up, and y is h Wd with its adapter term (of h), of type yt.  lora_gate,
+ * lora_up and lora_down may each be NULL (no adapters on that projection) and
+ * may differ in rank and number of adapters; one adapter_ids [M] serves all
+ * three.  h stays float32 between the projections, and enters the adapters'
+ * product in three bf16 pieces.
+ * Errors: as w4a16_swiglu_mlp and w4a16_gemm_lora (but a null lora is none).
+ */
+W4A16_API w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt, int32_t M,
+                                               const w4a16_weight_t* gate, const w4a16_weight_t* up,
+                                               const w4a16_weight_t* down, const w4a16_lora_t* lora_gate,
+                                               const w4a16_lora_t* lora_up, const w4a16_lora_t* lora_down,
+                                               const int32_t* adapter_ids, void* y, w4a16_dtype_t yt, void* ws,
+                                               size_t ws_bytes, hipStream_t stream);
+
+/*
  * Router: the top_k experts of every token and their gate weights (page "The
  * Final Wire", section "What the Edit Actually Changes": for each token the
  * router selects top-k experts).  The pages give no gating rule; this library

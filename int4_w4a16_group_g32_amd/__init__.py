@@ -37,6 +37,10 @@ EXPORTS = (
     "w4a16_swiglu_mlp",
     "w4a16_swiglu_mlp_timed",
     "w4a16_swiglu_mlp_static",
+    "w4a16_gemm_lora_workspace_bytes",
+    "w4a16_gemm_lora",
+    "w4a16_swiglu_mlp_lora_workspace_bytes",
+    "w4a16_swiglu_mlp_lora",
     "w4a16_moe_topk",
     "w4a16_moe_route",
     "w4a16_moe_workspace_bytes",
@@ -65,6 +69,17 @@ class WeightDesc(ctypes.Structure):
     ]
 
 
+class LoraDesc(ctypes.Structure):
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("ranks", ctypes.c_void_p),
+        ("rank", ctypes.c_int32),
+        ("num_adapters", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -77,6 +92,7 @@ def load_library() -> ctypes.CDLL:
         lib = ctypes.CDLL(LIB_PATH)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         dp = ctypes.POINTER(WeightDesc)
+        lp = ctypes.POINTER(LoraDesc)
         sig = {
             "w4a16_status_string": (ctypes.c_char_p, [i32]),
             "w4a16_workspace_init": (i32, [vp, sz, vp]),
@@ -93,6 +109,10 @@ def load_library() -> ctypes.CDLL:
             "w4a16_swiglu_mlp_timed": (i32, [vp, i32, i32, dp, dp, dp, vp, vp, sz, vp, vp, i32,
                                              ctypes.POINTER(i32)]),
             "w4a16_swiglu_mlp_static": (i32, [vp, i32, i32, dp, dp, dp, vp, vp]),
+            "w4a16_gemm_lora_workspace_bytes": (sz, [i32, dp, i32, lp]),
+            "w4a16_gemm_lora": (i32, [vp, i32, i32, dp, lp, vp, vp, i32, vp, sz, vp]),
+            "w4a16_swiglu_mlp_lora_workspace_bytes": (sz, [i32, i32, dp, dp, dp, lp, lp, lp]),
+            "w4a16_swiglu_mlp_lora": (i32, [vp, i32, i32, dp, dp, dp, lp, lp, lp, vp, vp, i32, vp, sz, vp]),
             "w4a16_moe_topk": (i32, [vp, i32, i32, i32, vp, vp, vp]),
             "w4a16_moe_route": (i32, [vp, i32, i32, i32, vp, vp, vp, vp, vp]),
             "w4a16_moe_workspace_bytes": (sz, [i32, i32, i32, dp, dp, dp]),
@@ -184,6 +204,35 @@ class Weight:
                           self.num_experts, self.layout)
 
 
+@dataclass
+class Lora:
+    """The adapters of one projection [K -> N], one stack for all requests."""
+    a: torch.Tensor                     # bfloat16 [n][R][K]
+    b: torch.Tensor                     # bfloat16 [n][N][R]
+    scale: torch.Tensor                 # float32 [n]
+    ranks: torch.Tensor | None = None   # int32 [n]: ranks in use (None: R)
+
+    def desc(self) -> LoraDesc:
+        return LoraDesc(self.a.data_ptr(), self.b.data_ptr(), self.scale.data_ptr(),
+                        None if self.ranks is None else self.ranks.data_ptr(), self.a.shape[1], self.a.shape[0])
+
+    def check(self, K: int, N: int):
+        """The stack's dtypes, shapes and devices for a projection [K -> N]."""
+        if not isinstance(self.a, torch.Tensor) or self.a.dim() != 3:
+            raise ValueError("lora.a must be [num_adapters][rank][K]")
+        n, R, _ = self.a.shape
+        _need(self.a, "lora.a", torch.bfloat16, (n, R, K))
+        _need(self.b, "lora.b", torch.bfloat16, (n, N, R))
+        _need(self.scale, "lora.scale", torch.float32, (n,))
+        if self.ranks is not None:
+            _need(self.ranks, "lora.ranks", torch.int32, (n,))
+        _on_device(lora_a=self.a, lora_b=self.b, lora_scale=self.scale, lora_ranks=self.ranks)
+
+
+def _lref(lora):
+    return None if lora is None else ctypes.byref(lora.desc())
+
+
 def _dref(w):
     return None if w is None else ctypes.byref(w.desc() if isinstance(w, Weight) else w)
 
@@ -269,6 +318,60 @@ def swiglu_mlp_static(x: torch.Tensor, gate: Weight, up: Weight, down: Weight, y
     _on_device(x=x, y=y)
     _check(load_library().w4a16_swiglu_mlp_static(_ptr(x), _dtype_code(x), x.shape[0], _dref(gate), _dref(up),
                                                   _dref(down), _ptr(y), _stream(stream)), "w4a16_swiglu_mlp_static")
+
+
+def _need_y(y, shape) -> int:
+    """y float32 or bfloat16 of this shape; returns its dtype code."""
+    yt = _dtype_code(y)
+    _need(y, "y", y.dtype, shape)
+    return yt
+
+
+def _need_ids(adapter_ids, M: int):
+    _need(adapter_ids, "adapter_ids", torch.int32, (M,))
+    _on_device(adapter_ids=adapter_ids)
+
+
+def gemm_lora_workspace_bytes(M: int, w: Weight, xt: int, lora: Lora) -> int:
+    return load_library().w4a16_gemm_lora_workspace_bytes(M, _dref(w), xt, _lref(lora))
+
+
+def gemm_lora(x: torch.Tensor, w: Weight, lora: Lora, adapter_ids: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
+              stream=None):
+    """gemm plus each row's low-rank adapter (adapter_ids int32 [M], -1: none); y float32 or bfloat16."""
+    _need_x(x, w.K)
+    lora.check(w.K, w.N)
+    _need_ids(adapter_ids, x.shape[0])
+    yt = _need_y(y, (x.shape[0], w.N))
+    _need(ws, "ws", torch.uint8)
+    _on_device(x=x, y=y, ws=ws)
+    _check(load_library().w4a16_gemm_lora(_ptr(x), _dtype_code(x), x.shape[0], _dref(w), _lref(lora),
+                                          _ptr(adapter_ids), _ptr(y), yt, _ptr(ws), _nbytes(ws), _stream(stream)),
+           "w4a16_gemm_lora")
+
+
+def swiglu_mlp_lora_workspace_bytes(M: int, xt: int, gate: Weight, up: Weight, down: Weight, lora_gate: Lora | None,
+                                    lora_up: Lora | None, lora_down: Lora | None) -> int:
+    return load_library().w4a16_swiglu_mlp_lora_workspace_bytes(M, xt, _dref(gate), _dref(up), _dref(down),
+                                                                _lref(lora_gate), _lref(lora_up), _lref(lora_down))
+
+
+def swiglu_mlp_lora(x: torch.Tensor, gate: Weight, up: Weight, down: Weight, lora_gate: Lora | None,
+                    lora_up: Lora | None, lora_down: Lora | None, adapter_ids: torch.Tensor, y: torch.Tensor,
+                    ws: torch.Tensor, stream=None):
+    """swiglu_mlp plus each row's low-rank adapters on any of the three projections (None: no adapters there)."""
+    _need_x(x, gate.K)
+    for lora, w in ((lora_gate, gate), (lora_up, up), (lora_down, down)):
+        if lora is not None:
+            lora.check(w.K, w.N)
+    _need_ids(adapter_ids, x.shape[0])
+    yt = _need_y(y, (x.shape[0], down.N))
+    _need(ws, "ws", torch.uint8)
+    _on_device(x=x, y=y, ws=ws)
+    _check(load_library().w4a16_swiglu_mlp_lora(_ptr(x), _dtype_code(x), x.shape[0], _dref(gate), _dref(up),
+                                                _dref(down), _lref(lora_gate), _lref(lora_up), _lref(lora_down),
+                                                _ptr(adapter_ids), _ptr(y), yt, _ptr(ws), _nbytes(ws),
+                                                _stream(stream)), "w4a16_swiglu_mlp_lora")
 
 
 def moe_topk(logits: torch.Tensor, top_k: int, topk_ids: torch.Tensor, topk_w: torch.Tensor, stream=None):

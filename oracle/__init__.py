@@ -22,3 +22,10 @@ from .w4a16 import (  # noqa: F401
     moe_shared64,
     rel_frobenius,
 )
+from .lora import (  # noqa: F401
+    gemm_lora64,
+    lora_rank,
+    lora_rows,
+    lora_term64,
+    swiglu_mlp_lora64,
+)
