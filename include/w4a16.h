@@ -421,6 +421,47 @@ W4A16_API w4a16_status_t w4a16_moe_grouped_shared(const void* x, w4a16_dtype_t x
                                         size_t ws_bytes, hipStream_t stream);
 
 /*
+ * Bytes of workspace w4a16_moe_decode needs (0 for invalid arguments).  The
+ * shared expert's three descriptors are all NULL or all given.
+ */
+W4A16_API size_t w4a16_moe_decode_workspace_bytes(int32_t M, int32_t top_k, w4a16_dtype_t xt,
+                                                  const w4a16_weight_t* gate, const w4a16_weight_t* up,
+                                                  const w4a16_weight_t* down, const w4a16_weight_t* shared_gate,
+                                                  const w4a16_weight_t* shared_up,
+                                                  const w4a16_weight_t* shared_down);
+
+/*
+ * The whole MoE layer for a few tokens, from router logits to outputs, in two
+ * kernels: the choice of w4a16_moe_topk, then the layer of w4a16_moe_grouped
+ * (or, with a shared expert, w4a16_moe_grouped_shared), for up to 8 tokens
+ * with float32 x or 16 with bf16 x.
+ *   y[t] = sum over the chosen experts e of w[t][e] MLP_e(x[t])  (+ MLP_shared(x[t]))
+ * summed in ascending expert index, the shared expert last; y is of type yt
+ * (float32, or bf16 rounded once, to nearest even).  The weights are streamed
+ * once whatever the tokens choose, and the choice needs no launch of its own.
+ * h = silu(gate) up stays float32 until the down projection takes it, times
+ * its gate weight, as f16 pieces (two with float32 x, one with bf16 x) scaled
+ * by a power of two.  Deterministic, but not bitwise w4a16_moe_grouped.
+ * logits [M][E] float32: a NaN counts as -infinity.  The k largest, ties in
+ * ascending expert index, as in w4a16_moe_topk, also where they are infinite:
+ * an expert at -infinity has weight 0, +infinity counts as the largest finite
+ * value, and a token with no logit above -infinity has weight 0 everywhere.
+ * An expert of weight 0 is not read.  topk_ids and topk_w [M][top_k] receive
+ * the choice, each unless NULL.
+ * Rows do not affect one another: an infinity or NaN in x[t] reaches y[t]
+ * only.
+ * Errors: as w4a16_moe_grouped_shared (INVALID_ARG also where one or two of
+ * the shared descriptors are NULL, and for an unknown yt), plus UNSUPPORTED
+ * for more tokens than above, more than 1024 experts or top_k above 32.
+ */
+W4A16_API w4a16_status_t w4a16_moe_decode(const void* x, w4a16_dtype_t xt, int32_t M, const float* logits,
+                                          int32_t top_k, const w4a16_weight_t* gate, const w4a16_weight_t* up,
+                                          const w4a16_weight_t* down, const w4a16_weight_t* shared_gate,
+                                          const w4a16_weight_t* shared_up, const w4a16_weight_t* shared_down,
+                                          int32_t* topk_ids, float* topk_w, void* y, w4a16_dtype_t yt, void* ws,
+                                          size_t ws_bytes, hipStream_t stream);
+
+/*
  * Measurement variant of w4a16_moe_grouped: identical work and results, and in
  * addition brackets each kernel it launches with two of the caller's events,
  * as w4a16_swiglu_mlp_timed does: events[2i] at the start and events[2i+1] at

@@ -47,6 +47,8 @@ EXPORTS = (
     "w4a16_moe_grouped",
     "w4a16_moe_shared_workspace_bytes",
     "w4a16_moe_grouped_shared",
+    "w4a16_moe_decode_workspace_bytes",
+    "w4a16_moe_decode",
     "w4a16_moe_grouped_timed",
 )
 
@@ -120,6 +122,8 @@ def load_library() -> ctypes.CDLL:
             "w4a16_moe_shared_workspace_bytes": (sz, [i32, i32, i32, dp, dp, dp, dp, dp, dp]),
             "w4a16_moe_grouped_shared": (i32, [vp, i32, i32, vp, vp, i32, dp, dp, dp, dp, dp, dp, vp, vp, sz,
                                                vp]),
+            "w4a16_moe_decode_workspace_bytes": (sz, [i32, i32, i32, dp, dp, dp, dp, dp, dp]),
+            "w4a16_moe_decode": (i32, [vp, i32, i32, vp, i32, dp, dp, dp, dp, dp, dp, vp, vp, vp, i32, vp, sz, vp]),
             "w4a16_moe_grouped_timed": (i32, [vp, i32, i32, vp, vp, i32, dp, dp, dp, vp, vp, sz, vp, vp,
                                               i32, ctypes.POINTER(i32)]),
         }
@@ -445,6 +449,34 @@ def moe_grouped(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, g
                                             _dref(gate), _dref(up), _dref(down), _ptr(y), _ptr(ws),
                                             ws.numel() * ws.element_size(), _stream(stream)),
            "w4a16_moe_grouped")
+
+
+def moe_decode_workspace_bytes(M: int, top_k: int, xt: int, gate: Weight, up: Weight, down: Weight,
+                               shared: tuple[Weight, Weight, Weight] | None = None) -> int:
+    sg, su, sd = shared if shared is not None else (None, None, None)
+    return load_library().w4a16_moe_decode_workspace_bytes(M, top_k, xt, _dref(gate), _dref(up), _dref(down),
+                                                           _dref(sg), _dref(su), _dref(sd))
+
+
+def moe_decode(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate: Weight, up: Weight, down: Weight,
+               y: torch.Tensor, ws: torch.Tensor, shared: tuple[Weight, Weight, Weight] | None = None,
+               topk_ids: torch.Tensor | None = None, topk_w: torch.Tensor | None = None, stream=None):
+    """The MoE layer of a few tokens from its router logits (at most 8 float32 or 16 bfloat16 rows); y float32
+    or bfloat16, shared = (gate, up, down) of a shared expert, topk_ids / topk_w receive the choice."""
+    _need_x(x, gate.K)
+    M = x.shape[0]
+    _need(logits, "logits", torch.float32, (M, gate.num_experts))
+    yt = _need_y(y, (M, down.N))
+    _need(ws, "ws", torch.uint8)
+    if topk_ids is not None:
+        _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
+    if topk_w is not None:
+        _need(topk_w, "topk_w", torch.float32, (M, top_k))
+    _on_device(x=x, logits=logits, y=y, ws=ws, topk_ids=topk_ids, topk_w=topk_w)
+    sg, su, sd = shared if shared is not None else (None, None, None)
+    _check(load_library().w4a16_moe_decode(_ptr(x), _dtype_code(x), M, _ptr(logits), top_k, _dref(gate), _dref(up),
+                                           _dref(down), _dref(sg), _dref(su), _dref(sd), _ptr(topk_ids), _ptr(topk_w),
+                                           _ptr(y), yt, _ptr(ws), _nbytes(ws), _stream(stream)), "w4a16_moe_decode")
 
 
 # ---------------------------------------------------------------- helpers
