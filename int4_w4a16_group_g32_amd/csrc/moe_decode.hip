@@ -9,16 +9,16 @@
 // weights stream (27.5 MB each at hidden 7168, intermediate 2048): what it
 // must avoid is launches and idle CUs.  Every workgroup of the first launch
 // routes all the tokens itself (they fit one workgroup's waves), so there is
-// no routing launch.  The first launch gives one workgroup an expert, a
-// column tile of gate and up and a K split, and stores the split sums per
-// (token, slot) pair.  The second treats the down projections of all chosen
+// no routing launch; it then forms h for one expert and one tile of columns
+// over the whole of K, its waves sharing columns and K between them, and
+// stores h times the gate weight per (expert, token) pair with its largest
+// magnitude.  The second launch treats the down projections of all chosen
 // experts as one long product: its K axis runs through the experts one after
 // another, A row t holds token t's weighted h where the expert is one of
 // its own and zero elsewhere, so one accumulator sums over experts as well.
 // That axis is cut into equal pieces, and the last workgroup of a column tile
 // to arrive adds the pieces in order.
 #include <cfloat>
-#include <type_traits>
 
 #include "dispatch.h"
 #include "stream.h"
@@ -26,12 +26,13 @@
 namespace w4 {
 namespace {
 
-constexpr int kMdQuad = 256;      // threads of a quad: four waves, 256 columns
 constexpr int kMdMaxE = 1024;
 constexpr int kMdMaxK = 32;
-constexpr int kMdRing = 4;        // groups of codes in flight per wave
+constexpr int kMdMaxThreads = 1024;
+constexpr int kMdCus = 256;       // 16 waves resident on each
+constexpr int kMdUnits = 512;     // window units (16 bytes) per wave: four workgroups of 4 waves share a CU
+constexpr int kMdCols = 256;      // output columns of a down tile (four blocks of 64)
 constexpr int kMdMaxSplits = 64;  // pieces of the down projection's long axis
-constexpr int kMdTarget = 1024;   // quads resident at once (four per CU)
 
 // What the tokens chose: the distinct experts of nonzero weight in ascending
 // order (the items), which tokens each serves, and the gate weights of the
@@ -42,7 +43,8 @@ struct MdItems {
   short experts[kStreamRows * kMdMaxK];     // by item
   uint16_t tokens[kStreamRows * kMdMaxK];   // by item: bit t
   uint16_t first[kStreamRows * kMdMaxK];    // by item
-  int n, pad[3];
+  uint8_t token[kStreamRows * kMdMaxK];     // by pair
+  int n, pairs, pad[2];
 };
 
 // The choices as they are made, before they are turned into items.
@@ -58,151 +60,192 @@ __device__ __forceinline__ int md_pair(const MdItems& it, int item, int t) {
   return it.first[item] + __popc(it.tokens[item] & ((1u << t) - 1u));
 }
 
-// A wave-uniform value in scalar registers.
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return static_cast<uint64_t>(hi) << 32 | lo;
-}
-
-// Largest value of the wave, as a scalar: row shifts within 16 lanes, then
-// broadcasts across rows; lane 63 ends with all of them.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  auto step = [&](auto ctrl, auto rows) {
-    const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
-        0, static_cast<int>(v), decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
-    v = v > t ? v : t;
-  };
-  using std::integral_constant;
-  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
-  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
-  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
-}
-
 // One wave selects a token's experts: the largest logits first, equal ones in
 // ascending expert index, NaN as -infinity.  Keys are the logits' bits in
-// unsigned order; 0 marks a taken or absent expert.  Weights are
-// exp(l - l_max) / sum over the chosen, as w4a16_moe_topk computes them; a
-// token with no logit above -infinity gets weight 0 everywhere.
+// unsigned order; 0 marks an absent expert.  Lane l holds the kJ experts from
+// l kJ on, sorted once (stably, so the lower index stays first); a round takes
+// the first lane with the wave's largest head and shifts that lane's list.
+// Weights are exp(l - l_max) / sum over the chosen, as w4a16_moe_topk
+// computes them; a token with no logit above -infinity gets weight 0
+// everywhere.
 template <int kJ>
 __device__ __forceinline__ void md_topk(const float* __restrict__ logits, int E, int k, int lane, short* ids,
                                         float* w) {
   uint32_t key[kJ];
+  uint64_t order = 0;  // four bits each: which of the lane's experts the sorted keys are
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
-    const int e = lane + kWave * j;
-    float v = e < E ? logits[e] : 0.0f;
+    const int e = lane * kJ + j;
+    float v = logits[min(e, E - 1)];
     if (v != v) v = -INFINITY;
     const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);  // -0 and 0 are equal
     key[j] = e < E ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
   }
-  float mine = 0.0f;
+  {
+    uint32_t idx[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) idx[j] = j;
+#pragma unroll
+    for (int pass = 0; pass < kJ; ++pass)  // odd-even transposition
+#pragma unroll
+      for (int j = pass & 1; j + 1 < kJ; j += 2) {
+        const bool swap = key[j] < key[j + 1];
+        const uint32_t hi = swap ? key[j + 1] : key[j], lo = swap ? key[j] : key[j + 1];
+        const uint32_t ih = swap ? idx[j + 1] : idx[j], il = swap ? idx[j] : idx[j + 1];
+        key[j] = hi;
+        key[j + 1] = lo;
+        idx[j] = ih;
+        idx[j + 1] = il;
+      }
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) order |= static_cast<uint64_t>(idx[j]) << (4 * j);
+  }
+  uint32_t mine_key = 0;
   int mine_e = 0;
   for (int r = 0; r < k; ++r) {
-    uint32_t best = key[0];
+    const uint32_t top = wave_max(key[0]);
+    const int l = __builtin_ctzll(__ballot(key[0] == top));
+    const int j = __builtin_amdgcn_readlane(static_cast<int>(order), l) & 15;
+    mine_key = lane == r ? top : mine_key;
+    mine_e = lane == r ? l * kJ + j : mine_e;
+    const bool taken = lane == l;
 #pragma unroll
-    for (int j = 1; j < kJ; ++j) best = best > key[j] ? best : key[j];
-    best = wave_max(best);
-    int e = -1;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      if (e < 0) {
-        const uint64_t at = __ballot(key[j] == best);
-        if (at != 0) e = kWave * j + __ffsll(static_cast<unsigned long long>(at)) - 1;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-      if (e == lane + kWave * j) key[j] = 0;
-    if (lane == r) {
-      mine = __uint_as_float(best & 0x80000000u ? best & 0x7fffffffu : ~best);
-      mine_e = e;
-    }
+    for (int i = 0; i + 1 < kJ; ++i) key[i] = taken ? key[i + 1] : key[i];
+    key[kJ - 1] = taken ? 0u : key[kJ - 1];
+    order = taken ? order >> 4 : order;
   }
+  float mine = __uint_as_float(mine_key & 0x80000000u ? mine_key & 0x7fffffffu : ~mine_key);
   mine = fminf(mine, FLT_MAX);  // inf - inf
-  const float vmax = __shfl(mine, 0);
+  const float vmax = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(mine)));
   const float z = lane < k && vmax > -INFINITY ? expf(mine - vmax) : 0.0f;
   float sum = z;
 #pragma unroll
   for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_down(sum, off);
-  sum = __shfl(sum, 0);
+  sum = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sum)));
   if (lane < k) {
     ids[lane] = static_cast<short>(mine_e);
     w[lane] = sum > 0.0f ? z / sum : 0.0f;
   }
 }
 
-// All tokens' choices, by every workgroup for itself (every thread calls it;
-// it ends with a barrier).
-__device__ __forceinline__ void md_route(const float* __restrict__ logits, int M, int E, int k, MdChoice& ch,
-                                         MdItems& it) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = lane_id();
-  if (tid < kMdMaxE / 32) ch.present[tid] = 0;
-  for (int i = tid; i < M * k; i += nt) ch.mask[i] = 0;
-  for (int t = wave_id(); t < M; t += nt / kWave) {
+// The tokens' choices, one wave a token.
+__device__ __forceinline__ void md_choose(const float* __restrict__ logits, int M, int E, int k, MdChoice& ch) {
+  const int lane = lane_id();
+  for (int t = wave_id(); t < M; t += static_cast<int>(blockDim.x) / kWave) {
     const float* l = logits + static_cast<size_t>(t) * E;
     if (E <= 2 * kWave)
       md_topk<2>(l, E, k, lane, ch.ids[t], ch.w[t]);
-    else if (E <= 8 * kWave)
-      md_topk<8>(l, E, k, lane, ch.ids[t], ch.w[t]);
+    else if (E <= 4 * kWave)
+      md_topk<4>(l, E, k, lane, ch.ids[t], ch.w[t]);
+    else if (E <= 6 * kWave)
+      md_topk<6>(l, E, k, lane, ch.ids[t], ch.w[t]);
     else
       md_topk<16>(l, E, k, lane, ch.ids[t], ch.w[t]);
   }
-  __syncthreads();
-  for (int p = tid; p < M * k; p += nt) {
-    const int e = ch.ids[p / k][p % k];
-    if (ch.w[p / k][p % k] != 0.0f) atomicOr(&ch.present[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  if (wave_id() == 0) {
-    uint32_t bits = lane < kMdMaxE / 32 ? ch.present[lane] : 0u;
-    const int c = __popc(bits);
-    int at = c;
+}
+
+// LDS accesses of one wave, in program order.
+__device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup"); }
+
+// Inclusive scan over the wave.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int t = __shfl_up(at, off);
-      if (lane >= off) at += t;
-    }
-    if (lane == kWave - 1) it.n = at;
-    at -= c;
-    if (lane < kMdMaxE / 32) ch.below[lane] = static_cast<short>(at);
-    for (; bits != 0; bits &= bits - 1) it.experts[at++] = static_cast<short>(32 * lane + __ffs(bits) - 1);
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int t = __shfl_up(v, off);
+    if (lane >= off) v += t;
   }
-  __syncthreads();
+  return v;
+}
+
+// The choices as items, by one wave.  Up to 64 (token, slot) pairs: one a lane,
+// each compared with all (about 700 cycles for 32 pairs, where the general
+// form takes about 4000).
+__device__ __forceinline__ void md_items64(int M, int k, int lane, const MdChoice& ch, MdItems& it) {
+  const int n = M * k, t = lane / k, s = lane - t * k;
+  const float w = lane < n ? ch.w[t][s] : 0.0f;
+  const int e = w != 0.0f ? ch.ids[t][s] : kMdMaxE;
+  int less = 0, earlier = 0;  // pairs of lower experts; of this one and a lower lane
+  uint32_t tokens = 0;
+  for (int j = 0; j < n; ++j) {
+    const int ej = __builtin_amdgcn_readlane(e, j), tj = __builtin_amdgcn_readlane(t, j);
+    less += ej < e ? 1 : 0;
+    earlier += ej == e && j < lane ? 1 : 0;
+    tokens |= ej == e ? 1u << tj : 0u;
+  }
+  const bool first = w != 0.0f && earlier == 0;
+  uint64_t firsts = __ballot(first);
+  const int items = __popcll(firsts), used = __popcll(__ballot(w != 0.0f));
+  int item = 0;
+  for (; firsts != 0; firsts &= firsts - 1) item += __builtin_amdgcn_readlane(e, __builtin_ctzll(firsts)) < e ? 1 : 0;
+  if (w != 0.0f) {  // lanes are in token order
+    it.w[less + earlier] = w;
+    it.token[less + earlier] = static_cast<uint8_t>(t);
+  }
+  if (first) {
+    it.experts[item] = static_cast<short>(e);
+    it.tokens[item] = static_cast<uint16_t>(tokens);
+    it.first[item] = static_cast<uint16_t>(less);
+  }
+  if (lane == 0) {
+    it.n = items;
+    it.pairs = used;
+  }
+}
+
+__device__ __forceinline__ void md_items(int M, int k, int lane, MdChoice& ch, MdItems& it) {
+  const int n = M * k;
+  if (n <= kWave) {
+    md_items64(M, k, lane, ch, it);
+    return;
+  }
+  if (lane < kMdMaxE / 32) ch.present[lane] = 0;
+  for (int p = lane; p < n; p += kWave) ch.mask[p] = 0;
+  wave_order();
+  for (int p = lane; p < n; p += kWave) {
+    const int t = p / k, s = p - t * k, e = ch.ids[t][s];
+    if (ch.w[t][s] != 0.0f) atomicOr(&ch.present[e >> 5], 1u << (e & 31));
+  }
+  wave_order();
+  uint32_t bits = lane < kMdMaxE / 32 ? ch.present[lane] : 0u;
+  const int c = __popc(bits);
+  int at = wave_scan(c, lane);
+  const int items = __shfl(at, kWave - 1);
+  at -= c;
+  if (lane < kMdMaxE / 32) ch.below[lane] = static_cast<short>(at);
+  for (; bits != 0; bits &= bits - 1) it.experts[at++] = static_cast<short>(32 * lane + __ffs(bits) - 1);
+  wave_order();
   auto item_of = [&](int e) {
     return ch.below[e >> 5] + __popc(ch.present[e >> 5] & ((1u << (e & 31)) - 1u));
   };
-  for (int p = tid; p < M * k; p += nt)
-    if (ch.w[p / k][p % k] != 0.0f) atomicOr(&ch.mask[item_of(ch.ids[p / k][p % k])], 1 << (p / k));
-  __syncthreads();
-  if (wave_id() == 0) {
-    int carry = 0;
-    for (int i0 = 0; i0 < it.n; i0 += kWave) {
-      const int m = i0 + lane < it.n ? ch.mask[i0 + lane] : 0;
-      const int c = __popc(m);
-      int at = c;
-#pragma unroll
-      for (int off = 1; off < kWave; off <<= 1) {
-        const int t = __shfl_up(at, off);
-        if (lane >= off) at += t;
-      }
-      if (i0 + lane < it.n) {
-        it.tokens[i0 + lane] = static_cast<uint16_t>(m);
-        it.first[i0 + lane] = static_cast<uint16_t>(carry + at - c);
-      }
-      carry += __shfl(at, kWave - 1);
+  for (int p = lane; p < n; p += kWave) {
+    const int t = p / k, s = p - t * k;
+    if (ch.w[t][s] != 0.0f) atomicOr(&ch.mask[item_of(ch.ids[t][s])], 1 << t);
+  }
+  wave_order();
+  int pairs = 0;
+  for (int i0 = 0; i0 < items; i0 += kWave) {
+    const int m = i0 + lane < items ? ch.mask[i0 + lane] : 0;
+    const int pc = __popc(m), incl = wave_scan(pc, lane);
+    if (i0 + lane < items) {
+      it.tokens[i0 + lane] = static_cast<uint16_t>(m);
+      it.first[i0 + lane] = static_cast<uint16_t>(pairs + incl - pc);
+    }
+    pairs += __shfl(incl, kWave - 1);
+  }
+  if (lane == 0) {
+    it.n = items;
+    it.pairs = pairs;
+  }
+  wave_order();
+  for (int p = lane; p < n; p += kWave) {
+    const int t = p / k, s = p - t * k;
+    const float w = ch.w[t][s];
+    if (w != 0.0f) {
+      const int pair = md_pair(it, item_of(ch.ids[t][s]), t);
+      it.w[pair] = w;
+      it.token[pair] = static_cast<uint8_t>(t);
     }
   }
-  __syncthreads();
-  for (int p = tid; p < M * k; p += nt) {
-    const float w = ch.w[p / k][p % k];
-    if (w != 0.0f) it.w[md_pair(it, item_of(ch.ids[p / k][p % k]), p / k)] = w;
-  }
-  __syncthreads();
 }
 
 struct MdArgs {
@@ -214,10 +257,11 @@ struct MdArgs {
   const u32x4 *xqg, *xqu, *xqd;  // shared expert (null: none)
   const float *xsg, *xsu, *xsd;
   int gshift, dshift;
-  int tiles, S, gps;     // gate/up: tiles of 128 h columns, K splits, groups per split
-  int dtiles, dsplits;   // down: tiles of 256 columns, pieces of the long axis
-  int pairs;             // M * k (+ M for the shared expert: pair M * k + t)
-  float* planes;         // [S][pairs][2][I] split sums of gate and up
+  int cols, tiles, parts, gpp;  // gate/up: 64-column blocks per workgroup, column tiles, K parts, groups a part
+  int dparts, dtiles, dsplits;  // down: K parts of a workgroup, column tiles, pieces of the long axis
+  int units;                                    // LDS units of a workgroup's window
+  float* h;              // [M * k (+ M)][I]: h times the gate weight, by pair (the shared expert's last)
+  float* amax;           // [M * k (+ M)][I / 64]: largest |h| of 64 columns
   float* partials;       // [dtiles][dsplits][M][256]
   int* counters;         // [dtiles], zero between calls
   MdItems* items;        // the choice, for the second launch
@@ -227,208 +271,263 @@ struct MdArgs {
   int y_bf16;
 };
 
-// 16 consecutive activations.
+// Shape of a workgroup's staged window: `wing` groups for each K part, 2^rshift
+// LDS rows a group.
+struct MdWindow {
+  int rshift, wing;
+};
 template <int kP>
-__device__ __forceinline__ void md_load_x(const void* x, size_t at, float v[16]) {
-  if (kP == 1) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint4 u = p[q];
-      const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        v[8 * q + 2 * t] = __uint_as_float(wd[t] << 16);
-        v[8 * q + 2 * t + 1] = __uint_as_float(wd[t] & 0xffff0000u);
-      }
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 u = p[q];
-      v[4 * q] = u.x;
-      v[4 * q + 1] = u.y;
-      v[4 * q + 2] = u.z;
-      v[4 * q + 3] = u.w;
-    }
-  }
+__device__ __forceinline__ MdWindow md_window(int rows, int units, int parts, int groups) {
+  MdWindow w;
+  w.rshift = stream_rshift<kP>(rows);
+  w.wing = max(kStreamRing, min(groups, (units / parts >> (w.rshift + 2)) / kStreamRing * kStreamRing));
+  return w;
 }
 
-// Gate and up of one expert, one tile of 128 h columns (of a quad's waves 0, 1
-// gate, 2, 3 the same columns of up), one K split.  The kQ quads of a
-// workgroup take consecutive parts of the split's K and meet in LDS, so that
-// few split sums go through memory.
-template <int kQ, int kP>
-__global__ __launch_bounds__(kMdQuad * kQ) __attribute__((amdgpu_waves_per_eu(4)))
+// Largest magnitude of eight activations and `mx`, as bits.
+template <int kP>
+__device__ __forceinline__ uint32_t md_max8(const StreamX8<kP>& x, uint32_t mx) {
+  float v[8];
+  stream_x_values<kP>(x, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+  return mx;
+}
+
+// Eight activations scaled for a row of this largest magnitude, as pieces.
+template <int kP, int kXP>
+__device__ __forceinline__ void md_put(uint4* lds, int unit, const StreamX8<kXP>& x, uint32_t amax) {
+  float v[8];
+  stream_x_values<kXP>(x, v);
+  const float scale = ldexpf(1.0f, stream_exp(__uint_as_float(amax)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
+  stream_put<kP>(lds, unit, v);
+}
+
+constexpr int kMdChoiceUnits = static_cast<int>((sizeof(MdChoice) + 15) / 16);
+
+// h of one expert and `cols` blocks of 64 columns.  Wave w takes matrix w & 1
+// (gate, up), one column block and one K part (gpp groups, a multiple of the
+// ring); the parts meet in LDS, then gate and up.
+//
+// Where all tokens' rows fit the window they are staged while the choice is
+// made, as A rows in token order, and the results of tokens that did not
+// choose the expert are dropped; else the expert's own rows are, afterwards.
+template <int kP, int kI>
+__global__ __launch_bounds__(kMdMaxThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void md_gate_up_kernel(const MdArgs a) {
-  constexpr int kRows = kP == 2 ? 8 : 16;
-  __shared__ StreamLds lds_all[kQ];
+  extern __shared__ uint4 lds[];
   __shared__ MdItems rt;
   __shared__ int token[kStreamRows];
-  const int split = blockIdx.x % a.S;
-  const int rest = blockIdx.x / a.S;
-  const int tile = rest % a.tiles;
-  int item = rest / a.tiles;
+  __shared__ uint32_t amax[kStreamRows];
+  const int tile = blockIdx.x % a.tiles;
+  int item = blockIdx.x / a.tiles;
+  const int tid = threadIdx.x, nt = blockDim.x;
   const int wv = wave_id(), lane = lane_id();
-  const int q = wv >> 2, wq = wv & 3;
   const int lc = lane & 15, kb = lane >> 4;
-  StreamLds& lds = lds_all[q];
+  const int G = a.H / kGroup, nch = G * 4;  // chunks of 8 values: k block c & 3 of group c >> 2
+  const int all_groups = a.parts * a.gpp;   // (with those past the last of K)
+  const int rshift_all = stream_rshift<kP>(a.M);
+  const bool whole = (all_groups * 4 << rshift_all) + kMdChoiceUnits <= a.units;
 
-  // the choice is made in what will be the first window
-  static_assert(sizeof(MdChoice) <= sizeof(lds_all[0].buf), "the choice must fit in a window");
-  MdChoice& ch = *reinterpret_cast<MdChoice*>(lds_all[0].buf);
-  md_route(a.logits, a.M, a.E, a.k, ch, rt);
+  // the choice is made behind the window, or in it
+  MdChoice& ch = *reinterpret_cast<MdChoice*>(lds + kStreamLds0 + (whole ? a.units - kMdChoiceUnits : 0));
+  if (tid < kStreamLds0) lds[tid] = make_uint4(0, 0, 0, 0);
+  if (tid < kStreamRows) amax[tid] = 0;
+  if (whole) __syncthreads();
+  auto row_max = [&](int m, int row) {
+    uint32_t mx = 0;
+    for (int c = tid; c < nch; c += nt)
+      mx = md_max8<kP>(stream_load_x<kP>(a.x, static_cast<size_t>(row) * a.H + 8 * c), mx);
+    mx = wave_max(mx);
+    if (lane == 0) atomicMax(&amax[m], mx);
+  };
+  if (whole)
+    for (int m = 0; m < a.M; ++m) row_max(m, m);
+  md_choose(a.logits, a.M, a.E, a.k, ch);
+  __syncthreads();
+  if (wv == 0) {
+    md_items(a.M, a.k, lane, ch, rt);
+  } else if (whole) {
+    for (int m = 0; m < a.M; ++m)
+      for (int c = tid - kWave; c < all_groups * 4; c += nt - kWave) {
+        const int unit = stream_unit(c >> 2, c & 3, m * kP, rshift_all);
+        if (c < nch)
+          md_put<kP, kP>(lds, unit, stream_load_x<kP>(a.x, static_cast<size_t>(m) * a.H + 8 * c), amax[m]);
+        else
+          stream_put_zero<kP>(lds, unit);
+      }
+  }
+  __syncthreads();
   if (blockIdx.x == 0) {  // for the second launch and the caller
-    for (int p = threadIdx.x; p < a.M * a.k; p += kMdQuad * kQ) {
+    for (int p = tid; p < a.M * a.k; p += nt) {
       if (a.out_ids != nullptr) a.out_ids[p] = ch.ids[p / a.k][p % a.k];
       if (a.out_w != nullptr) a.out_w[p] = ch.w[p / a.k][p % a.k];
     }
     static_assert(sizeof(MdItems) % 16 == 0, "copied in 16-byte units");
-    for (int i = threadIdx.x; i < static_cast<int>(sizeof(MdItems) / 16); i += kMdQuad * kQ)
+    for (int i = tid; i < static_cast<int>(sizeof(MdItems) / 16); i += nt)
       reinterpret_cast<uint4*>(a.items)[i] = reinterpret_cast<const uint4*>(&rt)[i];
   }
   const bool is_shared = a.xqg != nullptr && item == 0;
   if (a.xqg != nullptr) --item;
   if (item >= rt.n) return;
   const int expert = is_shared ? 0 : __builtin_amdgcn_readfirstlane(rt.experts[item]);
-
-  // the expert's rows, in token order
+  // the tokens it serves, and its A rows
   const uint32_t has = __builtin_amdgcn_readfirstlane(is_shared ? (1u << a.M) - 1u : rt.tokens[item]);
-  const int nrows = __popc(has);
+  const int nrows = whole ? a.M : __popc(has);
   const int pair0 = __builtin_amdgcn_readfirstlane(is_shared ? a.M * a.k : rt.first[item]);
-  if (wv == 0 && lane < kStreamRows && ((has >> lane) & 1)) token[__popc(has & ((1u << lane) - 1u))] = lane;
-  __syncthreads();
 
-  const int mat = wq >> 1;
-  const int c0 = tile * 128 + (wq & 1) * 64;
-  const bool wave_ok = c0 < a.I;
-  const int G = a.H / kGroup;
-  const size_t ebase = static_cast<size_t>(expert) * G * a.I;
+  // weights: wave-uniform bases, the ring from the part's first group on
+  const int mat = wv & 1, col = (wv >> 1) & (a.cols - 1);
+  const int part = (wv >> 1) / a.cols;
+  const int block = tile * a.cols + col;
+  const bool wave_ok = block * 64 < a.I;
+  const uint64_t ebase = static_cast<uint64_t>(expert) * G * a.I;
   const u32x4* qw = (is_shared ? (mat ? a.xqu : a.xqg) : (mat ? a.qu : a.qg)) + ebase;
   const float* sc = (is_shared ? (mat ? a.xsu : a.xsg) : (mat ? a.su : a.sg)) + (ebase >> a.gshift);
-  // a wave past the last column streams column block 0 and stores nothing
-  const StreamLane off = stream_lane(wave_ok ? c0 : 0, lane);
-  // (a quad past the last group streams the last one and adds zero)
-  const int part = split * kQ + q;
-  const int g_lo = min(G, part * a.gps), g_hi = min(G, g_lo + a.gps), g_last = max(g_hi - 1, 0);
+  // a wave past the last column streams column block 0 and stores nothing, a
+  // part past the last group the last one (against staged zeros)
+  const StreamLane off = stream_lane(wave_ok ? block * 64 : 0, lane);
+  const int g_last = G - 1;
+  int g = min(part * a.gpp, g_last);
+  auto next = [&](StreamCodes& c) {
+    stream_codes(uniform_at(qw, static_cast<uint64_t>(g) * a.I * 16),
+                 uniform_at(sc, static_cast<uint64_t>(g >> a.gshift) * a.I * 4), a.I, off, c);
+    g = min(g + 1, g_last);
+  };
   const uint32_t magic = magic_vgpr();
-  const bool arow = (kP == 2 ? (lc & 7) : lc) < nrows;
-  auto codes = [&](int g, StreamCodes& c) {
-    const size_t gg = static_cast<size_t>(min(g, g_last));
-    stream_codes(qw + gg * a.I, sc + (gg >> a.gshift) * a.I, a.I, off, c);
-  };
+  StreamCodes ring[kStreamRing];
+  if (!whole) {
+    __syncthreads();  // the choice's LDS is free
+    if (tid < kStreamRows && ((has >> tid) & 1)) token[__popc(has & ((1u << tid) - 1u))] = tid;
+    __syncthreads();
+    for (int m = 0; m < nrows; ++m) row_max(m, token[m]);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kStreamRing; ++j) next(ring[j]);
 
-  f32x4 tot[4];
+  float acc[4][kI];
 #pragma unroll
-  for (int cb = 0; cb < 4; ++cb) tot[cb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  StreamCodes ring[kMdRing];
-  float xv[16];
-  auto load = [&](int gw, int m) {
-    const int g = min(gw + (lane >> 1), g_last);
-    md_load_x<kP>(a.x, static_cast<size_t>(token[m]) * a.H + g * kGroup + 16 * (lane & 1), xv);
-  };
-  if (wq < nrows) load(g_lo, wq);
+  for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
-  for (int j = 0; j < kMdRing; ++j) codes(g_lo + j, ring[j]);
-  // every quad runs the same number of windows, so that all meet at the barriers
-  for (int w0 = 0; w0 < a.gps; w0 += kStreamWin) {
-    const int gw = g_lo + w0;
-    const int nw = max(0, min(kStreamWin, g_hi - gw));
-    if (w0 != 0) {
-      __syncthreads();  // the previous window is consumed
-      if (wq < nrows) load(gw, wq);
+    for (int i = 0; i < kI; ++i) acc[cb][i] = 0.0f;
+  const MdWindow win = whole ? MdWindow{rshift_all, a.gpp} : md_window<kP>(nrows, a.units, a.parts, a.gpp);
+  const StreamFrag frag = stream_frag<kP>(lane, nrows, part * win.wing, win.rshift);
+  for (int w0 = 0; w0 < a.gpp; w0 += win.wing) {
+    if (!whole) {
+      if (w0 != 0) __syncthreads();  // the previous window is consumed
+      // nt / parts threads (a power of two) stage a part
+      const int tpp = nt / a.parts, p = tid / tpp;
+      for (int m = 0; m < nrows; ++m)
+        for (int u = tid - p * tpp; u < win.wing * 4; u += tpp) {
+          const int gl = u >> 2, gg = p * a.gpp + w0 + gl;
+          const int unit = stream_unit(p * win.wing + gl, u & 3, m * kP, win.rshift);
+          if (w0 + gl < a.gpp && gg < G)
+            md_put<kP, kP>(lds, unit,
+                           stream_load_x<kP>(a.x, static_cast<size_t>(token[m]) * a.H + gg * kGroup + 8 * (u & 3)),
+                           amax[m]);
+          else
+            stream_put_zero<kP>(lds, unit);
+        }
+      __syncthreads();
     }
-    for (int m = wq; m < kRows; m += 4) {
-      if (m >= nrows) {
-        if (lane == 0) stream_no_row(lds, m);
-        continue;
-      }
-      if (m != wq) load(gw, m);
-      if ((lane >> 1) >= nw) {
+    const int n = min(win.wing, a.gpp - w0);
+    if (kI == 1 || nrows <= 4) {
+      float one[4][1];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xv[i] = 0.0f;
-      }
-      stream_store<kP>(lds, m, nw, lane, w0 == 0, true, xv);
-    }
-    __syncthreads();
-    if (w0 != 0) stream_rescale<kP>(lds, kb, tot);
-    for (int gl = 0; gl < nw; gl += kMdRing) {
+      for (int cb = 0; cb < 4; ++cb) one[cb][0] = acc[cb][0];
+      stream_run<kP, 1>(lds, frag, n, magic, ring, next, one);
 #pragma unroll
-      for (int j = 0; j < kMdRing; ++j) {
-        const bool on = gl + j < nw;
-        stream_mma(lds, on ? gl + j : gl, lc, kb, arow && on, magic, ring[j], tot);
-        codes(gw + gl + j + kMdRing, ring[j]);
-      }
+      for (int cb = 0; cb < 4; ++cb) acc[cb][0] = one[cb][0];
+    } else {
+      stream_run<kP, kI>(lds, frag, n, magic, ring, next, acc);
     }
   }
-  stream_finish<kP>(lds, kb, tot);
-  if (kQ > 1) {  // the quads' sums, in order
-    __syncthreads();  // the windows are free
-    f32x4* red = reinterpret_cast<f32x4*>(lds_all[q].buf);
-    if (q > 0) {
+
+  // the parts' sums, in order; then up's to gate's waves
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  const int pw = 2 * a.cols;  // waves of a part
+  __syncthreads();  // the window is free
+  if (part > 0) {
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) red[(wq * 4 + cb) * kWave + lane] = tot[cb];
-    }
-    __syncthreads();
-    if (q > 0) return;
+    for (int i = 0; i < kI; ++i)
+      red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+  }
+  __syncthreads();
+  if (part == 0) {
+    for (int p = 1; p < a.parts; ++p)
 #pragma unroll
-    for (int p = 1; p < kQ; ++p) {
-      const f32x4* r = reinterpret_cast<const f32x4*>(lds_all[p].buf);
+      for (int i = 0; i < kI; ++i) {
+        const f32x4 v = red[((p * pw + wv) * kI + i) * kWave + lane];
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) tot[cb] += r[(wq * 4 + cb) * kWave + lane];
+        for (int cb = 0; cb < 4; ++cb) acc[cb][i] += v[cb];
+      }
+    if (mat == 1) {  // (the first part's own places are free)
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+        red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
     }
   }
-  if (!wave_ok || (kP == 2 && lane >= 32)) return;
+  __syncthreads();
+  if (part != 0 || mat != 0 || !wave_ok) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * kb + i;
-    if (r < nrows) {
-      float* o = a.planes + ((static_cast<size_t>(split) * a.pairs + pair0 + r) * 2 + mat) * a.I + c0 + 4 * lc;
-      *reinterpret_cast<f32x4*>(o) = f32x4{tot[0][i], tot[1][i], tot[2][i], tot[3][i]};
+  for (int i = 0; i < kI; ++i) {
+    const int m = kb + 4 * i;
+    // (all 16 lanes of a row together)
+    if (m >= nrows || (whole && ((has >> m) & 1) == 0)) continue;
+    const int pair = pair0 + (whole ? __popc(has & ((1u << m) - 1u)) : m);
+    const float f = ldexpf(1.0f, -stream_exp(__uint_as_float(amax[m])));
+    const float wt = is_shared ? 1.0f : rt.w[pair];
+    const f32x4 u = red[((wv + 1) * kI + i) * kWave + lane];
+    f32x4 h;
+    float mx = 0.0f;
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb) {
+      h[cb] = silu(acc[cb][i] * f) * (u[cb] * f) * wt;
+      mx = fmaxf(mx, fabsf(h[cb]));
     }
+    *reinterpret_cast<f32x4*>(a.h + static_cast<size_t>(pair) * a.I + block * 64 + 4 * lc) = h;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    if (lc == 0) a.amax[static_cast<size_t>(pair) * (a.I / 64) + block] = mx;
   }
 }
 
-// 16 consecutive values of h = silu(gate) up of one pair, from the split sums:
-// all of the first sum's loads in flight, then four values at a time
-// (registers: the weights in flight need the rest).
-__device__ __forceinline__ void md_load_h(const MdArgs& a, int pair, int k, float w, float v[16]) {
-  const float* b = a.planes + static_cast<size_t>(pair) * 2 * a.I + k;
-  const size_t step = static_cast<size_t>(a.pairs) * 2 * a.I;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f32x4 g = *reinterpret_cast<const f32x4*>(b + 4 * i);
-    f32x4 u = *reinterpret_cast<const f32x4*>(b + a.I + 4 * i);
-#pragma unroll 1
-    for (int s = 1; s < a.S; ++s) {
-      g += *reinterpret_cast<const f32x4*>(b + s * step + 4 * i);
-      u += *reinterpret_cast<const f32x4*>(b + s * step + a.I + 4 * i);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[4 * i + j] = silu(g[j]) * u[j] * w;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-}
-
-// One tile of 256 output columns, one piece of the long axis.  Groups are
-// numbered through the experts: group f belongs to item f / G.  A window may
-// span experts, and the code ring runs on across them.
-template <int kP>
-__global__ __launch_bounds__(kMdQuad) __attribute__((amdgpu_waves_per_eu(4)))
+// One tile of 256 output columns, one piece of the long axis, its K parts over
+// quads of waves.  Groups are numbered through the experts: group f belongs to
+// item f / G.  A window may span experts, and the code ring runs on across
+// them.
+template <int kP, int kI>
+__global__ __launch_bounds__(kMdMaxThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void md_down_kernel(const MdArgs a) {
-  constexpr int kRows = kP == 2 ? 8 : 16;
-  __shared__ StreamLds lds;
+  extern __shared__ uint4 lds[];
   __shared__ MdItems rt;
+  __shared__ uint32_t amax[kStreamRows];
   __shared__ int last;
   const int split = blockIdx.x % a.dsplits;
   const int tile = blockIdx.x / a.dsplits;
+  const int tid = threadIdx.x, nt = blockDim.x;
   const int wv = wave_id(), lane = lane_id();
   const int lc = lane & 15, kb = lane >> 4;
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(MdItems) / 16); i += kMdQuad)
+  // the choice, and the largest magnitudes of h, 16 blocks of a pair a thread
+  // (those of pairs that are not there are dropped below)
+  const int nblk = a.I / 64, nseg = (nblk + 15) / 16;
+  const int nval = (a.M * a.k + (a.xqd != nullptr ? a.M : 0)) * nseg;
+  auto largest = [&](int q) {
+    const int p = q / nseg, b0 = (q - p * nseg) * 16;
+    const float* v = a.amax + static_cast<size_t>(p) * nblk;
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) mx = fmaxf(mx, v[min(b0 + j, nblk - 1)]);
+    return mx;
+  };
+  const float mine_max = tid < nval ? largest(tid) : 0.0f;
+  for (int i = tid; i < static_cast<int>(sizeof(MdItems) / 16); i += nt)
     reinterpret_cast<uint4*>(&rt)[i] = reinterpret_cast<const uint4*>(a.items)[i];
+  if (tid < kStreamLds0) lds[tid] = make_uint4(0, 0, 0, 0);
+  if (tid < kStreamRows) amax[tid] = 0;
   __syncthreads();
   const int G = a.I / kGroup;
   const int routed = __builtin_amdgcn_readfirstlane(rt.n);
@@ -436,166 +535,305 @@ void md_down_kernel(const MdArgs a) {
   const int per = max(1, (total + a.dsplits - 1) / a.dsplits);
   const int live = max(1, (total + per - 1) / per);  // pieces that hold anything
   if (split >= live) return;
-  const int f_lo = split * per, f_hi = min(total, f_lo + per);
-
-  const int c0 = tile * kStreamCols + wv * 64;
-  const bool wave_ok = c0 < a.H;
-  const StreamLane off = stream_lane(wave_ok ? c0 : 0, lane);
+  const int piece_lo = split * per, piece_hi = min(total, piece_lo + per);
+  const int gpp = (per + a.dparts * kStreamRing - 1) / (a.dparts * kStreamRing) * kStreamRing;
+  const int block = tile * (kMdCols / 64) + (wv & 3), part = wv >> 2;
+  const bool wave_ok = block * 64 < a.H;
+  const StreamLane off = stream_lane(wave_ok ? block * 64 : 0, lane);
   const uint32_t magic = magic_vgpr();
-  const bool arow = (kP == 2 ? (lc & 7) : lc) < a.M;
-  f32x4 tot[4];
-#pragma unroll
-  for (int cb = 0; cb < 4; ++cb) tot[cb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  if (f_hi > f_lo) {
-    // the ring's position: item and group.  It advances without a branch (one
-    // would cost the loop its registers): the next item's expert is read
-    // from LDS with every step.
-    int item = f_lo / G, g = f_lo % G, left = f_hi - f_lo;
-    int ex = rt.experts[min(item, max(routed - 1, 0))];
-    // (the shared expert's weights as distances from the stacks': a choice
-    // between pointers would become a branch)
-    const uint64_t estride = static_cast<uint64_t>(G) * a.H;  // slots of an expert; scales: estride >> dshift
-    const uint64_t xw = a.xqd == nullptr ? 0 : reinterpret_cast<uintptr_t>(a.xqd) - reinterpret_cast<uintptr_t>(a.qd);
-    const uint64_t xs = a.xqd == nullptr ? 0 : reinterpret_cast<uintptr_t>(a.xsd) - reinterpret_cast<uintptr_t>(a.sd);
-    auto next = [&](StreamCodes& c) {  // past the end: the last group again
-      const uint64_t e = estride * static_cast<unsigned>(__builtin_amdgcn_readfirstlane(ex));
-      const uint64_t ew = item >= routed ? xw : e * 16, es = item >= routed ? xs : (e >> a.dshift) * 4;
-      stream_codes(reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(a.qd) +
-                                                  uniform64(ew + static_cast<uint64_t>(g) * a.H * 16)),
-                   reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.sd) +
-                                                  uniform64(es + static_cast<uint64_t>(g >> a.dshift) * a.H * 4)),
-                   a.H, off, c);
-      const int go = left > 1 ? 1 : 0;
-      const int wrap = g + go == G ? 1 : 0;
-      left -= go;
-      g = wrap != 0 ? 0 : g + go;
-      item += wrap;
-      ex = rt.experts[min(item, max(routed - 1, 0))];
+  // The ring's position: item and group.  It advances without a branch (one
+  // would cost the loop its registers): the item's expert is read from LDS
+  // with every step, and the shared expert's weights are distances from the
+  // stacks' (a choice between pointers would become a branch).
+  int left = max(1, min(piece_hi - piece_lo - part * gpp, gpp));
+  int item, g;
+  {
+    const int f = max(0, min(piece_lo + part * gpp, total - 1));
+    item = __builtin_amdgcn_readfirstlane(f / G);
+    g = __builtin_amdgcn_readfirstlane(f % G);
+  }
+  const int item_max = max(routed - 1, 0);
+  int ex = rt.experts[min(item, item_max)];
+  const uint64_t estride = static_cast<uint64_t>(G) * a.H;  // slots of an expert; scales: estride >> dshift
+  const uint64_t xw = a.xqd == nullptr ? 0 : reinterpret_cast<uintptr_t>(a.xqd) - reinterpret_cast<uintptr_t>(a.qd);
+  const uint64_t xs = a.xqd == nullptr ? 0 : reinterpret_cast<uintptr_t>(a.xsd) - reinterpret_cast<uintptr_t>(a.sd);
+  auto next = [&](StreamCodes& c) {  // past the end: the last group again
+    const uint64_t e = estride * static_cast<unsigned>(__builtin_amdgcn_readfirstlane(ex));
+    const uint64_t ew = item >= routed ? xw : e * 16, es = item >= routed ? xs : (e >> a.dshift) * 4;
+    stream_codes(uniform_at(a.qd, ew + static_cast<uint64_t>(g) * a.H * 16),
+                 uniform_at(a.sd, es + static_cast<uint64_t>(g >> a.dshift) * a.H * 4), a.H, off, c);
+    const int go = left > 1 ? 1 : 0;
+    const int wrap = g + go == G ? 1 : 0;
+    left -= go;
+    g = wrap != 0 ? 0 : g + go;
+    item += wrap;
+    ex = rt.experts[min(item, item_max)];
+  };
+
+  float acc[4][kI];
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+    for (int i = 0; i < kI; ++i) acc[cb][i] = 0.0f;
+  StreamCodes ring[kStreamRing];
+  if (total > 0) {
+    // A quad's 256 threads stage its part: thread (chunk, row) takes every
+    // rstep-th row of its chunks.
+    MdWindow win = md_window<kP>(a.M, a.units, a.dparts, gpp);
+    if (win.wing < gpp) win = md_window<kP>(a.M, a.units / 2, a.dparts, gpp);  // two windows in turn
+    const int half = win.wing < gpp ? (a.dparts * win.wing * 4) << win.rshift : 0;  // units
+    const StreamFrag frag = stream_frag<kP>(lane, a.M, part * win.wing, win.rshift);
+    const int cshift = min(8, 32 - __builtin_clz(win.wing * 4 - 1));  // chunks of a pass: 2^cshift
+    const int chunk0 = tid & ((1 << cshift) - 1), row0 = (tid & 255) >> cshift, rstep = 256 >> cshift;
+    const float rcp_g = 1.0f / static_cast<float>(G);
+    struct Place {
+      int unit, item, k;
+      uint32_t who;
     };
-    // row m of the window at item w_item, group w_g: true if some group of it
-    // is the token's
-    int w_item = f_lo / G, w_g = f_lo % G;
-    float hv[16];
-    auto load = [&](int nw, int m) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) hv[i] = 0.0f;
-      bool mine = false;
-      if ((lane >> 1) < nw) {
-        int it = w_item, gg = w_g + (lane >> 1);
-        for (; gg >= G; gg -= G) ++it;
-        mine = it >= routed || ((rt.tokens[it] >> m) & 1);
-        if (mine) {
-          const int pair = it >= routed ? a.M * a.k + m : md_pair(rt, it, m);
-          md_load_h(a, pair, gg * kGroup + 16 * (lane & 1), it >= routed ? 1.0f : rt.w[pair], hv);
-        }
+    auto place = [&](int c, int w0) {
+      Place q;
+      const int gl = c >> 2, f = piece_lo + part * gpp + w0 + gl;
+      const bool in = gl < win.wing && w0 + gl < gpp && f < piece_hi;
+      // f / G: at most 513 items, so the float quotient is off by one at most
+      int it = static_cast<int>(static_cast<float>(f) * rcp_g), r = f - it * G;
+      if (r < 0) {
+        r += G;
+        --it;
+      } else if (r >= G) {
+        r -= G;
+        ++it;
       }
-      return __ballot(mine) != 0;
+      q.item = in ? it : 0;
+      q.unit = stream_unit(part * win.wing + gl, c & 3, 0, win.rshift);
+      q.k = r * kGroup + 8 * (c & 3);
+      q.who = !in ? 0u : (it >= routed ? (1u << a.M) - 1u : rt.tokens[it]);
+      return q;
     };
-    StreamCodes ring[kMdRing];
-#pragma unroll
-    for (int j = 0; j < kMdRing; ++j) next(ring[j]);
-    for (int fw = f_lo; fw < f_hi; fw += kStreamWin) {
-      const int nw = min(kStreamWin, f_hi - fw);
-      __syncthreads();  // the previous window is consumed
-      for (int m = wv; m < kRows; m += 4) {
-        if (m >= a.M) {
-          if (lane == 0) stream_no_row(lds, m);
-          continue;
+    auto load = [&](const Place& q, int m) {
+      const int pair = q.item >= routed ? a.M * a.k + m : md_pair(rt, q.item, m);
+      return stream_load_x<2>(a.h, static_cast<size_t>(pair) * a.I + q.k);
+    };
+    // A window's h is loaded while the window before the last one is used: up to
+    // two rows of the thread's place (more tokens seldom share an expert here;
+    // theirs are loaded late).
+    Place here;
+    int here_m[2] = {-1, -1};
+    StreamX8<2> here_h[2];
+    auto prefetch = [&](int w0) {
+      here = place(chunk0, w0);
+      here_m[0] = here_m[1] = -1;
+      for (int m = row0; m < a.M; m += rstep)
+        if ((here.who >> m) & 1) {
+          here_m[1] = here_m[0] >= 0 && here_m[1] < 0 ? m : here_m[1];
+          here_m[0] = here_m[0] < 0 ? m : here_m[0];
         }
-        const bool live_row = load(nw, m);
-        stream_store<kP>(lds, m, nw, lane, fw == f_lo, live_row, hv);
-      }
-      __syncthreads();
-      for (w_g += nw; w_g >= G; w_g -= G) ++w_item;
-      if (fw != f_lo) stream_rescale<kP>(lds, kb, tot);
-      for (int gl = 0; gl < nw; gl += kMdRing) {
 #pragma unroll
-        for (int j = 0; j < kMdRing; ++j) {
-          const bool on = gl + j < nw;
-          stream_mma(lds, on ? gl + j : gl, lc, kb, arow && on, magic, ring[j], tot);
-          next(ring[j]);
+      for (int j = 0; j < 2; ++j)
+        if (here_m[j] >= 0) here_h[j] = load(here, here_m[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto put = [&](int w0, uint4* buf) {
+      for (int c = chunk0; c < win.wing * 4; c += 1 << cshift) {
+        const bool ahead = c == chunk0;
+        const Place q = ahead ? here : place(c, w0);
+        for (int m = row0; m < a.M; m += rstep) {
+          if ((q.who >> m) & 1) {
+            StreamX8<2> h;
+            if (ahead && m == here_m[0])
+              h = here_h[0];
+            else if (ahead && m == here_m[1])
+              h = here_h[1];
+            else
+              h = load(q, m);
+            md_put<kP, 2>(buf, q.unit + m * kP, h, amax[m]);
+          } else {
+            stream_put_zero<kP>(buf, q.unit + m * kP);
+          }
         }
       }
+    };
+    prefetch(0);
+#pragma unroll
+    for (int j = 0; j < kStreamRing; ++j) next(ring[j]);
+    // every token's largest |w h| over its pairs
+    for (int q = tid; q < nval; q += nt) {
+      const int p = q / nseg;
+      if (p < rt.pairs || p >= a.M * a.k)
+        atomicMax(&amax[p < a.M * a.k ? rt.token[p] : p - a.M * a.k],
+                  __float_as_uint(q == tid ? mine_max : largest(q)));
     }
-    stream_finish<kP>(lds, kb, tot);
+    __syncthreads();  // the largest magnitudes are known
+    put(0, lds);
+    if (win.wing < gpp) prefetch(win.wing);
+    __syncthreads();
+    int odd = 0;
+    for (int w0 = 0; w0 < gpp; w0 += win.wing) {
+      const int w1 = w0 + win.wing;
+      if (w1 < gpp) put(w1, lds + (odd ? 0 : half));
+      if (w1 + win.wing < gpp) prefetch(w1 + win.wing);
+      // (absent A rows read the zeros in front of the first window)
+      StreamFrag f = frag;
+      if (odd && f.step != 0) f.at += half;
+      stream_run<kP, kI>(lds, f, min(win.wing, gpp - w0), magic, ring, next, acc);
+      __syncthreads();  // this window is consumed, the next one staged
+      odd ^= 1;
+    }
+  }
+
+  // the parts' sums, in order
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  if (a.dparts > 1) {
+    if (part > 0) {
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+        red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+    }
+    __syncthreads();
+    if (part == 0) {
+      for (int p = 1; p < a.dparts; ++p)
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+          const f32x4 v = red[((p * 4 + wv) * kI + i) * kWave + lane];
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb) acc[cb][i] += v[cb];
+        }
+    }
   }
 
   // The pieces of a tile meet as in the split-K GEMV: agent-scope stores reach
   // the device's coherence point, the counter says who came last, and that
   // workgroup's agent-scope loads read the pieces back, summed in order.
-  float* base = a.partials + static_cast<size_t>(tile) * a.dsplits * a.M * kStreamCols;
-  const size_t ps = static_cast<size_t>(a.M) * kStreamCols;
-  if (kP == 1 || lane < 32) {
+  float* base = a.partials + static_cast<size_t>(tile) * a.dsplits * a.M * kMdCols;
+  const size_t ps = static_cast<size_t>(a.M) * kMdCols;
+  if (part == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * kb + i;
-      if (r < a.M)
+    for (int i = 0; i < kI; ++i) {
+      const int m = kb + 4 * i;
+      if (m < a.M) {
+        const float f = ldexpf(1.0f, -stream_exp(__uint_as_float(amax[m])));
+        uint64_t* o = reinterpret_cast<uint64_t*>(base + split * ps + m * kMdCols + wv * 64 + 4 * lc);
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb)
-          __hip_atomic_store(base + split * ps + r * kStreamCols + wv * 64 + 4 * lc + cb, tot[cb][i],
-                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t v = static_cast<uint64_t>(__float_as_uint(acc[2 * j + 1][i] * f)) << 32 |
+                             __float_as_uint(acc[2 * j][i] * f);
+          __hip_atomic_store(o + j, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // this wave's stores are complete
   __syncthreads();
-  if (threadIdx.x == 0)
+  if (tid == 0)
     last = __hip_atomic_fetch_add(&a.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == live - 1;
   __syncthreads();
   if (!last) return;
-  if (threadIdx.x == 0) __hip_atomic_store(&a.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int n = tile * kStreamCols + static_cast<int>(threadIdx.x);
+  if (tid == 0) __hip_atomic_store(&a.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // two columns a thread, kRows rows' pieces in flight together
+  constexpr int kRows = kI == 1 ? 1 : 2, kB = 12, kPer = kMdCols / 2;
+  const int c = 2 * (tid % kPer), n = tile * kMdCols + c, rs = nt / kPer;
   if (n >= a.H) return;
-  for (int r = 0; r < a.M; ++r) {
-    constexpr int kB = 16;
-    float v = 0.0f;
+  for (int r0 = tid / kPer; r0 < a.M; r0 += rs * kRows) {
+    float v[kRows][2];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) v[r][0] = v[r][1] = 0.0f;
     for (int s0 = 0; s0 < live; s0 += kB) {
-      float q[kB];
+      uint64_t q[kRows][kB];
 #pragma unroll
-      for (int j = 0; j < kB; ++j)
-        q[j] = __hip_atomic_load(base + min(s0 + j, live - 1) * ps + r * kStreamCols + threadIdx.x, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
+      for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int j = 0; j < kB; ++j)
-        if (s0 + j < live) v += q[j];
+        for (int j = 0; j < kB; ++j)
+          q[r][j] = __hip_atomic_load(
+              reinterpret_cast<const uint64_t*>(base + min(s0 + j, live - 1) * ps + min(r0 + r * rs, a.M - 1) * kMdCols + c),
+              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+          if (s0 + j < live) {
+            v[r][0] += __uint_as_float(static_cast<uint32_t>(q[r][j]));
+            v[r][1] += __uint_as_float(static_cast<uint32_t>(q[r][j] >> 32));
+          }
     }
-    const size_t at = static_cast<size_t>(r) * a.H + n;
-    if (a.y_bf16)
-      static_cast<uint16_t*>(a.y)[at] = f32_to_bf16(v);
-    else
-      static_cast<float*>(a.y)[at] = v;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (r0 + r * rs >= a.M) continue;
+      const size_t at = static_cast<size_t>(r0 + r * rs) * a.H + n;
+      if (a.y_bf16)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) =
+            f32_to_bf16(v[r][0]) | static_cast<uint32_t>(f32_to_bf16(v[r][1])) << 16;
+      else
+        *reinterpret_cast<float2*>(static_cast<float*>(a.y) + at) = make_float2(v[r][0], v[r][1]);
+    }
   }
 }
 
 struct MdPlan {
-  int tiles = 0, quads = 1, S = 1, gps = 1, dtiles = 0, dsplits = 1, items = 0, pairs = 0;
-  size_t items_off = 0, planes_off = 0, partials_off = 0, bytes = 0;
+  int items = 0;
+  int waves = 4, cols = 2, tiles = 0, parts = 1, gpp = 1;  // gate/up
+  int dwaves = 4, dtiles = 0, dsplits = 1;                 // down
+  size_t items_off = 0, h_off = 0, amax_off = 0, partials_off = 0, bytes = 0;
 };
 
 MdPlan plan_md(int M, int k, const w4a16_weight_t* gate, bool shared) {
   MdPlan p;
   const int H = gate->K, I = gate->N, G = H / kGroup;
   p.items = std::min(M * k, gate->num_experts) + (shared ? 1 : 0);
-  p.pairs = M * k + (shared ? M : 0);
-  p.tiles = (I + 127) / 128;
-  // parts of gate and up's K until one round of quads fills the chip, each
-  // of at least 8 groups; up to four parts are the quads of one workgroup
-  const int parts = std::max(1, std::min(kMdTarget / std::max(1, p.items * p.tiles), G / 8));
-  p.quads = parts >= 4 ? 4 : (parts >= 2 ? 2 : 1);
-  p.S = std::min(parts / p.quads, 8);
-  p.gps = std::max(1, (G + p.S * p.quads - 1) / (p.S * p.quads));
-  p.S = std::max(1, (G + p.gps * p.quads - 1) / (p.gps * p.quads));  // no empty split
-  p.dtiles = (H + kStreamCols - 1) / kStreamCols;
+  // Gate and up: workgroups of 4 waves, and of 8 or 16 (more K parts), at last
+  // of half the columns, while the launch would leave waves of the chip unused
+  // and a part keeps a ring of groups.
+  auto wgs = [&](int cols) { return static_cast<size_t>(p.items) * ((I / 64 + cols - 1) / cols); };
+  while (p.waves < 16 && wgs(p.cols) * p.waves < 16 * kMdCus && G / (p.waves / p.cols) >= kStreamRing) p.waves *= 2;
+  if (p.waves == 16 && wgs(2) < kMdCus && G / 8 >= kStreamRing) p.cols = 1;
+  p.tiles = (I / 64 + p.cols - 1) / p.cols;
+  p.parts = p.waves / (2 * p.cols);
+  p.gpp = (G + p.parts * kStreamRing - 1) / (p.parts * kStreamRing) * kStreamRing;
+  // Down: workgroups of 16 waves, one per CU, while each of the four parts has
+  // a ring of groups or more.
+  p.dtiles = (H + kMdCols - 1) / kMdCols;
   const int total = p.items * (I / kGroup);
-  p.dsplits = std::max(1, std::min({kMdTarget / std::max(1, p.dtiles), total / 8, kMdMaxSplits}));
+  p.dwaves = total >= 16 ? 16 : 4;
+  const int parts = p.dwaves / 4;
+  p.dsplits = std::max(1, std::min({kMdCus / p.dtiles, total / (4 * parts), kMdMaxSplits}));
+  const size_t pairs = static_cast<size_t>(M) * k + (shared ? M : 0);
   Carve c;
   size_t counters;
   c.take(counters, kCounterBytes);
   c.take(p.items_off, sizeof(MdItems));
-  c.take(p.planes_off, static_cast<size_t>(p.S) * p.pairs * 2 * I * 4);
-  c.take(p.partials_off, static_cast<size_t>(p.dtiles) * p.dsplits * M * kStreamCols * 4);
+  c.take(p.h_off, pairs * I * 4);
+  c.take(p.amax_off, pairs * (I / 64) * 4);
+  c.take(p.partials_off, static_cast<size_t>(p.dtiles) * p.dsplits * M * kMdCols * 4);
   p.bytes = c.cursor;
   return p;
+}
+
+// LDS of a workgroup: the window, which also holds the choice before and the
+// parts' sums (1 KiB a wave and accumulator) after.
+size_t md_lds_bytes(int waves) { return (static_cast<size_t>(waves) * kMdUnits + kStreamLds0) * 16; }
+
+template <int kP>
+w4a16_status_t launch_md(const MdPlan& p, MdArgs a, hipStream_t stream) {
+  static_assert(kMdChoiceUnits <= 4 * kMdUnits && 4 * kWave <= kMdUnits, "the choice and the sums must fit");
+  const size_t blocks = static_cast<size_t>(p.items) * p.tiles;
+  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+  const dim3 g1(static_cast<unsigned>(blocks)), t1(p.waves * kWave);
+  a.units = p.waves * kMdUnits;
+  const size_t l1 = md_lds_bytes(p.waves), l2 = md_lds_bytes(p.dwaves);
+  if (a.M <= 4)
+    md_gate_up_kernel<kP, 1><<<g1, t1, l1, stream>>>(a);
+  else
+    md_gate_up_kernel<kP, 4 / kP><<<g1, t1, l1, stream>>>(a);
+  const w4a16_status_t st = launch_status();
+  if (st != W4A16_OK) return st;
+  const dim3 g2(static_cast<unsigned>(p.dtiles * p.dsplits)), t2(p.dwaves * kWave);
+  a.units = p.dwaves * kMdUnits;
+  if (a.M <= 4)
+    md_down_kernel<kP, 1><<<g2, t2, l2, stream>>>(a);
+  else if (a.M <= 8)
+    md_down_kernel<kP, 2><<<g2, t2, l2, stream>>>(a);
+  else
+    md_down_kernel<kP, 4 / kP><<<g2, t2, l2, stream>>>(a);
+  return launch_status();
 }
 
 w4a16_status_t check_md_stack(const w4a16_weight_t* gate, const w4a16_weight_t* up, const w4a16_weight_t* down) {
@@ -629,7 +867,7 @@ w4a16_status_t check_md(int M, int k, w4a16_dtype_t xt, const w4a16_weight_t* ga
   // 32-bit group counts and row sizes, and one counter per column tile
   if (gate->K >= 1 << 26 || gate->N >= 1 << 26) return W4A16_ERR_UNSUPPORTED;
   if (static_cast<size_t>(gate->N / kGroup) * (E + 1) >= (size_t{1} << 31)) return W4A16_ERR_UNSUPPORTED;
-  if (static_cast<size_t>((gate->K + kStreamCols - 1) / kStreamCols) * sizeof(int) > kCounterBytes)
+  if (static_cast<size_t>((gate->K + kMdCols - 1) / kMdCols) * sizeof(int) > kCounterBytes)
     return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
@@ -695,13 +933,15 @@ extern "C" w4a16_status_t w4a16_moe_decode(const void* x, w4a16_dtype_t xt, int3
   }
   a.gshift = group_shift(gate);
   a.dshift = group_shift(down);
+  a.cols = p.cols;
   a.tiles = p.tiles;
-  a.S = p.S;
-  a.gps = p.gps;
+  a.parts = p.parts;
+  a.gpp = p.gpp;
+  a.dparts = p.dwaves / 4;
   a.dtiles = p.dtiles;
   a.dsplits = p.dsplits;
-  a.pairs = p.pairs;
-  a.planes = reinterpret_cast<float*>(b + p.planes_off);
+  a.h = reinterpret_cast<float*>(b + p.h_off);
+  a.amax = reinterpret_cast<float*>(b + p.amax_off);
   a.partials = reinterpret_cast<float*>(b + p.partials_off);
   a.counters = reinterpret_cast<int*>(b);
   a.items = reinterpret_cast<MdItems*>(b + p.items_off);
@@ -709,29 +949,5 @@ extern "C" w4a16_status_t w4a16_moe_decode(const void* x, w4a16_dtype_t xt, int3
   a.out_w = topk_w;
   a.y = y;
   a.y_bf16 = yt == W4A16_BF16;
-  const size_t blocks = static_cast<size_t>(p.items) * p.tiles * p.S;
-  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
-  const dim3 g1(static_cast<unsigned>(blocks)), t1(kMdQuad * p.quads);
-  if (xt == W4A16_BF16) {
-    if (p.quads == 4)
-      md_gate_up_kernel<4, 1><<<g1, t1, 0, stream>>>(a);
-    else if (p.quads == 2)
-      md_gate_up_kernel<2, 1><<<g1, t1, 0, stream>>>(a);
-    else
-      md_gate_up_kernel<1, 1><<<g1, t1, 0, stream>>>(a);
-  } else {
-    if (p.quads == 4)
-      md_gate_up_kernel<4, 2><<<g1, t1, 0, stream>>>(a);
-    else if (p.quads == 2)
-      md_gate_up_kernel<2, 2><<<g1, t1, 0, stream>>>(a);
-    else
-      md_gate_up_kernel<1, 2><<<g1, t1, 0, stream>>>(a);
-  }
-  if ((st = launch_status()) != W4A16_OK) return st;
-  const dim3 g2(static_cast<unsigned>(p.dtiles * p.dsplits)), t2(kMdQuad);
-  if (xt == W4A16_BF16)
-    md_down_kernel<1><<<g2, t2, 0, stream>>>(a);
-  else
-    md_down_kernel<2><<<g2, t2, 0, stream>>>(a);
-  return launch_status();
+  return xt == W4A16_BF16 ? launch_md<1>(p, a, stream) : launch_md<2>(p, a, stream);
 }

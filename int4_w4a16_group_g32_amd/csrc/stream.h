@@ -6,88 +6,97 @@
 // four adjacent columns, one per MFMA block) and their four scales per block,
 // and the block's result is scaled by s[g][n] on float32 accumulators.
 //
-// Rows are staged in LDS one window of 32 groups at a time as f16 pieces of
-// x * 2^e, with a running power of two per row: e is the smallest that keeps
-// every value so far under 2^15, and the accumulators follow it by exact
-// powers of two.  Two pieces (8 rows, float32 x): A row m holds piece 0 of
-// row m, A row 8 + m piece 1, 22 significant bits in all.  One piece (16 rows,
-// bf16 x): exact for bf16 values.
+// Rows are staged in LDS as f16 pieces of x * 2^e, with one power of two per
+// row that puts its largest magnitude in [2^14, 2^15): two pieces for float32
+// values (22 significant bits), one for bf16 ones (exact).  Row m of x is A
+// row 4 (m & 3) + (m >> 2), or with two pieces 4 (m & 3) + 2 (m >> 2) + piece,
+// so that element i of a lane's result (A row 4 (lane >> 4) + i) belongs to
+// row (lane >> 4) + 4 i: up to four rows need one accumulator per column and
+// lane, not four.  LDS holds the rows there are and no others (few rows leave
+// room for long windows); lanes of absent A rows read a unit of zeros.
 #pragma once
+
+#include <type_traits>
 
 #include "common.h"
 #include "mfma_ops.h"
 
 namespace w4 {
 
-constexpr int kStreamWin = 32;    // groups per staged window
-constexpr int kStreamRows = 16;   // A rows
-constexpr int kStreamCols = 256;  // columns of one quad of four waves
-constexpr int kStreamNoExp = 1 << 20;
+constexpr int kStreamRows = 16;  // A rows
+constexpr int kStreamRing = 4;   // groups of codes in flight per wave
+constexpr int kStreamLds0 = 4;   // first unit of the window (unit 0 is zeros)
 
-struct StreamLds {
-  uint4 buf[kStreamWin * kStreamRows * 4];  // A fragments, unit (group, row, k block) at stream_unit
-  float f[kStreamRows];                     // per row: the accumulators' rescale before this window
-  int e[kStreamRows];                       // per row: the running exponent
-};
-
-// A fragment read (16 rows of one group and k block) and a staging store (16
-// lanes: one row, eight groups, two k blocks) each cover all bank groups.
-__device__ __forceinline__ int stream_unit(int g, int r, int kb) {
-  return (g * 16 + ((r & ~3) | ((r & 3) ^ (g & 3)))) * 4 + (kb ^ ((r >> 2) & 3) ^ ((g >> 2) & 1));
+// Unit of (group, k block, LDS row); 2^rshift LDS rows a group: row m's piece
+// p is LDS row m * kP + p.
+__device__ __forceinline__ int stream_unit(int g, int kb, int r, int rshift) {
+  return kStreamLds0 + (((g * 4 + kb) << rshift) + r);
 }
 
-// Stores the 16 values at half `lane & 1` of group `lane >> 1` of one row of a
-// window as pieces and moves the row's running exponent; one wave a row.
-// `live`: some lane of the row holds a value (wave-uniform); a row without any
-// is stored as zeros.
+// log2 of the LDS rows that hold n rows of kP pieces.
 template <int kP>
-__device__ __forceinline__ void stream_store(StreamLds& lds, int m, int nw, int lane, bool first, bool live,
-                                             const float v[16]) {
-  const int gl = lane >> 1, hb = lane & 1;
-  const int e_old = first ? kStreamNoExp : lds.e[m];  // (all lanes read before lane 0 writes)
-  int e = e_old;
-  float scale = 0.0f;
-  if (live) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    if (amax > 0.0f) {
-      int lg = ilogbf(amax);
-      lg = lg > 120 ? 120 : (lg < -112 ? -112 : lg);  // 2^e stays a normal float
-      e = min(e_old, 14 - lg);
-    }
-    scale = e < kStreamNoExp ? ldexpf(1.0f, e) : 0.0f;
-  }
-  if (lane == 0) {
-    lds.f[m] = e_old < kStreamNoExp ? ldexpf(1.0f, e - e_old) : 1.0f;
-    lds.e[m] = e;
-  }
-  if (gl < nw) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      half8 p0 = half8{}, p1 = half8{};
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t = v[8 * b + kCodeOrder[i]] * scale;
-          const _Float16 h0 = static_cast<_Float16>(t);
-          p0[i] = h0;
-          if (kP == 2) p1[i] = static_cast<_Float16>(t - static_cast<float>(h0));
-        }
-      }
-      const int kb = 2 * hb + b;
-      *reinterpret_cast<half8*>(&lds.buf[stream_unit(gl, m, kb)]) = p0;
-      if (kP == 2) *reinterpret_cast<half8*>(&lds.buf[stream_unit(gl, 8 + m, kb)]) = p1;
-    }
-  }
+__device__ __forceinline__ int stream_rshift(int n) {
+  return (n > 1 ? 32 - __builtin_clz(n - 1) : 0) + (kP - 1);
 }
 
-// A row that no window holds: its accumulators are dropped.
-__device__ __forceinline__ void stream_no_row(StreamLds& lds, int m) {
-  lds.f[m] = 0.0f;
-  lds.e[m] = kStreamNoExp;
+// Where a lane finds its A fragment: unit `at` of group 0, `step` units a group.
+struct StreamFrag {
+  int at, step;
+};
+template <int kP>
+__device__ __forceinline__ StreamFrag stream_frag(int lane, int nrows, int g0, int rshift) {
+  const int lc = lane & 15, kb = lane >> 4;
+  const int m = kP == 2 ? (lc >> 2) + 4 * ((lc >> 1) & 1) : (lc >> 2) + 4 * (lc & 3);
+  const int p = kP == 2 ? lc & 1 : 0;
+  if (m >= nrows) return StreamFrag{0, 0};
+  return StreamFrag{stream_unit(g0, kb, m * kP + p, rshift), 4 << rshift};
+}
+
+// The exponent that brings a row's largest magnitude into [2^14, 2^15) (any
+// will do for a row of zeros; infinities and NaNs pass through as such), kept
+// to where 2^e and 2^-e are normal floats.
+__device__ __forceinline__ int stream_exp(float amax) {
+  const int e = 15 - __builtin_amdgcn_frexp_expf(amax);
+  return e > 126 ? 126 : e;
+}
+
+// Largest value of the wave, as a scalar: row shifts within 16 lanes, then
+// broadcasts across rows; lane 63 ends with all of them.  (Non-negative
+// floats compare as their bits.)
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto step = [&](auto ctrl, auto rows) {
+    const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(v), decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+    v = v > t ? v : t;
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// Eight values (already scaled) as pieces: units u and, of two pieces, u + 1.
+template <int kP>
+__device__ __forceinline__ void stream_put(uint4* lds, int u, const float v[8]) {
+  half8 p0, p1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = v[kCodeOrder[i]];
+    const _Float16 h = static_cast<_Float16>(t);
+    p0[i] = h;
+    if (kP == 2) p1[i] = static_cast<_Float16>(t - static_cast<float>(h));
+  }
+  *reinterpret_cast<half8*>(lds + u) = p0;
+  if (kP == 2) *reinterpret_cast<half8*>(lds + u + 1) = p1;
+}
+template <int kP>
+__device__ __forceinline__ void stream_put_zero(uint4* lds, int u) {
+  lds[u] = make_uint4(0, 0, 0, 0);
+  if (kP == 2) lds[u + 1] = make_uint4(0, 0, 0, 0);
 }
 
 struct StreamCodes {
@@ -125,45 +134,76 @@ __device__ __forceinline__ void stream_codes(const u32x4* wrow, const float* sro
   __builtin_amdgcn_sched_barrier(0);
 }
 
-__device__ __forceinline__ void stream_mma(const StreamLds& lds, int gl, int lc, int kb, bool on, uint32_t magic,
-                                           const StreamCodes& c, f32x4 acc[4]) {
-  half8 af = *reinterpret_cast<const half8*>(&lds.buf[stream_unit(gl, lc, kb)]);
-  if (!on) af = half8{};
+// n groups (a multiple of the ring; groups past the end are staged as zeros)
+// from LDS group 0 of `frag`; next(codes) loads the ring's next group.
+// acc[cb][i] is row (lane >> 4) + 4 i, column 4 (lane & 15) + cb.  Every wave of
+// the workgroup runs the same n: a bare barrier a round (no fence, so no wait
+// on the ring) keeps the waves in step, which otherwise finish one after
+// another, oldest first, with ever fewer loads in flight (down projections of
+// four tokens: 59 -> 54.5 us).
+template <int kP, int kI, class Next>
+__device__ __forceinline__ void stream_run(const uint4* lds, StreamFrag frag, int n, uint32_t magic,
+                                           StreamCodes ring[kStreamRing], Next&& next, float acc[4][kI]) {
+  for (int g = 0; g < n; g += kStreamRing) {
 #pragma unroll
-  for (int cb = 0; cb < 4; ++cb) {
-    const half8 bq = codes_f16(c.w[cb], magic);
-    const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bq, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+    for (int j = 0; j < kStreamRing; ++j) {
+      const half8 af = *reinterpret_cast<const half8*>(lds + frag.at);
+      frag.at += frag.step;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[cb][i] = fmaf(c.s[cb], d[i], acc[cb][i]);
+      for (int cb = 0; cb < 4; ++cb) {
+        const half8 bq = codes_f16(ring[j].w[cb], magic);
+        const f32x4 d =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(af, bq, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kI; ++i)
+          acc[cb][i] = fmaf(ring[j].s[cb], kP == 2 ? d[2 * i] + d[2 * i + 1] : d[i], acc[cb][i]);
+      }
+      next(ring[j]);
+    }
+    __builtin_amdgcn_s_barrier();
   }
 }
 
-// Brings the accumulators to the window's powers of two.
-template <int kP>
-__device__ __forceinline__ void stream_rescale(const StreamLds& lds, int kb, f32x4 tot[4]) {
-  const int r0 = kP == 2 ? 4 * (kb & 1) : 4 * kb;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float f = lds.f[r0 + i];
-#pragma unroll
-    for (int cb = 0; cb < 4; ++cb) tot[cb][i] *= f;
-  }
+// A wave-uniform value in scalar registers.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+template <class T>
+__device__ __forceinline__ const T* uniform_at(const T* base, uint64_t bytes) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + uniform64(bytes));
 }
 
-// Back from the running powers of two (rows without a nonzero value give 0),
-// pieces joined: element i of block cb is row 4 (kb & 1) + i (two pieces, the
-// same in both halves of the wave) or 4 kb + i (one), column 4 lc + cb.
+// Eight consecutive activations from element `at`.
 template <int kP>
-__device__ __forceinline__ void stream_finish(const StreamLds& lds, int kb, f32x4 tot[4]) {
-  const int r0 = kP == 2 ? 4 * (kb & 1) : 4 * kb;
+struct StreamX8 {
+  uint4 v[kP];
+};
+template <int kP>
+__device__ __forceinline__ StreamX8<kP> stream_load_x(const void* x, size_t at) {
+  StreamX8<kP> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (kP == 2 ? 4 : 2));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = lds.e[r0 + i];
-    const float f = e < kStreamNoExp ? ldexpf(1.0f, -e) : 0.0f;
+  for (int i = 0; i < kP; ++i) r.v[i] = p[i];
+  return r;
+}
+template <int kP>
+__device__ __forceinline__ void stream_x_values(const StreamX8<kP>& r, float v[8]) {
+  if (kP == 1) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
-    for (int cb = 0; cb < 4; ++cb) {
-      tot[cb][i] *= f;
-      if (kP == 2) tot[cb][i] += __shfl_xor(tot[cb][i], 32);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      v[4 * i] = __uint_as_float(r.v[i].x);
+      v[4 * i + 1] = __uint_as_float(r.v[i].y);
+      v[4 * i + 2] = __uint_as_float(r.v[i].z);
+      v[4 * i + 3] = __uint_as_float(r.v[i].w);
     }
   }
 }
