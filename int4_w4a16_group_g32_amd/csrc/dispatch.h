@@ -25,6 +25,13 @@ struct MfmaPlan {
 // allow_wide: the caller launches wide tiles when the plan says so
 MfmaPlan plan_mfma(int rows, int N, int mode, int K, w4a16_dtype_t xt, bool allow_wide);
 
+size_t mfma_partial_bytes(const MfmaPlan& m);
+MfmaArgs mfma_dense_args(const MfmaPlan& m, int rows, const w4a16_weight_t* w0, const w4a16_weight_t* w1, int mode,
+                         const _Float16* ap, const float* rs, char* ws, size_t partials_off, size_t counters_off);
+// Split sums to planes in the partials region, reduced by the next kernel
+// (dense tile launches with S > 1).
+void defer_split_k(MfmaArgs& a, const MfmaPlan& m);
+
 struct GemmPlan {
   int S = 1, gps = 1;
   int tiles = 0;

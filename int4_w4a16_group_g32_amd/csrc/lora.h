@@ -3,13 +3,13 @@
 #pragma once
 
 #include "common.h"
+#include "gemv.h"
 
 namespace w4 {
 
 constexpr int kLoraMaxRank = 256;
-constexpr int kLoraChunk = 64;    // adapter ranks handled together
-constexpr int kLoraRows = 16;     // rows of one MFMA block
-constexpr int kLoraMaxSplits = 16;  // K splits of the first product
+constexpr int kLoraChunk = 64;  // adapter ranks handled together by the block kernels
+constexpr int kLoraRows = 16;   // rows of one MFMA block
 
 // One projection's adapters as the kernels read them.
 struct LoraSet {
@@ -17,7 +17,7 @@ struct LoraSet {
   const uint16_t* b;   // bf16 [n][N][R]
   const float* scale;  // [n]
   const int* ranks;    // [n], or null: R for every adapter
-  float* t;            // split sums of x A^T: [splits][M][R], float32
+  float* t;            // scale * x A^T, split sums: [splits][M][R], float32
   int R, n;
 };
 
@@ -34,33 +34,67 @@ inline LoraSet lora_set(const w4a16_lora_t* l, float* t) {
   return s;
 }
 
-// Launch shape of the first product: 16-row blocks per workgroup, K splits,
-// and adapter slots (workgroups that share the distinct adapters of a row
-// block between them).
+// Launch shape of the first product: by rows (one dot product of one row per
+// workgroup and rank) or by blocks of 64 rows, in K splits.
 struct ShrinkShape {
-  int rb = 1, splits = 1, slots = 1;
+  bool rows = true;
+  int splits = 1;
 };
-ShrinkShape shrink_shape(int M, int K, int R, int n, int sets);
+ShrinkShape shrink_shape(int M, int K, int R);
 
-// t[split][m][r] = sum over the split's k of x[m][k] * a[id][r][k] for the
-// rows m with an adapter id = ids[m] in [0, n) and r < R (the other entries
-// are left as they were).  Up to two projections of the same x.
+// t[split][m][r] = scale[id] * sum over the split's k of x[m][k] * a[id][r][k]
+// for the rows m with an adapter id = ids[m] in [0, n) and the ranks r it uses
+// (the other entries are left as they were).  Up to two projections of the
+// same x.
 w4a16_status_t launch_lora_shrink(const void* x, w4a16_dtype_t xt, int M, int K, const int* ids, const LoraSet* sets,
                                   int n_sets, const ShrinkShape& sh, hipStream_t stream);
 
-// out[m][n] = base[m][n] + scale * (t[m] . b[id][n]); with two sets (gate,
-// up), h[m][n] = silu(gate) * up of two such sums.  base is float32 [M][N];
-// out float32 or bf16 (round to nearest even).
+// The base product's sums as a tile launch left them: rs[m] * the sum of S
+// planes (plane_rows x ld), in split order.
+struct LoraBase {
+  const float* p;
+  int S, plane_rows, ld;
+  size_t split_stride;  // floats from one split's plane to the next
+  const float* rs;      // row factors, or null: 1
+};
+
+// out[m][n] = base[m][n] + t[m] . b[id][n]; with two bases (gate, up), h[m][n]
+// = silu(gate) * up of two such sums.  out float32 or bf16 (round to nearest
+// even).
 struct LoraFinishArgs {
-  const float* base0;
-  const float* base1;  // up (SwiGLU), else null
+  LoraBase base0, base1;  // base1.p: up (SwiGLU), else null
   LoraSet s0, s1;
   const int* ids;
-  int splits;  // K splits of t
+  int rows, splits;  // the shape of t
   int M, N;
   void* out;
   int out_bf16;
 };
 w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream);
+
+// The base product of a few rows (up to 8 in two pieces, 16 in one) with the
+// adapters' second product in its epilogue, one launch.
+struct LoraStreamPlan {
+  bool ok = false;
+  int waves = 16, cols = 1, parts = 1, splits = 1, gpp = 4, tiles = 1;
+  size_t partial_bytes = 0;
+};
+LoraStreamPlan plan_lora_stream(int M, int pieces, int N, int mats, int K);
+struct LoraStreamArgs {
+  const void* x;
+  int x_f32, pieces;  // activations float32 or bf16, as 2 or 1 pieces
+  int M, K, N;
+  const u32x4 *qw0, *qw1;  // qw1: up (SwiGLU), else null
+  const float *sc0, *sc1;
+  int gshift;
+  LoraSet s0, s1;
+  const int* ids;
+  int cols, parts, splits, gpp, tiles;  // the plan
+  float* partials;
+  int* counters;
+  void* out;
+  int out_bf16;
+};
+w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hipStream_t stream);
 
 }  // namespace w4

@@ -5,25 +5,31 @@
 // with A_a [R][K] and B_a [N][R] in bf16 and a row without an adapter
 // (ids[m] outside [0, n)) taking the first term alone.
 //
-// Both small products run on v_mfma_f32_16x16x32_bf16.  bf16 operands enter
-// as they are; a float32 operand (x, and always t = x A^T) enters as three
-// bf16 pieces of 8 significant bits each: bf16 has float32's exponent range, so no
-// scaling is needed, and the pieces hold the value's 24 bits.  Sums are
-// float32.
-//
-// Rows of different adapters share an MFMA block of 16 rows: the block is
-// multiplied by every adapter that occurs in it and each row keeps the result
-// of its own.  The results are selected, never multiplied by zero, so an
-// infinity or NaN in one adapter reaches no row of another.
+// What a row costs beside the shared product is the reading of its adapter
+// (2 R (K + N) bytes), so the kernels differ by who shares an adapter.  A few
+// rows of many requests: every row by itself, float32 dot products on the
+// vector units, spread over as many waves as there are (row, rank) or (row,
+// column) pairs; the second product runs in the epilogue of the streamed base
+// product, or where its split sums are added.  Many rows (prompts): blocks of
+// rows on v_mfma_f32_16x16x32_bf16.  There bf16 operands enter as they are,
+// and a float32 operand (x, and always t = x A^T) as three bf16 pieces of 8
+// significant bits each: bf16 has float32's exponent range, so no scaling is
+// needed, and the pieces hold the value's 24 bits.  Rows of different adapters
+// share an MFMA block: it is multiplied by every adapter that occurs in it and
+// each row keeps the result of its own.  Results are selected, never
+// multiplied by zero, so an infinity or NaN in one adapter reaches no row of
+// another.
 #include "lora.h"
 
+#include <cmath>
+
 #include "dispatch.h"
+#include "stream.h"
 
 namespace w4 {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma_bf16(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
@@ -93,30 +99,209 @@ __device__ __forceinline__ int rank_of(const LoraSet& s, int id) {
   return r < 0 ? 0 : (r > s.R ? s.R : r);
 }
 
-// ---------------------------------------------------------------- x A^T
+// ---------------------------------------------------------------- by rows
 
-constexpr int kShrinkThreads = 256;
-constexpr int kShrinkWaves = kShrinkThreads / kWave;
+// The sum over the wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
 
 struct ShrinkArgs {
   const void* x;
   const int* ids;
   LoraSet s[2];
-  int M, K, splits, slots, chunks;  // chunks: of kLoraChunk ranks, over the larger R
+  int M, K, splits, chunks;  // chunks: of kLoraChunk ranks, over the larger R
 };
 
-// One workgroup: 16 kRB rows, one chunk of 16 kCB ranks, one K split, one slot
-// of the block's distinct adapters, one projection.  The four waves take
-// quarters of the split's K and meet in LDS.
-template <typename XT, int kXP, int kRB, int kCB>
-__global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const ShrinkArgs a) {
-  constexpr int kU = kRB == 1 ? 4 : 2;
+// t of one row and kQ ranks: the four waves of a workgroup take quarters of K,
+// all of a step's loads in flight together.
+template <int kXP, int kQ>
+__global__ __launch_bounds__(256) void shrink_rows_kernel(const ShrinkArgs a) {
+  __shared__ float red[4][kQ];
+  const LoraSet s = a.s[blockIdx.z];
+  const int m = blockIdx.x, r0 = blockIdx.y * kQ;
+  const int id = s.a != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
+  if (id < 0 || r0 >= rank_of(s, id)) return;
+  const int wv = wave_id(), lane = lane_id();
+  const int nc = a.K / 8, per = (nc + 255) / 256 * 64;  // chunks of 8, per wave
+  const int c_lo = wv * per, c_hi = min(nc, c_lo + per);
+  const size_t xrow = static_cast<size_t>(m) * a.K;
+  const uint16_t* ar = s.a + (static_cast<size_t>(id) * s.R + r0) * a.K;
+  float acc[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) acc[q] = 0.0f;
+  constexpr int kU = 4;
+  for (int c0 = c_lo + lane; c0 < c_hi; c0 += 64 * kU) {
+    StreamX8<kXP> x[kU];
+    uint4 w[kU][kQ];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int c = min(c0 + 64 * u, nc - 1);
+      x[u] = stream_load_x<kXP>(a.x, xrow + 8 * static_cast<size_t>(c));
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)  // (ranks past R read the last one and are not stored)
+        w[u][q] = *reinterpret_cast<const uint4*>(ar + static_cast<size_t>(min(q, s.R - 1 - r0)) * a.K +
+                                                  8 * static_cast<size_t>(c));
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (c0 + 64 * u >= c_hi) break;
+      float v[8];
+      stream_x_values<kXP>(x[u], v);
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const uint32_t d[4] = {w[u][q].x, w[u][q].y, w[u][q].z, w[u][q].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[q] = fmaf(v[2 * i], __uint_as_float(d[i] << 16), acc[q]);
+          acc[q] = fmaf(v[2 * i + 1], __uint_as_float(d[i] & 0xffff0000u), acc[q]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    acc[q] = wave_sum(acc[q]);
+    if (lane == 0) red[wv][q] = acc[q];
+  }
+  __syncthreads();
+  const int q = threadIdx.x;
+  if (q < kQ && r0 + q < s.R)
+    s.t[static_cast<size_t>(m) * s.R + r0 + q] = s.scale[id] * ((red[0][q] + red[1][q]) + (red[2][q] + red[3][q]));
+}
+
+// 8 ranks r .. r + 7 of one row of B, those at or past `rank` as zero.
+__device__ __forceinline__ uint4 load_b8(const uint16_t* row, int r, int rank) {
+  if (r >= rank) return make_uint4(0, 0, 0, 0);
+  uint4 v = *reinterpret_cast<const uint4*>(row + r);
+  const int n = rank - r;
+  if (n < 8) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : (2 * i < n ? w[i] & 0xffffu : 0u);
+  }
+  return v;
+}
+
+// v[i] += t . row i of b (kC rows ld apart), ranks below `rank` in ascending
+// order; 32 ranks' loads in flight together.  t is read up to the next
+// multiple of 8.
+template <int kC>
+__device__ __forceinline__ void row_dots(const float* t, const uint16_t* b, int ld, int rank, float v[kC]) {
+  for (int r0 = 0; r0 < rank; r0 += 32) {
+    uint4 w[kC][4];
+    float4 tv[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + 8 * j;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) w[i][j] = load_b8(b + static_cast<size_t>(i) * ld, r, rank);
+      if (r < rank) {
+        tv[j][0] = *reinterpret_cast<const float4*>(t + r);
+        tv[j][1] = *reinterpret_cast<const float4*>(t + r + 4);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = rank - r0 - 8 * j;
+      if (n <= 0) break;
+      float tj[8] = {tv[j][0].x, tv[j][0].y, tv[j][0].z, tv[j][0].w, tv[j][1].x, tv[j][1].y, tv[j][1].z, tv[j][1].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tj[e] = e < n ? tj[e] : 0.0f;  // (what was never written)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const uint32_t d[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[i] = fmaf(tj[2 * e], __uint_as_float(d[e] << 16), v[i]);
+          v[i] = fmaf(tj[2 * e + 1], __uint_as_float(d[e] & 0xffff0000u), v[i]);
+        }
+      }
+    }
+  }
+}
+
+constexpr int kFinishThreads = 256;
+constexpr int kFinishSplits = kMaxSplits;
+constexpr int kLoraUnits = 512;  // LDS units (16 bytes) per wave of the streamed product
+
+// Four columns of base: rs * the sum of the planes, in split order, all loads
+// in flight before the sum.
+__device__ __forceinline__ f32x4 base_sum(const LoraBase& b, int m, int n) {
+  const float* p = b.p + static_cast<size_t>(m) * b.ld + n;
+  f32x4 v[kFinishSplits];
+#pragma unroll
+  for (int s = 0; s < kFinishSplits; ++s)
+    if (s < b.S) v[s] = *reinterpret_cast<const f32x4*>(p + s * b.split_stride);
+  f32x4 t = v[0];
+#pragma unroll
+  for (int s = 1; s < kFinishSplits; ++s)
+    if (s < b.S) t += v[s];
+  return b.rs != nullptr ? t * b.rs[m] : t;
+}
+
+// The same without room for all planes at once.
+__device__ __forceinline__ f32x4 base_sum_loop(const LoraBase& b, int m, int n) {
+  const float* p = b.p + static_cast<size_t>(m) * b.ld + n;
+  f32x4 t = *reinterpret_cast<const f32x4*>(p);
+  for (int s = 1; s < b.S; ++s) t += *reinterpret_cast<const f32x4*>(p + s * b.split_stride);
+  return b.rs != nullptr ? t * b.rs[m] : t;
+}
+
+__device__ __forceinline__ void store4(void* out, int bf16, size_t at, f32x4 v) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+                   f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
+}
+
+// One row, four columns a thread; the row's t is the workgroup's.
+template <bool kGlu>
+__global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(const LoraFinishArgs a) {
+  __shared__ __attribute__((aligned(16))) float t[2][kLoraMaxRank];
+  const int m = blockIdx.x, n = (blockIdx.y * kFinishThreads + static_cast<int>(threadIdx.x)) * 4;
+  int id[2], rank[2];
+#pragma unroll
+  for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
+    const LoraSet& s = w == 0 ? a.s0 : a.s1;
+    id[w] = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
+    rank[w] = id[w] >= 0 ? rank_of(s, id[w]) : 0;
+    for (int r = threadIdx.x; r < rank[w]; r += kFinishThreads) t[w][r] = s.t[static_cast<size_t>(m) * s.R + r];
+    // (ranks up to the next multiple of 8 are read, and dropped)
+  }
+  __syncthreads();
+  if (n >= a.N) return;
+  f32x4 v;
+#pragma unroll
+  for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
+    const LoraSet& s = w == 0 ? a.s0 : a.s1;
+    const f32x4 b = base_sum(w == 0 ? a.base0 : a.base1, m, n);
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (rank[w] > 0) row_dots<4>(t[w], s.b + (static_cast<size_t>(id[w]) * a.N + n) * s.R, s.R, rank[w], d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w == 0 ? b[i] + d[i] : silu(v[i]) * (b[i] + d[i]);
+  }
+  store4(a.out, a.out_bf16, static_cast<size_t>(m) * a.N + n, v);
+}
+
+// ---------------------------------------------------------------- by blocks: x A^T
+
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkWaves = kShrinkThreads / kWave;
+
+// One workgroup: 64 rows, one chunk of 16 kCB ranks, one K split, one
+// projection.  The four waves take quarters of the split's K and meet in LDS.
+template <int kXP, int kCB>
+__global__ __launch_bounds__(kShrinkThreads) void shrink_blocks_kernel(const ShrinkArgs a) {
+  constexpr int kRB = 4, kU = 2;
   __shared__ float red[kShrinkWaves][kRB * kLoraRows][kCB * 16];
   int b = blockIdx.x;
   const int split = b % a.splits;
   b /= a.splits;
-  const int slot = b % a.slots;
-  b /= a.slots;
   const int chunk = b % a.chunks;
   const int block = b / a.chunks;
   const LoraSet s = a.s[blockIdx.y];
@@ -127,22 +312,21 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const ShrinkArgs
   const int lc = lane & 15, kb = lane >> 4;
 
   // lane l knows the adapter of row m0 + l
-  const int mine = lane < kRB * kLoraRows ? adapter_of(a.ids, m0 + lane, a.M, s.n) : -1;
+  const int mine = adapter_of(a.ids, m0 + lane, a.M, s.n);
   const int steps = a.K / 32;
   const int per = (steps + a.splits * kShrinkWaves - 1) / (a.splits * kShrinkWaves);
   const int k_lo = min(steps, (split * kShrinkWaves + wv) * per), k_hi = min(steps, k_lo + per);
-  const XT* x = static_cast<const XT*>(a.x);
-  const XT* xr[kRB];
+  const char* xr[kRB];
 #pragma unroll
   for (int rb = 0; rb < kRB; ++rb)
-    xr[rb] = x + static_cast<size_t>(min(m0 + rb * kLoraRows + lc, a.M - 1)) * a.K + 8 * kb;
+    xr[rb] = static_cast<const char*>(a.x) +
+             (static_cast<size_t>(min(m0 + rb * kLoraRows + lc, a.M - 1)) * a.K + 8 * kb) * (kXP == 1 ? 2 : 4);
 
   uint64_t todo = __ballot(mine >= 0);
-  for (int turn = 0; todo != 0; ++turn) {
-    const int id = __builtin_amdgcn_readlane(mine, __ffsll(static_cast<unsigned long long>(todo)) - 1);
+  while (todo != 0) {
+    const int id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
     const uint64_t rows = __ballot(mine == id);
     todo &= ~rows;
-    if (turn % a.slots != slot) continue;
     f32x4 acc[kRB][kCB];
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
@@ -163,7 +347,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const ShrinkArgs
 #pragma unroll
         for (int cb = 0; cb < kCB; ++cb) af[u][cb] = *reinterpret_cast<const uint4*>(ar[cb] + k);
 #pragma unroll
-        for (int rb = 0; rb < kRB; ++rb) xw[u][rb] = load_x8<kXP>(xr[rb] + k);
+        for (int rb = 0; rb < kRB; ++rb) xw[u][rb] = load_x8<kXP>(xr[rb] + k * (kXP == 1 ? 2 : 4));
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -174,7 +358,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const ShrinkArgs
         }
 #pragma unroll
         for (int rb = 0; rb < kRB; ++rb) {
-          if (kRB > 1 && ((rows >> (rb * kLoraRows)) & 0xffffu) == 0) continue;  // (wave-uniform)
+          if (((rows >> (rb * kLoraRows)) & 0xffffu) == 0) continue;  // (wave-uniform)
           uint4 xf[kXP];
           pieces_x8<kXP>(xw[u][rb], xf);
 #pragma unroll
@@ -196,18 +380,19 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(const ShrinkArgs
         for (int i = 0; i < 4; ++i) red[wv][rb * kLoraRows + 4 * kb + i][16 * cb + lc] = acc[rb][cb][i];
     __syncthreads();
     float* t = s.t + static_cast<size_t>(split) * a.M * s.R;
+    const float scale = s.scale[id];
     for (int e = threadIdx.x; e < kRB * kLoraRows * kCB * 16; e += kShrinkThreads) {
       const int r = e % (kCB * 16), m = e / (kCB * 16);
       if (((rows >> m) & 1) == 0 || r0 + r >= s.R) continue;
       float v = red[0][m][r];
 #pragma unroll
       for (int w = 1; w < kShrinkWaves; ++w) v += red[w][m][r];
-      t[static_cast<size_t>(m0 + m) * s.R + r0 + r] = v;
+      t[static_cast<size_t>(m0 + m) * s.R + r0 + r] = v * scale;
     }
   }
 }
 
-// ---------------------------------------------------------------- t B^T
+// ---------------------------------------------------------------- by blocks: t B^T
 
 // t of 16 rows and one chunk of ranks as bf16 pieces in LDS; rows are padded
 // so that the 16 rows of one fragment read spread over the banks.
@@ -216,7 +401,7 @@ struct TPieces {
   uint16_t p[3][kLoraRows][kTPad];
 };
 
-// Scaled split sums of the rows m0 .. m0 + 15, ranks r0 .. r0 + 63, as pieces.
+// Summed splits of the rows m0 .. m0 + 15, ranks r0 .. r0 + 63, as pieces.
 // Ranks the row's adapter does not use, and rows without one, are zero.
 __device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M, int m0, int r0, int splits,
                                         int tid, int nthreads, TPieces& tp) {
@@ -227,7 +412,6 @@ __device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M,
     if (id >= 0 && r0 + r < rank_of(s, id)) {
       const float* t = s.t + static_cast<size_t>(m0 + m) * s.R + r0 + r;
       for (int i = 0; i < splits; ++i) v += t[static_cast<size_t>(i) * M * s.R];
-      v *= s.scale[id];
     }
     uint16_t p[3];
     split3(v, p);
@@ -236,26 +420,11 @@ __device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M,
   }
 }
 
-// 8 ranks r .. r + 7 of one row of B, those at or past `rank` as zero.
-__device__ __forceinline__ uint4 load_b8(const uint16_t* row, int r, int rank) {
-  if (r >= rank) return make_uint4(0, 0, 0, 0);
-  uint4 v = *reinterpret_cast<const uint4*>(row + r);
-  const int n = rank - r;
-  if (n < 8) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : (2 * i < n ? w[i] & 0xffffu : 0u);
-  }
-  return v;
-}
-
-constexpr int kFinishThreads = 256;
-
 // One workgroup: 16 rows x 64 kNB columns, 16 kNB columns a wave.  B enters as
 // the MFMA's row operand and t as its column operand, so a lane's four
 // results are four adjacent columns of one row.
 template <int kNB, bool kGlu>
-__global__ __launch_bounds__(kFinishThreads) void finish_kernel(const LoraFinishArgs a) {
+__global__ __launch_bounds__(kFinishThreads) void finish_blocks_kernel(const LoraFinishArgs a) {
   __shared__ TPieces tp[kGlu ? 2 : 1];
   const int blocks = (a.M + kLoraRows - 1) / kLoraRows;
   const int m0 = static_cast<int>(blockIdx.x % blocks) * kLoraRows;
@@ -320,46 +489,271 @@ __global__ __launch_bounds__(kFinishThreads) void finish_kernel(const LoraFinish
     const int n = n0 + 16 * nb + 4 * kb;
     if (n >= a.N) break;
     const size_t at = static_cast<size_t>(row) * a.N + n;
-    f32x4 v = *reinterpret_cast<const f32x4*>(a.base0 + at) + sum[0][nb];
+    f32x4 v = base_sum_loop(a.base0, row, n) + sum[0][nb];
     if (kGlu) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(a.base1 + at) + sum[1][nb];
+      const f32x4 u = base_sum_loop(a.base1, row, n) + sum[1][nb];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
     }
-    if (a.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-          make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
-                     f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
-    else
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
+    store4(a.out, a.out_bf16, at, v);
   }
 }
 
-template <typename XT, int kXP, int kRB>
-void launch_shrink_rb(const ShrinkArgs& a, int cb, dim3 grid, hipStream_t stream) {
-  if (cb == 1)
-    shrink_kernel<XT, kXP, kRB, 1><<<grid, kShrinkThreads, 0, stream>>>(a);
-  else if (cb == 2)
-    shrink_kernel<XT, kXP, kRB, 2><<<grid, kShrinkThreads, 0, stream>>>(a);
+// ---------------------------------------------------------------- a few rows, one launch
+
+// The base product of a few rows, streamed as in stream.h, and the adapters'
+// second product in its epilogue.  A workgroup takes `cols` blocks of 64
+// columns (of gate and the same of up) and one K split; wave w takes matrix w %
+// kMats, one column block and one of the split's K parts (gpp groups each).
+// It stages all rows of its K range, each scaled by a power of two of its own
+// there.  The parts meet in LDS and the splits in memory as in the split-K
+// GEMV (agent-scope stores, an arrival counter, the last workgroup sums in
+// split order); then a thread takes a row and two columns: their sums, their
+// adapter's dot products and, with gate and up, silu(gate) * up.
+template <int kXP, int kP, int kI, int kMats>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4)))
+void lora_stream_kernel(const LoraStreamArgs a) {
+  constexpr int kHold = 4;  // chunks of x a thread keeps in registers
+  extern __shared__ uint4 lds[];
+  __shared__ uint32_t amax[kStreamRows];
+  __shared__ int last;
+  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int wv = wave_id(), lane = lane_id();
+  const int lc = lane & 15, kb = lane >> 4;
+  const int cshift = __builtin_ctz(a.cols);
+  const int mat = kMats == 2 ? wv & 1 : 0, col = (wv / kMats) & (a.cols - 1), part = (wv / kMats) >> cshift;
+  const int G = a.K / kGroup, groups = a.parts * a.gpp, g_wg = split * groups;
+  const int block = tile * a.cols + col;
+  const bool wave_ok = block * 64 < a.N;
+
+  // the ring: a wave past the last column streams column block 0 and stores
+  // nothing, a part past the last group the last one (against staged zeros)
+  const StreamLane off = stream_lane(wave_ok ? block * 64 : 0, lane);
+  const u32x4* qw = mat ? a.qw1 : a.qw0;
+  const float* sc = mat ? a.sc1 : a.sc0;
+  int g = min(g_wg + part * a.gpp, G - 1);
+  const int g_last = max(g, min(g_wg + (part + 1) * a.gpp, G) - 1);
+  auto next = [&](StreamCodes& c) {
+    stream_codes(uniform_at(qw, static_cast<uint64_t>(g) * a.N * 16),
+                 uniform_at(sc, static_cast<uint64_t>(g >> a.gshift) * a.N * 4), a.N, off, c);
+    g = min(g + 1, g_last);
+  };
+  StreamCodes ring[kStreamRing];
+
+  // Staging: 2^k threads a row, chunks of 8 values (k block c & 3 of group c >> 2).
+  const int rshift = stream_rshift<kP>(a.M);
+  const int tshift = 31 - __builtin_clz(nt) - stream_rshift<1>(a.M);  // log2 of a row's threads
+  const int row = tid >> tshift, c0 = tid & ((1 << tshift) - 1), cstep = 1 << tshift;
+  const int chunks = groups * 4, held = min(chunks, max(0, (G - g_wg) * 4));  // (chunks of K in range)
+  const size_t x0 = static_cast<size_t>(min(row, a.M - 1)) * a.K + static_cast<size_t>(g_wg) * kGroup;
+  if (tid < kStreamLds0) lds[tid] = make_uint4(0, 0, 0, 0);
+  if (tid < kStreamRows) amax[tid] = 0;
+  StreamX8<kXP> xh[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    xh[i] = stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(max(0, min(c0 + i * cstep, held - 1))));
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < kStreamRing; ++j) next(ring[j]);
+  __syncthreads();
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (c0 + i * cstep < held) mx = stream_max8<kXP>(xh[i], mx);
+  for (int c = c0 + kHold * cstep; c < held; c += cstep)
+    mx = stream_max8<kXP>(stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(c)), mx);
+  if (tshift >= 6) {  // a wave's lanes belong to one row
+    mx = wave_max(mx);
+    if (lane == 0 && row < a.M) atomicMax(&amax[row], mx);
+  } else if (row < a.M) {
+    atomicMax(&amax[row], mx);
+  }
+  __syncthreads();
+  if (row < a.M) {
+    const uint32_t am = amax[row];
+    for (int i = 0, c = c0; c < chunks; ++i, c += cstep) {
+      const int unit = stream_unit(c >> 2, c & 3, row * kP, rshift);
+      if (c >= held) {
+        stream_put_zero<kP>(lds, unit);
+        continue;
+      }
+      StreamX8<kXP> v;
+      if (i == 0)
+        v = xh[0];
+      else if (i == 1)
+        v = xh[1];
+      else if (i == 2)
+        v = xh[2];
+      else if (i == 3)
+        v = xh[3];
+      else
+        v = stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(c));
+      stream_put_row<kP, kXP>(lds, unit, v, am);
+    }
+  }
+  __syncthreads();
+
+  float acc[4][kI];
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+    for (int i = 0; i < kI; ++i) acc[cb][i] = 0.0f;
+  stream_run<kP, kI>(lds, stream_frag<kP>(lane, a.M, part * a.gpp, rshift), a.gpp, magic_vgpr(), ring, next, acc);
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const int m = kb + 4 * i;
+    const float f = m < a.M ? ldexpf(1.0f, -stream_exp(__uint_as_float(amax[m]))) : 0.0f;
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb) acc[cb][i] *= f;
+  }
+  // the parts' sums, in order
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  const int pw = kMats << cshift;  // waves of a part
+  __syncthreads();  // the window is free
+  if (part > 0) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+      red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+  }
+  __syncthreads();
+  // the tile's sums [mat][row][64 cols]: in LDS behind the parts', or the split's in memory
+  const int ld = 64 << cshift;
+  float* sums = reinterpret_cast<float*>(lds + (nt / kWave) * 256);
+  float* base = a.partials + static_cast<size_t>(tile) * a.splits * kMats * a.M * ld;
+  const size_t ps = static_cast<size_t>(kMats) * a.M * ld;
+  if (part == 0) {
+    for (int p = 1; p < a.parts; ++p)
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const f32x4 v = red[((p * pw + wv) * kI + i) * kWave + lane];
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) acc[cb][i] += v[cb];
+      }
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int m = kb + 4 * i;
+      if (m >= a.M) continue;
+      const size_t at = (static_cast<size_t>(mat) * a.M + m) * ld + col * 64 + 4 * lc;
+      if (a.splits == 1) {
+        *reinterpret_cast<f32x4*>(sums + at) = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+      } else {
+        uint64_t* o = reinterpret_cast<uint64_t*>(base + split * ps + at);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          __hip_atomic_store(o + j,
+                             static_cast<uint64_t>(__float_as_uint(acc[2 * j + 1][i])) << 32 |
+                                 __float_as_uint(acc[2 * j][i]),
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+  }
+  if (a.splits > 1) {
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's stores are complete
+    __syncthreads();
+    if (tid == 0)
+      last = __hip_atomic_fetch_add(&a.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.splits - 1;
+    __syncthreads();
+    if (!last) return;
+    if (tid == 0) __hip_atomic_store(&a.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  } else {
+    __syncthreads();
+  }
+  const int pshift = 5 + cshift;  // pairs of columns of a row: 2^pshift
+  for (int q = tid; q < a.M << pshift; q += nt) {
+    const int m = q >> pshift, c = 2 * (q - (m << pshift)), n = tile * ld + c;
+    if (n >= a.N) continue;
+    float v[kMats][2];
+#pragma unroll
+    for (int w = 0; w < kMats; ++w) {
+      const size_t at = (static_cast<size_t>(w) * a.M + m) * ld + c;
+      if (a.splits == 1) {
+        v[w][0] = sums[at];
+        v[w][1] = sums[at + 1];
+      } else {
+        constexpr int kB = 8;
+        v[w][0] = v[w][1] = 0.0f;
+        for (int s0 = 0; s0 < a.splits; s0 += kB) {
+          uint64_t p[kB];
+#pragma unroll
+          for (int j = 0; j < kB; ++j)
+            p[j] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(base + min(s0 + j, a.splits - 1) * ps + at),
+                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+          for (int j = 0; j < kB; ++j)
+            if (s0 + j < a.splits) {
+              v[w][0] += __uint_as_float(static_cast<uint32_t>(p[j]));
+              v[w][1] += __uint_as_float(static_cast<uint32_t>(p[j] >> 32));
+            }
+        }
+      }
+      const LoraSet& s = w == 0 ? a.s0 : a.s1;
+      const int id = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
+      if (id >= 0)
+        row_dots<2>(s.t + static_cast<size_t>(m) * s.R, s.b + (static_cast<size_t>(id) * a.N + n) * s.R, s.R,
+                    rank_of(s, id), v[w]);
+    }
+    if (kMats == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[0][i] = silu(v[0][i]) * v[kMats - 1][i];
+    }
+    const size_t at = static_cast<size_t>(m) * a.N + n;
+    if (a.out_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+          f32_to_bf16(v[0][0]) | static_cast<uint32_t>(f32_to_bf16(v[0][1])) << 16;
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(v[0][0], v[0][1]);
+  }
+}
+
+template <int kXP, int kP, int kMats>
+void launch_stream_mats(const LoraStreamArgs& a, dim3 grid, dim3 threads, size_t lds, hipStream_t stream) {
+  if (a.M <= 4)
+    lora_stream_kernel<kXP, kP, 1, kMats><<<grid, threads, lds, stream>>>(a);
+  else if (a.M <= 8 || kP == 2)
+    lora_stream_kernel<kXP, kP, 2, kMats><<<grid, threads, lds, stream>>>(a);
   else
-    shrink_kernel<XT, kXP, kRB, 4><<<grid, kShrinkThreads, 0, stream>>>(a);
+    lora_stream_kernel<kXP, kP, 4 / kP, kMats><<<grid, threads, lds, stream>>>(a);
+}
+
+// Ranks a workgroup of the row kernel takes: one, until there are workgroups
+// enough that sharing the reads of x is worth more.
+int shrink_quota(size_t dots) { return dots >= 2048 ? 4 : (dots >= 1024 ? 2 : 1); }
+
+// 16-rank column blocks of one workgroup's chunk.
+int shrink_cols(int R) { return R <= 16 ? 1 : (R <= 32 ? 2 : 4); }
+
+template <int kXP>
+void launch_shrink_blocks(const ShrinkArgs& a, int cb, dim3 grid, hipStream_t stream) {
+  if (cb == 1)
+    shrink_blocks_kernel<kXP, 1><<<grid, kShrinkThreads, 0, stream>>>(a);
+  else if (cb == 2)
+    shrink_blocks_kernel<kXP, 2><<<grid, kShrinkThreads, 0, stream>>>(a);
+  else
+    shrink_blocks_kernel<kXP, 4><<<grid, kShrinkThreads, 0, stream>>>(a);
+}
+
+template <int kXP>
+void launch_shrink_rows(const ShrinkArgs& a, int R, int n_sets, hipStream_t stream) {
+  const int q = shrink_quota(static_cast<size_t>(a.M) * R * n_sets);
+  const dim3 grid(a.M, (R + q - 1) / q, n_sets);
+  if (q == 4)
+    shrink_rows_kernel<kXP, 4><<<grid, 256, 0, stream>>>(a);
+  else if (q == 2)
+    shrink_rows_kernel<kXP, 2><<<grid, 256, 0, stream>>>(a);
+  else
+    shrink_rows_kernel<kXP, 1><<<grid, 256, 0, stream>>>(a);
 }
 
 }  // namespace
 
-// 16-rank column blocks of one workgroup's chunk.
-static int shrink_cols(int R) { return R <= 16 ? 1 : (R <= 32 ? 2 : 4); }
-
-ShrinkShape shrink_shape(int M, int K, int R, int n, int sets) {
+ShrinkShape shrink_shape(int M, int K, int R) {
   ShrinkShape sh;
-  sh.rb = M <= kLoraRows ? 1 : 4;
-  const int rows = sh.rb * kLoraRows;
-  const int blocks = (M + rows - 1) / rows;
-  const int chunks = (R + 16 * shrink_cols(R) - 1) / (16 * shrink_cols(R));
-  sh.slots = std::min({std::min(M, rows), n, 8});
-  // about two workgroups per CU, a wave keeping at least two k steps
-  const int most = std::max(1, std::min(M <= 256 ? kLoraMaxSplits : 4, K / 32 / (2 * kShrinkWaves)));
-  sh.splits = std::min(most, std::max(1, 512 / std::max(1, blocks * chunks * sets * sh.slots)));
+  sh.rows = static_cast<size_t>(M) * R <= 4096;
+  if (sh.rows) return sh;
+  const int blocks = (M + 63) / 64, chunks = (R + 16 * shrink_cols(R) - 1) / (16 * shrink_cols(R));
+  // about one workgroup per CU, a wave keeping at least four k steps
+  sh.splits = std::max(1, std::min({8, 256 / (blocks * chunks), K / 32 / (4 * kShrinkWaves)}));
   return sh;
 }
 
@@ -369,38 +763,47 @@ w4a16_status_t launch_lora_shrink(const void* x, w4a16_dtype_t xt, int M, int K,
   ShrinkArgs a{};
   a.x = x;
   a.ids = ids;
-  for (int i = 0; i < n_sets; ++i) {
-    a.s[i] = sets[i];
-    if (sets[i].a != nullptr) R = std::max(R, sets[i].R);
-  }
-  if (R == 0 || M == 0) return W4A16_OK;
-  const int cb = shrink_cols(R);
   a.M = M;
   a.K = K;
   a.splits = sh.splits;
-  a.slots = sh.slots;
-  a.chunks = (R + 16 * cb - 1) / (16 * cb);
-  const size_t rows = static_cast<size_t>(sh.rb) * kLoraRows;
-  const size_t blocks = (M + rows - 1) / rows * a.chunks * a.slots * a.splits;
-  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n_sets));
-  if (xt == W4A16_BF16) {
-    if (sh.rb == 1)
-      launch_shrink_rb<uint16_t, 1, 1>(a, cb, grid, stream);
+  int n = 0;
+  for (int i = 0; i < n_sets; ++i)
+    if (sets[i].a != nullptr) {
+      a.s[n++] = sets[i];
+      R = std::max(R, sets[i].R);
+    }
+  if (n == 0 || M == 0) return W4A16_OK;
+  if (sh.rows) {
+    if (xt == W4A16_BF16)
+      launch_shrink_rows<1>(a, R, n, stream);
     else
-      launch_shrink_rb<uint16_t, 1, 4>(a, cb, grid, stream);
-  } else {
-    if (sh.rb == 1)
-      launch_shrink_rb<float, 3, 1>(a, cb, grid, stream);
-    else
-      launch_shrink_rb<float, 3, 4>(a, cb, grid, stream);
+      launch_shrink_rows<2>(a, R, n, stream);
+    return launch_status();
   }
+  const int cb = shrink_cols(R);
+  a.chunks = (R + 16 * cb - 1) / (16 * cb);
+  const size_t blocks = (static_cast<size_t>(M) + 63) / 64 * a.chunks * a.splits;
+  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n));
+  if (xt == W4A16_BF16)
+    launch_shrink_blocks<1>(a, cb, grid, stream);
+  else
+    launch_shrink_blocks<3>(a, cb, grid, stream);
   return launch_status();
 }
 
 w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return W4A16_OK;
-  const bool glu = a.base1 != nullptr;
+  if (a.base0.S > kFinishSplits || a.base1.S > kFinishSplits) return W4A16_ERR_UNSUPPORTED;
+  const bool glu = a.base1.p != nullptr;
+  if (a.rows) {
+    const dim3 grid(a.M, (a.N + 4 * kFinishThreads - 1) / (4 * kFinishThreads));
+    if (glu)
+      finish_rows_kernel<true><<<grid, kFinishThreads, 0, stream>>>(a);
+    else
+      finish_rows_kernel<false><<<grid, kFinishThreads, 0, stream>>>(a);
+    return launch_status();
+  }
   // 64 columns a wave once there are rows to fill the chip with; else 16
   const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{1} << 21);
   const int cols = tall ? 256 : 64;
@@ -408,13 +811,79 @@ w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
   if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks));
   if (glu && tall)
-    finish_kernel<4, true><<<grid, kFinishThreads, 0, stream>>>(a);
+    finish_blocks_kernel<4, true><<<grid, kFinishThreads, 0, stream>>>(a);
   else if (glu)
-    finish_kernel<1, true><<<grid, kFinishThreads, 0, stream>>>(a);
+    finish_blocks_kernel<1, true><<<grid, kFinishThreads, 0, stream>>>(a);
   else if (tall)
-    finish_kernel<4, false><<<grid, kFinishThreads, 0, stream>>>(a);
+    finish_blocks_kernel<4, false><<<grid, kFinishThreads, 0, stream>>>(a);
   else
-    finish_kernel<1, false><<<grid, kFinishThreads, 0, stream>>>(a);
+    finish_blocks_kernel<1, false><<<grid, kFinishThreads, 0, stream>>>(a);
+  return launch_status();
+}
+
+// Picks waves, column blocks, K parts and splits by an estimate of the launch's
+// time: the weights at 6.5 TB/s or, with few groups in flight, 0.35 us a group
+// of a wave; 2.5 us for staging and start; 2.5 us for splits to meet, and 0.1
+// us for each.
+LoraStreamPlan plan_lora_stream(int M, int pieces, int N, int mats, int K) {
+  LoraStreamPlan best;
+  const int G = K / kGroup, blocks = N / 64;
+  int rshift = pieces - 1;
+  while ((1 << (rshift - pieces + 1)) < M) ++rshift;
+  double best_us = 1e30;
+  for (int waves = 4; waves <= 16; waves *= 2)
+    for (int cols = 1; cols * mats <= waves; cols *= 2) {
+      const int parts = waves / (cols * mats), tiles = (blocks + cols - 1) / cols;
+      for (int splits = 1; splits <= kMaxSplits; ++splits) {
+        const int gpp = (G + splits * parts * kStreamRing - 1) / (splits * parts * kStreamRing) * kStreamRing;
+        if (splits > 1 && (splits - 1) * parts * gpp >= G) break;  // an empty split
+        if (((parts * gpp * 4) << rshift) > waves * kLoraUnits) continue;  // the window
+        if (splits > 1 && tiles * sizeof(int) > kCounterBytes) continue;
+        const double wgs = static_cast<double>(tiles) * splits, room = 256.0 * (16 / waves);
+        const double rounds = std::ceil(wgs / room);
+        const double bytes = wgs * waves * gpp * 1280.0;
+        const double us = std::max(bytes / 6.5e6, rounds * gpp * 0.35) + rounds * 2.5 +
+                          (splits > 1 ? 2.5 + 0.1 * splits : 0.0);
+        if (us < best_us) {
+          best_us = us;
+          best.ok = true;
+          best.waves = waves;
+          best.cols = cols;
+          best.parts = parts;
+          best.splits = splits;
+          best.gpp = gpp;
+          best.tiles = tiles;
+        }
+      }
+    }
+  if (best.splits > 1)
+    best.partial_bytes = static_cast<size_t>(best.tiles) * best.splits * mats * M * best.cols * 64 * 4;
+  return best;
+}
+
+w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hipStream_t stream) {
+  a.cols = p.cols;
+  a.parts = p.parts;
+  a.splits = p.splits;
+  a.gpp = p.gpp;
+  a.tiles = p.tiles;
+  const size_t blocks = static_cast<size_t>(p.tiles) * p.splits;
+  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks)), threads(p.waves * kWave);
+  const size_t lds = (static_cast<size_t>(p.waves) * kLoraUnits + kStreamLds0) * 16;
+  const bool glu = a.qw1 != nullptr;
+  if (a.x_f32 && a.pieces == 2) {
+    if (glu)
+      launch_stream_mats<2, 2, 2>(a, grid, threads, lds, stream);
+    else
+      launch_stream_mats<2, 2, 1>(a, grid, threads, lds, stream);
+  } else if (a.x_f32) {
+    launch_stream_mats<2, 1, 1>(a, grid, threads, lds, stream);  // h of a bf16 layer
+  } else if (glu) {
+    launch_stream_mats<1, 1, 2>(a, grid, threads, lds, stream);
+  } else {
+    launch_stream_mats<1, 1, 1>(a, grid, threads, lds, stream);
+  }
   return launch_status();
 }
 
@@ -432,50 +901,169 @@ w4a16_status_t check_lora(const w4a16_lora_t* l) {
 
 bool known_type(w4a16_dtype_t t) { return t == W4A16_F32 || t == W4A16_BF16; }
 
-size_t t_bytes(const w4a16_lora_t* l, int M, int splits) {
-  return l == nullptr ? 0 : static_cast<size_t>(splits) * M * l->rank * 4;
+size_t t_bytes(const w4a16_lora_t* l, int M, const ShrinkShape& sh) {
+  return l == nullptr ? 0 : static_cast<size_t>(sh.splits) * M * l->rank * 4;
+}
+
+// One projection (or gate and up together) with its adapters' second product:
+// a few rows in one streamed launch, more on the tiles with the product where
+// the tiles' split sums, or their output, are finished.
+struct LinearPlan {
+  bool stream = false, pair = false;  // pair: gate and up as two plain products
+  int pieces = 1;
+  LoraStreamPlan st;
+  MfmaPlan mf;
+  size_t ap_off = 0, rs_off = 0, partials_off = 0, base0_off = 0, base1_off = 0;
+  size_t bytes = 0;  // from the workspace's start, counters included
+};
+
+// lt: the layer's activation type; x_f32: this product's x is float32 (h).
+LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t* w0, const w4a16_weight_t* w1) {
+  LinearPlan p;
+  const int K = w0->K, N = w0->N;
+  Carve c;
+  size_t counters;
+  c.take(counters, kCounterBytes);
+  if (M <= gemv_rows(lt)) {
+    p.pieces = x_f32 && M <= kMaxGemvRows ? 2 : 1;
+    p.st = plan_lora_stream(M, p.pieces, N, w1 != nullptr ? 2 : 1, K);
+    p.stream = p.st.ok;  // (else K is too long for the windows of 32 splits)
+  }
+  if (p.stream) {
+    c.take(p.partials_off, p.st.partial_bytes);
+    p.bytes = c.cursor;
+    return p;
+  }
+  p.pieces = mfma_pieces(lt);
+  p.mf = plan_mfma(M, N, w1 != nullptr ? 1 : 0, K, lt, w1 == nullptr);
+  if (w1 != nullptr && p.mf.S == 1) {
+    p.pair = true;
+    p.bytes = plan_gemm(M, w0, lt).bytes;
+    c.cursor = round_up(p.bytes, 256);
+    c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
+    c.take(p.base1_off, static_cast<size_t>(M) * N * 4);
+    p.bytes = c.cursor;
+    return p;
+  }
+  c.take(p.ap_off, static_cast<size_t>(p.mf.P) * p.mf.Mp * K * 2 + (p.mf.wide ? 256 : 0));
+  c.take(p.rs_off, static_cast<size_t>(p.mf.Mp) * 4);
+  c.take(p.partials_off, mfma_partial_bytes(p.mf));
+  if (p.mf.S == 1 || p.mf.wide) c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
+  p.bytes = c.cursor;
+  return p;
+}
+
+w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt, int M, const w4a16_weight_t* w0,
+                           const w4a16_weight_t* w1, const LoraSet& s0, const LoraSet& s1, const int* ids,
+                           const ShrinkShape& sh, void* out, w4a16_dtype_t ot, char* ws, hipStream_t stream) {
+  const int K = w0->K, N = w0->N;
+  if (p.stream) {
+    LoraStreamArgs a{};
+    a.x = x;
+    a.x_f32 = xt == W4A16_F32;
+    a.pieces = p.pieces;
+    a.M = M;
+    a.K = K;
+    a.N = N;
+    a.qw0 = reinterpret_cast<const u32x4*>(w0->qw);
+    a.sc0 = w0->scales;
+    if (w1 != nullptr) {
+      a.qw1 = reinterpret_cast<const u32x4*>(w1->qw);
+      a.sc1 = w1->scales;
+    }
+    a.gshift = group_shift(w0);
+    a.s0 = s0;
+    a.s1 = s1;
+    a.ids = ids;
+    a.partials = reinterpret_cast<float*>(ws + p.partials_off);
+    a.counters = reinterpret_cast<int*>(ws);
+    a.out = out;
+    a.out_bf16 = ot == W4A16_BF16;
+    return launch_lora_stream(a, p.st, stream);
+  }
+  LoraFinishArgs f{};
+  f.s0 = s0;
+  f.s1 = s1;
+  f.ids = ids;
+  f.rows = sh.rows;
+  f.splits = sh.splits;
+  f.M = M;
+  f.N = N;
+  f.out = out;
+  f.out_bf16 = ot == W4A16_BF16;
+  float* base0 = reinterpret_cast<float*>(ws + p.base0_off);
+  w4a16_status_t st;
+  if (p.pair) {
+    float* base1 = reinterpret_cast<float*>(ws + p.base1_off);
+    const size_t gemm_bytes = plan_gemm(M, w0, xt).bytes;
+    if ((st = w4a16_gemm(x, xt, M, w0, base0, ws, gemm_bytes, stream)) != W4A16_OK) return st;
+    if ((st = w4a16_gemm(x, xt, M, w1, base1, ws, gemm_bytes, stream)) != W4A16_OK) return st;
+    f.base0 = LoraBase{base0, 1, M, N, 0, nullptr};
+    f.base1 = LoraBase{base1, 1, M, N, 0, nullptr};
+    return launch_lora_finish(f, stream);
+  }
+  _Float16* ap = reinterpret_cast<_Float16*>(ws + p.ap_off);
+  float* rs = reinterpret_cast<float*>(ws + p.rs_off);
+  st = launch_mfma_prep(x, xt, M, p.mf.Mp, K, p.mf.P, nullptr, 0, nullptr, ap, rs, stream);
+  if (st != W4A16_OK) return st;
+  MfmaArgs a = mfma_dense_args(p.mf, M, w0, w1, w1 != nullptr ? 1 : 0, ap, rs, ws, p.partials_off, 0);
+  if (p.mf.wide || p.mf.S == 1) {
+    a.out = base0;
+    st = p.mf.wide ? launch_wide(a, p.mf.tasks * p.mf.S, stream) : launch_mfma(a, p.mf.P, p.mf.tasks, stream);
+    f.base0 = LoraBase{base0, 1, M, N, 0, nullptr};
+  } else {
+    defer_split_k(a, p.mf);
+    st = launch_mfma(a, p.mf.P, p.mf.tasks * p.mf.S, stream);
+    const size_t plane = static_cast<size_t>(a.plane_rows) * a.plane_ld;
+    f.base0 = LoraBase{a.planes, a.S, a.plane_rows, a.plane_ld, plane * (w1 != nullptr ? 2 : 1), rs};
+    if (w1 != nullptr) {
+      f.base1 = f.base0;
+      f.base1.p += plane;
+    }
+  }
+  if (st != W4A16_OK) return st;
+  return launch_lora_finish(f, stream);
 }
 
 struct LoraGemmPlan {
   ShrinkShape sh;
-  size_t gemm_bytes = 0, t_off = 0, base_off = 0, bytes = 0;
+  LinearPlan lin;
+  size_t t_off = 0, bytes = 0;
 };
 
 LoraGemmPlan plan_lora_gemm(int M, const w4a16_weight_t* w, w4a16_dtype_t xt, const w4a16_lora_t* l) {
   LoraGemmPlan p;
-  p.sh = shrink_shape(M, w->K, l->rank, l->num_adapters, 1);
-  p.gemm_bytes = plan_gemm(M, w, xt).bytes;
+  p.sh = shrink_shape(M, w->K, l->rank);
+  p.lin = plan_linear(M, xt, xt == W4A16_F32, w, nullptr);
   Carve c;
   size_t start;
-  c.take(start, p.gemm_bytes);
-  c.take(p.t_off, t_bytes(l, M, p.sh.splits));
-  c.take(p.base_off, static_cast<size_t>(M) * w->N * 4);
+  c.take(start, p.lin.bytes);
+  c.take(p.t_off, t_bytes(l, M, p.sh));
   p.bytes = c.cursor;
   return p;
 }
 
 struct LoraMlpPlan {
   ShrinkShape sh_gu, sh_d;
-  size_t gemm_bytes = 0, tg_off = 0, tu_off = 0, td_off = 0, g_off = 0, u_off = 0, h_off = 0, bytes = 0;
+  LinearPlan gu, dn;
+  size_t tg_off = 0, tu_off = 0, td_off = 0, h_off = 0, bytes = 0;
 };
 
-LoraMlpPlan plan_lora_mlp(int M, w4a16_dtype_t xt, const w4a16_weight_t* gate, const w4a16_weight_t* down,
-                          const w4a16_lora_t* lg, const w4a16_lora_t* lu, const w4a16_lora_t* ld) {
+LoraMlpPlan plan_lora_mlp(int M, w4a16_dtype_t xt, const w4a16_weight_t* gate, const w4a16_weight_t* up,
+                          const w4a16_weight_t* down, const w4a16_lora_t* lg, const w4a16_lora_t* lu,
+                          const w4a16_lora_t* ld) {
   LoraMlpPlan p;
   const int H = gate->K, I = gate->N;
-  const int rank = std::max(lg ? lg->rank : 1, lu ? lu->rank : 1);
-  const int n = std::max(lg ? lg->num_adapters : 1, lu ? lu->num_adapters : 1);
-  p.sh_gu = shrink_shape(M, H, rank, n, (lg != nullptr) + (lu != nullptr) > 1 ? 2 : 1);
-  if (ld != nullptr) p.sh_d = shrink_shape(M, I, ld->rank, ld->num_adapters, 1);
-  p.gemm_bytes = std::max(plan_gemm(M, gate, xt).bytes, plan_gemm(M, down, W4A16_F32).bytes);
+  p.sh_gu = shrink_shape(M, H, std::max(lg ? lg->rank : 1, lu ? lu->rank : 1));
+  p.sh_d = shrink_shape(M, I, ld ? ld->rank : 1);
+  p.gu = plan_linear(M, xt, xt == W4A16_F32, gate, up);
+  p.dn = plan_linear(M, xt, true, down, nullptr);
   Carve c;
   size_t start;
-  c.take(start, p.gemm_bytes);
-  c.take(p.tg_off, t_bytes(lg, M, p.sh_gu.splits));
-  c.take(p.tu_off, t_bytes(lu, M, p.sh_gu.splits));
-  c.take(p.td_off, t_bytes(ld, M, p.sh_d.splits));
-  c.take(p.g_off, static_cast<size_t>(M) * std::max(I, H) * 4);
-  c.take(p.u_off, static_cast<size_t>(M) * I * 4);
+  c.take(start, std::max(p.gu.bytes, p.dn.bytes));
+  c.take(p.tg_off, t_bytes(lg, M, p.sh_gu));
+  c.take(p.tu_off, t_bytes(lu, M, p.sh_gu));
+  c.take(p.td_off, t_bytes(ld, M, p.sh_d));
   c.take(p.h_off, static_cast<size_t>(M) * I * 4);
   p.bytes = c.cursor;
   return p;
@@ -510,20 +1098,9 @@ extern "C" w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32
   const LoraGemmPlan p = plan_lora_gemm(M, w, xt, lora);
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
-  float* base = reinterpret_cast<float*>(b + p.base_off);
   const LoraSet set = lora_set(lora, reinterpret_cast<float*>(b + p.t_off));
   if ((st = launch_lora_shrink(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, stream)) != W4A16_OK) return st;
-  if ((st = w4a16_gemm(x, xt, M, w, base, ws, p.gemm_bytes, stream)) != W4A16_OK) return st;
-  LoraFinishArgs f{};
-  f.base0 = base;
-  f.s0 = set;
-  f.ids = adapter_ids;
-  f.splits = p.sh.splits;
-  f.M = M;
-  f.N = w->N;
-  f.out = y;
-  f.out_bf16 = yt == W4A16_BF16;
-  return launch_lora_finish(f, stream);
+  return lora_linear(p.lin, x, xt, M, w, nullptr, set, LoraSet{}, adapter_ids, p.sh, y, yt, b, stream);
 }
 
 extern "C" size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_weight_t* gate,
@@ -533,7 +1110,7 @@ extern "C" size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t
   if (M <= 0 || check_mlp(gate, up, down) != W4A16_OK || !known_type(xt)) return 0;
   for (const w4a16_lora_t* l : {lora_gate, lora_up, lora_down})
     if (check_lora(l) != W4A16_OK) return 0;
-  return plan_lora_mlp(M, xt, gate, down, lora_gate, lora_up, lora_down).bytes;
+  return plan_lora_mlp(M, xt, gate, up, down, lora_gate, lora_up, lora_down).bytes;
 }
 
 extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt, int32_t M,
@@ -554,39 +1131,17 @@ extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt,
   if (ranges_overlap(x, static_cast<size_t>(M) * H * dtype_bytes(xt), y,
                      static_cast<size_t>(M) * H * dtype_bytes(yt)))
     return W4A16_ERR_INVALID_ARG;
-  const LoraMlpPlan p = plan_lora_mlp(M, xt, gate, down, lora_gate, lora_up, lora_down);
+  const LoraMlpPlan p = plan_lora_mlp(M, xt, gate, up, down, lora_gate, lora_up, lora_down);
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
-  float* g = reinterpret_cast<float*>(b + p.g_off);
-  float* u = reinterpret_cast<float*>(b + p.u_off);
   float* h = reinterpret_cast<float*>(b + p.h_off);
   const LoraSet gu[2] = {lora_set(lora_gate, reinterpret_cast<float*>(b + p.tg_off)),
                          lora_set(lora_up, reinterpret_cast<float*>(b + p.tu_off))};
   const LoraSet d = lora_set(lora_down, reinterpret_cast<float*>(b + p.td_off));
   if ((st = launch_lora_shrink(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, stream)) != W4A16_OK) return st;
-  if ((st = w4a16_gemm(x, xt, M, gate, g, ws, p.gemm_bytes, stream)) != W4A16_OK) return st;
-  if ((st = w4a16_gemm(x, xt, M, up, u, ws, p.gemm_bytes, stream)) != W4A16_OK) return st;
-  LoraFinishArgs f{};
-  f.base0 = g;
-  f.base1 = u;
-  f.s0 = gu[0];
-  f.s1 = gu[1];
-  f.ids = adapter_ids;
-  f.splits = p.sh_gu.splits;
-  f.M = M;
-  f.N = I;
-  f.out = h;
-  if ((st = launch_lora_finish(f, stream)) != W4A16_OK) return st;
+  if ((st = lora_linear(p.gu, x, xt, M, gate, up, gu[0], gu[1], adapter_ids, p.sh_gu, h, W4A16_F32, b, stream)) !=
+      W4A16_OK)
+    return st;
   if ((st = launch_lora_shrink(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, stream)) != W4A16_OK) return st;
-  if ((st = w4a16_gemm(h, W4A16_F32, M, down, g, ws, p.gemm_bytes, stream)) != W4A16_OK) return st;
-  LoraFinishArgs o{};
-  o.base0 = g;
-  o.s0 = d;
-  o.ids = adapter_ids;
-  o.splits = p.sh_d.splits;
-  o.M = M;
-  o.N = H;
-  o.out = y;
-  o.out_bf16 = yt == W4A16_BF16;
-  return launch_lora_finish(o, stream);
+  return lora_linear(p.dn, h, W4A16_F32, M, down, nullptr, d, LoraSet{}, adapter_ids, p.sh_d, y, yt, b, stream);
 }

@@ -284,27 +284,6 @@ __device__ __forceinline__ MdWindow md_window(int rows, int units, int parts, in
   return w;
 }
 
-// Largest magnitude of eight activations and `mx`, as bits.
-template <int kP>
-__device__ __forceinline__ uint32_t md_max8(const StreamX8<kP>& x, uint32_t mx) {
-  float v[8];
-  stream_x_values<kP>(x, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
-  return mx;
-}
-
-// Eight activations scaled for a row of this largest magnitude, as pieces.
-template <int kP, int kXP>
-__device__ __forceinline__ void md_put(uint4* lds, int unit, const StreamX8<kXP>& x, uint32_t amax) {
-  float v[8];
-  stream_x_values<kXP>(x, v);
-  const float scale = ldexpf(1.0f, stream_exp(__uint_as_float(amax)));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= scale;
-  stream_put<kP>(lds, unit, v);
-}
-
 constexpr int kMdChoiceUnits = static_cast<int>((sizeof(MdChoice) + 15) / 16);
 
 // h of one expert and `cols` blocks of 64 columns.  Wave w takes matrix w & 1
@@ -339,7 +318,7 @@ void md_gate_up_kernel(const MdArgs a) {
   auto row_max = [&](int m, int row) {
     uint32_t mx = 0;
     for (int c = tid; c < nch; c += nt)
-      mx = md_max8<kP>(stream_load_x<kP>(a.x, static_cast<size_t>(row) * a.H + 8 * c), mx);
+      mx = stream_max8<kP>(stream_load_x<kP>(a.x, static_cast<size_t>(row) * a.H + 8 * c), mx);
     mx = wave_max(mx);
     if (lane == 0) atomicMax(&amax[m], mx);
   };
@@ -354,7 +333,7 @@ void md_gate_up_kernel(const MdArgs a) {
       for (int c = tid - kWave; c < all_groups * 4; c += nt - kWave) {
         const int unit = stream_unit(c >> 2, c & 3, m * kP, rshift_all);
         if (c < nch)
-          md_put<kP, kP>(lds, unit, stream_load_x<kP>(a.x, static_cast<size_t>(m) * a.H + 8 * c), amax[m]);
+          stream_put_row<kP, kP>(lds, unit, stream_load_x<kP>(a.x, static_cast<size_t>(m) * a.H + 8 * c), amax[m]);
         else
           stream_put_zero<kP>(lds, unit);
       }
@@ -425,7 +404,7 @@ void md_gate_up_kernel(const MdArgs a) {
           const int gl = u >> 2, gg = p * a.gpp + w0 + gl;
           const int unit = stream_unit(p * win.wing + gl, u & 3, m * kP, win.rshift);
           if (w0 + gl < a.gpp && gg < G)
-            md_put<kP, kP>(lds, unit,
+            stream_put_row<kP, kP>(lds, unit,
                            stream_load_x<kP>(a.x, static_cast<size_t>(token[m]) * a.H + gg * kGroup + 8 * (u & 3)),
                            amax[m]);
           else
@@ -646,7 +625,7 @@ void md_down_kernel(const MdArgs a) {
               h = here_h[1];
             else
               h = load(q, m);
-            md_put<kP, 2>(buf, q.unit + m * kP, h, amax[m]);
+            stream_put_row<kP, 2>(buf, q.unit + m * kP, h, amax[m]);
           } else {
             stream_put_zero<kP>(buf, q.unit + m * kP);
           }

@@ -208,4 +208,25 @@ __device__ __forceinline__ void stream_x_values(const StreamX8<kP>& r, float v[8
   }
 }
 
+// Largest magnitude of eight activations and `mx`, as bits.
+template <int kP>
+__device__ __forceinline__ uint32_t stream_max8(const StreamX8<kP>& x, uint32_t mx) {
+  float v[8];
+  stream_x_values<kP>(x, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+  return mx;
+}
+
+// Eight activations scaled for a row of this largest magnitude, as pieces.
+template <int kP, int kXP>
+__device__ __forceinline__ void stream_put_row(uint4* lds, int unit, const StreamX8<kXP>& x, uint32_t amax) {
+  float v[8];
+  stream_x_values<kXP>(x, v);
+  const float scale = ldexpf(1.0f, stream_exp(__uint_as_float(amax)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
+  stream_put<kP>(lds, unit, v);
+}
+
 }  // namespace w4

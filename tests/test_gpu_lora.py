@@ -10,7 +10,7 @@ import oracle as O
 import workloads as W
 from helpers import rel_err, tol_for, x_for_dtype, x_values
 from lora_bounds import (adapters, codes, device_lora, device_weight, gemm_lora_bound, id_pattern, mlp_lora_bound)
-from oracle_pool import check_elementwise
+from oracle_pool import TAU, check_elementwise, gemm_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -154,10 +154,17 @@ def test_no_adapters_is_the_plain_gemm(M, dtype):
     w, lo = device_weight(codes(K, N, 18)), device_lora(adapters(2, 8, K, N, 19))
     x = _x(M, K, dtype, 20)
     y = _gemm(x, w, lo, torch.full((M,), -1, dtype=torch.int32, device="cuda"), torch.float32)
+    other = device_lora(adapters(5, 24, K, N, 29))
+    assert torch.equal(_gemm(x, w, other, torch.full((M,), 7, dtype=torch.int32, device="cuda"), torch.float32), y)
     base = torch.empty((M, N), device="cuda")
     L.gemm(x, w, base, L.new_workspace(L.gemm_workspace_bytes(M, w, _code(dtype))))
     torch.cuda.synchronize()
-    assert torch.equal(y, base)
+    if M > 16:  # the same tiles
+        assert torch.equal(y, base)
+    else:       # other orders of the same sums
+        qw, sc = codes(K, N, 18)
+        bound = 2 * gemm_bound(x_values(x), qw, sc, TAU[dtype])
+        check_elementwise(y.cpu().numpy(), base.double().cpu().numpy(), bound, "no adapters")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
