@@ -34,20 +34,32 @@ inline LoraSet lora_set(const w4a16_lora_t* l, float* t) {
   return s;
 }
 
-// Launch shape of the first product: by rows (one dot product of one row per
-// workgroup and rank) or by blocks of 64 rows, in K splits.
+// Launch shape of the first product: by rows (a workgroup takes one row and a
+// few ranks) or by blocks of 64 rows, in K splits.
 struct ShrinkShape {
   bool rows = true;
   int splits = 1;
 };
 ShrinkShape shrink_shape(int M, int K, int R);
 
-// t[split][m][r] = scale[id] * sum over the split's k of x[m][k] * a[id][r][k]
-// for the rows m with an adapter id = ids[m] in [0, n) and the ranks r it uses
-// (the other entries are left as they were).  Up to two projections of the
-// same x.
-w4a16_status_t launch_lora_shrink(const void* x, w4a16_dtype_t xt, int M, int K, const int* ids, const LoraSet* sets,
-                                  int n_sets, const ShrinkShape& sh, hipStream_t stream);
+// What a projection needs of x beside t: f16 pieces, each row scaled by a power
+// of two (2^-e to rs), for the streamed product (units [K/32][4][2^rshift] of
+// 16 bytes) or for the tiles ([pieces][rows][K], rows past M zero); rows 0:
+// nothing.
+struct LoraPrep {
+  int pieces, rows;
+  uint4* stream;
+  int rshift;
+  _Float16* tiles;
+  float* rs;
+};
+
+// The pieces, and t[split][m][r] = scale[id] * sum over the split's k of
+// x[m][k] * a[id][r][k] for the rows m with an adapter id = ids[m] in [0, n) and
+// the ranks r it uses (the other entries are left as they were).  Up to two
+// projections of the same x.
+w4a16_status_t launch_lora_head(const void* x, w4a16_dtype_t xt, int M, int K, const int* ids, const LoraSet* sets,
+                                int n_sets, const ShrinkShape& sh, const LoraPrep& prep, hipStream_t stream);
 
 // The base product's sums as a tile launch left them: rs[m] * the sum of S
 // planes (plane_rows x ld), in split order.
@@ -81,8 +93,9 @@ struct LoraStreamPlan {
 };
 LoraStreamPlan plan_lora_stream(int M, int pieces, int N, int mats, int K);
 struct LoraStreamArgs {
-  const void* x;
-  int x_f32, pieces;  // activations float32 or bf16, as 2 or 1 pieces
+  const uint4* xs;  // the prepared rows
+  const float* rs;
+  int pieces;
   int M, K, N;
   const u32x4 *qw0, *qw1;  // qw1: up (SwiGLU), else null
   const float *sc0, *sc1;

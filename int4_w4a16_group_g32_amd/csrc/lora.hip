@@ -112,17 +112,83 @@ struct ShrinkArgs {
   const void* x;
   const int* ids;
   LoraSet s[2];
-  int M, K, splits, chunks;  // chunks: of kLoraChunk ranks, over the larger R
+  int M, K, splits, chunks;  // chunks: of a workgroup's ranks, over the larger R
 };
 
-// t of one row and kQ ranks: the four waves of a workgroup take quarters of K,
-// all of a step's loads in flight together.
-template <int kXP, int kQ>
-__global__ __launch_bounds__(256) void shrink_rows_kernel(const ShrinkArgs a) {
+// The rows of x as f16 pieces for the base product: scaled by one power of two
+// a row (2^-e to rs), in the order codes_f16 expands to.
+struct PrepArgs {
+  int pieces, rows;  // rows: M, or the tiles' padded count (the rest are zeros)
+  uint4* stream;     // units [K/32][4][2^rshift] as stream.h stages them, or
+  int rshift;
+  _Float16* tiles;   // [pieces][rows][K]
+  float* rs;
+};
+
+template <int kXP, int kP>
+__device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p, int m) {
+  constexpr int kHold = 4;  // chunks a thread keeps in registers
+  __shared__ uint32_t amax;
+  const int tid = threadIdx.x, nc = a.K / 8;
+  const size_t xrow = static_cast<size_t>(min(m, a.M - 1)) * a.K;
+  if (tid == 0) amax = 0;
+  StreamX8<kXP> x[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    x[i] = stream_load_x<kXP>(a.x, xrow + 8 * static_cast<size_t>(min(tid + i * 256, nc - 1)));
+  __syncthreads();
+  uint32_t mx = 0;
+  if (m < a.M) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) mx = stream_max8<kXP>(x[i], mx);
+    for (int c = tid + kHold * 256; c < nc; c += 256)
+      mx = stream_max8<kXP>(stream_load_x<kXP>(a.x, xrow + 8 * static_cast<size_t>(c)), mx);
+    mx = wave_max(mx);
+    if (lane_id() == 0) atomicMax(&amax, mx);
+  }
+  __syncthreads();
+  mx = amax;
+  const int e = stream_exp(__uint_as_float(mx));
+  if (tid == 0) p.rs[m] = mx != 0 ? ldexpf(1.0f, -e) : 0.0f;
+  const float scale = mx != 0 ? ldexpf(1.0f, e) : 0.0f;
+  auto put = [&](int c, const StreamX8<kXP>& xc) {
+    float v[8];
+    stream_x_values<kXP>(xc, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = mx != 0 ? v[i] * scale : 0.0f;
+    half8 h[2];
+    stream_pieces<kP>(v, h);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      uint4* o = p.stream != nullptr
+                     ? p.stream + ((static_cast<size_t>(c) << p.rshift) + m * kP + j)
+                     : reinterpret_cast<uint4*>(p.tiles + (static_cast<size_t>(j) * p.rows + m) * a.K + 8 * static_cast<size_t>(c));
+      *o = __builtin_bit_cast(uint4, h[j]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (tid + i * 256 < nc) put(tid + i * 256, x[i]);
+  for (int c = tid + kHold * 256; c < nc; c += 256)
+    put(c, stream_load_x<kXP>(a.x, xrow + 8 * static_cast<size_t>(c)));
+}
+
+// What comes before the base product, in one launch.  The first workgroups
+// each prepare a row; the others take one row and kQ ranks of t, their four
+// waves quarters of K, all of a step's loads in flight together.
+template <int kXP, int kP, int kQ>
+__global__ __launch_bounds__(256) void head_kernel(const ShrinkArgs a, const PrepArgs p) {
+  if (static_cast<int>(blockIdx.x) < p.rows) {
+    prep_row<kXP, kP>(a, p, blockIdx.x);
+    return;
+  }
   __shared__ float red[4][kQ];
-  const LoraSet s = a.s[blockIdx.z];
-  const int m = blockIdx.x, r0 = blockIdx.y * kQ;
-  const int id = s.a != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
+  int b = blockIdx.x - p.rows;
+  const int m = b % a.M;
+  b /= a.M;
+  const int r0 = b % a.chunks * kQ;
+  const LoraSet s = a.s[b / a.chunks];
+  const int id = adapter_of(a.ids, m, a.M, s.n);
   if (id < 0 || r0 >= rank_of(s, id)) return;
   const int wv = wave_id(), lane = lane_id();
   const int nc = a.K / 8, per = (nc + 255) / 256 * 64;  // chunks of 8, per wave
@@ -185,11 +251,11 @@ __device__ __forceinline__ uint4 load_b8(const uint16_t* row, int r, int rank) {
   return v;
 }
 
-// v[i] += t . row i of b (kC rows ld apart), ranks below `rank` in ascending
-// order; 32 ranks' loads in flight together.  t is read up to the next
+// v[i] += t . row i of b (kC of them), ranks below `rank` in ascending order;
+// 32 ranks' loads in flight together.  t is read up to the next
 // multiple of 8.
 template <int kC>
-__device__ __forceinline__ void row_dots(const float* t, const uint16_t* b, int ld, int rank, float v[kC]) {
+__device__ __forceinline__ void row_dots(const float* t, const uint16_t* const b[kC], int rank, float v[kC]) {
   for (int r0 = 0; r0 < rank; r0 += 32) {
     uint4 w[kC][4];
     float4 tv[4][2];
@@ -197,7 +263,7 @@ __device__ __forceinline__ void row_dots(const float* t, const uint16_t* b, int 
     for (int j = 0; j < 4; ++j) {
       const int r = r0 + 8 * j;
 #pragma unroll
-      for (int i = 0; i < kC; ++i) w[i][j] = load_b8(b + static_cast<size_t>(i) * ld, r, rank);
+      for (int i = 0; i < kC; ++i) w[i][j] = load_b8(b[i], r, rank);
       if (r < rank) {
         tv[j][0] = *reinterpret_cast<const float4*>(t + r);
         tv[j][1] = *reinterpret_cast<const float4*>(t + r + 4);
@@ -224,25 +290,39 @@ __device__ __forceinline__ void row_dots(const float* t, const uint16_t* b, int 
 }
 
 constexpr int kFinishThreads = 256;
-constexpr int kFinishSplits = kMaxSplits;
 constexpr int kLoraUnits = 512;  // LDS units (16 bytes) per wave of the streamed product
 
-// Four columns of base: rs * the sum of the planes, in split order, all loads
-// in flight before the sum.
-__device__ __forceinline__ f32x4 base_sum(const LoraBase& b, int m, int n) {
-  const float* p = b.p + static_cast<size_t>(m) * b.ld + n;
-  f32x4 v[kFinishSplits];
+// kC columns of base, 64 apart: rs * the sum of the planes, in split order, 16
+// planes' loads in flight together.
+template <int kC>
+__device__ __forceinline__ void base_sum(const LoraBase& b, int m, int n, int N, float v[kC]) {
+  constexpr int kB = 16;
+  const float* p = b.p + static_cast<size_t>(m) * b.ld;
 #pragma unroll
-  for (int s = 0; s < kFinishSplits; ++s)
-    if (s < b.S) v[s] = *reinterpret_cast<const f32x4*>(p + s * b.split_stride);
-  f32x4 t = v[0];
+  for (int i = 0; i < kC; ++i) v[i] = 0.0f;
+  for (int s0 = 0; s0 < b.S; s0 += kB) {
+    float q[kC][kB];
 #pragma unroll
-  for (int s = 1; s < kFinishSplits; ++s)
-    if (s < b.S) t += v[s];
-  return b.rs != nullptr ? t * b.rs[m] : t;
+    for (int s = 0; s < kB; ++s)
+      if (s0 + s < b.S) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i) q[i][s] = p[(s0 + s) * b.split_stride + min(n + 64 * i, N - 1)];
+      }
+#pragma unroll
+    for (int s = 0; s < kB; ++s)
+      if (s0 + s < b.S) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i) v[i] += q[i][s];
+      }
+  }
+  if (b.rs != nullptr) {
+    const float f = b.rs[m];
+#pragma unroll
+    for (int i = 0; i < kC; ++i) v[i] *= f;
+  }
 }
 
-// The same without room for all planes at once.
+// Four adjacent columns, one plane after another.
 __device__ __forceinline__ f32x4 base_sum_loop(const LoraBase& b, int m, int n) {
   const float* p = b.p + static_cast<size_t>(m) * b.ld + n;
   f32x4 t = *reinterpret_cast<const f32x4*>(p);
@@ -259,33 +339,49 @@ __device__ __forceinline__ void store4(void* out, int bf16, size_t at, f32x4 v) 
     *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
 }
 
-// One row, four columns a thread; the row's t is the workgroup's.
+// One row; a thread takes two columns 64 apart, so that a wave reads adjacent
+// rows of B together.  The row's t is the workgroup's.
+constexpr int kFinishCols = 2;
+
 template <bool kGlu>
 __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(const LoraFinishArgs a) {
   __shared__ __attribute__((aligned(16))) float t[2][kLoraMaxRank];
-  const int m = blockIdx.x, n = (blockIdx.y * kFinishThreads + static_cast<int>(threadIdx.x)) * 4;
+  const int m = blockIdx.x, n = (blockIdx.y * 4 + wave_id()) * 64 * kFinishCols + lane_id();
   int id[2], rank[2];
 #pragma unroll
   for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
     const LoraSet& s = w == 0 ? a.s0 : a.s1;
     id[w] = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
     rank[w] = id[w] >= 0 ? rank_of(s, id[w]) : 0;
-    for (int r = threadIdx.x; r < rank[w]; r += kFinishThreads) t[w][r] = s.t[static_cast<size_t>(m) * s.R + r];
     // (ranks up to the next multiple of 8 are read, and dropped)
+    for (int r = threadIdx.x; r < rank[w]; r += kFinishThreads) t[w][r] = s.t[static_cast<size_t>(m) * s.R + r];
   }
   __syncthreads();
-  if (n >= a.N) return;
-  f32x4 v;
+  float v[kFinishCols];
 #pragma unroll
   for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
     const LoraSet& s = w == 0 ? a.s0 : a.s1;
-    const f32x4 b = base_sum(w == 0 ? a.base0 : a.base1, m, n);
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (rank[w] > 0) row_dots<4>(t[w], s.b + (static_cast<size_t>(id[w]) * a.N + n) * s.R, s.R, rank[w], d);
+    float d[kFinishCols], b[kFinishCols];
+    base_sum<kFinishCols>(w == 0 ? a.base0 : a.base1, m, n, a.N, b);
+    const uint16_t* rows[kFinishCols];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = w == 0 ? b[i] + d[i] : silu(v[i]) * (b[i] + d[i]);
+    for (int i = 0; i < kFinishCols; ++i) {
+      d[i] = 0.0f;
+      rows[i] = s.b + (static_cast<size_t>(max(id[w], 0)) * a.N + min(n + 64 * i, a.N - 1)) * s.R;
+    }
+    if (rank[w] > 0) row_dots<kFinishCols>(t[w], rows, rank[w], d);
+#pragma unroll
+    for (int i = 0; i < kFinishCols; ++i) v[i] = w == 0 ? b[i] + d[i] : silu(v[i]) * (b[i] + d[i]);
   }
-  store4(a.out, a.out_bf16, static_cast<size_t>(m) * a.N + n, v);
+#pragma unroll
+  for (int i = 0; i < kFinishCols; ++i) {
+    if (n + 64 * i >= a.N) continue;
+    const size_t at = static_cast<size_t>(m) * a.N + n + 64 * i;
+    if (a.out_bf16)
+      static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v[i]);
+    else
+      static_cast<float*>(a.out)[at] = v[i];
+  }
 }
 
 // ---------------------------------------------------------------- by blocks: x A^T
@@ -505,27 +601,35 @@ __global__ __launch_bounds__(kFinishThreads) void finish_blocks_kernel(const Lor
 // second product in its epilogue.  A workgroup takes `cols` blocks of 64
 // columns (of gate and the same of up) and one K split; wave w takes matrix w %
 // kMats, one column block and one of the split's K parts (gpp groups each).
-// It stages all rows of its K range, each scaled by a power of two of its own
-// there.  The parts meet in LDS and the splits in memory as in the split-K
-// GEMV (agent-scope stores, an arrival counter, the last workgroup sums in
-// split order); then a thread takes a row and two columns: their sums, their
+// The rows' pieces were prepared by the launch before: staging is a copy.  The
+// parts meet in LDS and the splits in memory as in the split-K GEMV
+// (agent-scope stores, an arrival counter, the last workgroup sums in split
+// order); then a thread takes a row and two columns: their sums, their
 // adapter's dot products and, with gate and up, silu(gate) * up.
-template <int kXP, int kP, int kI, int kMats>
+template <int kP, int kI, int kMats>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4)))
 void lora_stream_kernel(const LoraStreamArgs a) {
-  constexpr int kHold = 4;  // chunks of x a thread keeps in registers
   extern __shared__ uint4 lds[];
-  __shared__ uint32_t amax[kStreamRows];
   __shared__ int last;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int wv = wave_id(), lane = lane_id();
-  const int lc = lane & 15, kb = lane >> 4;
   const int cshift = __builtin_ctz(a.cols);
   const int mat = kMats == 2 ? wv & 1 : 0, col = (wv / kMats) & (a.cols - 1), part = (wv / kMats) >> cshift;
   const int G = a.K / kGroup, groups = a.parts * a.gpp, g_wg = split * groups;
   const int block = tile * a.cols + col;
   const bool wave_ok = block * 64 < a.N;
+  const int rshift = stream_rshift<kP>(a.M);
+
+  // the window's units of this K range, ahead of the weights; groups past the
+  // last are zeros
+  const int units = (groups * 4) << rshift, held = min(units, (G - g_wg) * 4 << rshift);
+  const uint4* xs = a.xs + ((static_cast<size_t>(g_wg) * 4) << rshift);
+  constexpr int kAhead = 4;
+  uint4 xa[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) xa[i] = xs[min(tid + i * nt, held - 1)];
+  __builtin_amdgcn_sched_barrier(0);
 
   // the ring: a wave past the last column streams column block 0 and stores
   // nothing, a part past the last group the last one (against staged zeros)
@@ -540,58 +644,16 @@ void lora_stream_kernel(const LoraStreamArgs a) {
     g = min(g + 1, g_last);
   };
   StreamCodes ring[kStreamRing];
-
-  // Staging: 2^k threads a row, chunks of 8 values (k block c & 3 of group c >> 2).
-  const int rshift = stream_rshift<kP>(a.M);
-  const int tshift = 31 - __builtin_clz(nt) - stream_rshift<1>(a.M);  // log2 of a row's threads
-  const int row = tid >> tshift, c0 = tid & ((1 << tshift) - 1), cstep = 1 << tshift;
-  const int chunks = groups * 4, held = min(chunks, max(0, (G - g_wg) * 4));  // (chunks of K in range)
-  const size_t x0 = static_cast<size_t>(min(row, a.M - 1)) * a.K + static_cast<size_t>(g_wg) * kGroup;
-  if (tid < kStreamLds0) lds[tid] = make_uint4(0, 0, 0, 0);
-  if (tid < kStreamRows) amax[tid] = 0;
-  StreamX8<kXP> xh[kHold];
-#pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    xh[i] = stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(max(0, min(c0 + i * cstep, held - 1))));
-  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int j = 0; j < kStreamRing; ++j) next(ring[j]);
-  __syncthreads();
-  uint32_t mx = 0;
+  if (tid < kStreamLds0) lds[tid] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (c0 + i * cstep < held) mx = stream_max8<kXP>(xh[i], mx);
-  for (int c = c0 + kHold * cstep; c < held; c += cstep)
-    mx = stream_max8<kXP>(stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(c)), mx);
-  if (tshift >= 6) {  // a wave's lanes belong to one row
-    mx = wave_max(mx);
-    if (lane == 0 && row < a.M) atomicMax(&amax[row], mx);
-  } else if (row < a.M) {
-    atomicMax(&amax[row], mx);
+  for (int i = 0; i < kAhead; ++i) {
+    const int u = tid + i * nt;
+    if (u < units) lds[kStreamLds0 + u] = u < held ? xa[i] : make_uint4(0, 0, 0, 0);
   }
-  __syncthreads();
-  if (row < a.M) {
-    const uint32_t am = amax[row];
-    for (int i = 0, c = c0; c < chunks; ++i, c += cstep) {
-      const int unit = stream_unit(c >> 2, c & 3, row * kP, rshift);
-      if (c >= held) {
-        stream_put_zero<kP>(lds, unit);
-        continue;
-      }
-      StreamX8<kXP> v;
-      if (i == 0)
-        v = xh[0];
-      else if (i == 1)
-        v = xh[1];
-      else if (i == 2)
-        v = xh[2];
-      else if (i == 3)
-        v = xh[3];
-      else
-        v = stream_load_x<kXP>(a.x, x0 + 8 * static_cast<size_t>(c));
-      stream_put_row<kP, kXP>(lds, unit, v, am);
-    }
-  }
+  for (int u = tid + kAhead * nt; u < units; u += nt)
+    lds[kStreamLds0 + u] = u < held ? xs[u] : make_uint4(0, 0, 0, 0);
   __syncthreads();
 
   float acc[4][kI];
@@ -600,52 +662,38 @@ void lora_stream_kernel(const LoraStreamArgs a) {
 #pragma unroll
     for (int i = 0; i < kI; ++i) acc[cb][i] = 0.0f;
   stream_run<kP, kI>(lds, stream_frag<kP>(lane, a.M, part * a.gpp, rshift), a.gpp, magic_vgpr(), ring, next, acc);
-#pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    const int m = kb + 4 * i;
-    const float f = m < a.M ? ldexpf(1.0f, -stream_exp(__uint_as_float(amax[m]))) : 0.0f;
-#pragma unroll
-    for (int cb = 0; cb < 4; ++cb) acc[cb][i] *= f;
-  }
-  // the parts' sums, in order
+
+  // The parts' sums, in order: each thread adds some of the tile's [i][mat,
+  // col][lane] places over the parts.
   f32x4* red = reinterpret_cast<f32x4*>(lds);
-  const int pw = kMats << cshift;  // waves of a part
-  __syncthreads();  // the window is free
-  if (part > 0) {
+  const int pshift = cshift + kMats - 1;  // log2 of a part's waves
+  __syncthreads();                        // the window is free
 #pragma unroll
-    for (int i = 0; i < kI; ++i)
-      red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-  }
+  for (int i = 0; i < kI; ++i)
+    red[(wv * kI + i) * kWave + lane] = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
   __syncthreads();
   // the tile's sums [mat][row][64 cols]: in LDS behind the parts', or the split's in memory
   const int ld = 64 << cshift;
   float* sums = reinterpret_cast<float*>(lds + (nt / kWave) * 256);
   float* base = a.partials + static_cast<size_t>(tile) * a.splits * kMats * a.M * ld;
   const size_t ps = static_cast<size_t>(kMats) * a.M * ld;
-  if (part == 0) {
-    for (int p = 1; p < a.parts; ++p)
+  for (int q = tid; q < (kI * kWave) << pshift; q += nt) {
+    const int l = q & 63, i = (q >> 6) & (kI - 1), w = (q >> 6) / kI;  // lane, row group, wave of a part
+    const int m = (l >> 4) + 4 * i;
+    if (m >= a.M) continue;
+    f32x4 v = red[(w * kI + i) * kWave + l];
+#pragma unroll 4
+    for (int p = 1; p < a.parts; ++p) v += red[(((p << pshift) + w) * kI + i) * kWave + l];
+    v *= a.rs[m];
+    const size_t at = (static_cast<size_t>(kMats == 2 ? w & 1 : 0) * a.M + m) * ld + (w / kMats) * 64 + 4 * (l & 15);
+    if (a.splits == 1) {
+      *reinterpret_cast<f32x4*>(sums + at) = v;
+    } else {
+      uint64_t* o = reinterpret_cast<uint64_t*>(base + split * ps + at);
 #pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const f32x4 v = red[((p * pw + wv) * kI + i) * kWave + lane];
-#pragma unroll
-        for (int cb = 0; cb < 4; ++cb) acc[cb][i] += v[cb];
-      }
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const int m = kb + 4 * i;
-      if (m >= a.M) continue;
-      const size_t at = (static_cast<size_t>(mat) * a.M + m) * ld + col * 64 + 4 * lc;
-      if (a.splits == 1) {
-        *reinterpret_cast<f32x4*>(sums + at) = f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-      } else {
-        uint64_t* o = reinterpret_cast<uint64_t*>(base + split * ps + at);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          __hip_atomic_store(o + j,
-                             static_cast<uint64_t>(__float_as_uint(acc[2 * j + 1][i])) << 32 |
-                                 __float_as_uint(acc[2 * j][i]),
-                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      for (int j = 0; j < 2; ++j)
+        __hip_atomic_store(o + j, static_cast<uint64_t>(__float_as_uint(v[2 * j + 1])) << 32 | __float_as_uint(v[2 * j]),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
   if (a.splits > 1) {
@@ -659,9 +707,9 @@ void lora_stream_kernel(const LoraStreamArgs a) {
   } else {
     __syncthreads();
   }
-  const int pshift = 5 + cshift;  // pairs of columns of a row: 2^pshift
-  for (int q = tid; q < a.M << pshift; q += nt) {
-    const int m = q >> pshift, c = 2 * (q - (m << pshift)), n = tile * ld + c;
+  const int nshift = 5 + cshift;  // pairs of columns of a row: 2^nshift
+  for (int q = tid; q < a.M << nshift; q += nt) {
+    const int m = q >> nshift, c = 2 * (q - (m << nshift)), n = tile * ld + c;
     if (n >= a.N) continue;
     float v[kMats][2];
 #pragma unroll
@@ -687,11 +735,16 @@ void lora_stream_kernel(const LoraStreamArgs a) {
             }
         }
       }
+    }
+#pragma unroll
+    for (int w = 0; w < kMats; ++w) {
       const LoraSet& s = w == 0 ? a.s0 : a.s1;
       const int id = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
-      if (id >= 0)
-        row_dots<2>(s.t + static_cast<size_t>(m) * s.R, s.b + (static_cast<size_t>(id) * a.N + n) * s.R, s.R,
-                    rank_of(s, id), v[w]);
+      if (id >= 0) {
+        const uint16_t* b = s.b + (static_cast<size_t>(id) * a.N + n) * s.R;
+        const uint16_t* rows[2] = {b, b + s.R};
+        row_dots<2>(s.t + static_cast<size_t>(m) * s.R, rows, rank_of(s, id), v[w]);
+      }
     }
     if (kMats == 2) {
 #pragma unroll
@@ -706,14 +759,14 @@ void lora_stream_kernel(const LoraStreamArgs a) {
   }
 }
 
-template <int kXP, int kP, int kMats>
+template <int kP, int kMats>
 void launch_stream_mats(const LoraStreamArgs& a, dim3 grid, dim3 threads, size_t lds, hipStream_t stream) {
   if (a.M <= 4)
-    lora_stream_kernel<kXP, kP, 1, kMats><<<grid, threads, lds, stream>>>(a);
+    lora_stream_kernel<kP, 1, kMats><<<grid, threads, lds, stream>>>(a);
   else if (a.M <= 8 || kP == 2)
-    lora_stream_kernel<kXP, kP, 2, kMats><<<grid, threads, lds, stream>>>(a);
+    lora_stream_kernel<kP, 2, kMats><<<grid, threads, lds, stream>>>(a);
   else
-    lora_stream_kernel<kXP, kP, 4 / kP, kMats><<<grid, threads, lds, stream>>>(a);
+    lora_stream_kernel<kP, 4 / kP, kMats><<<grid, threads, lds, stream>>>(a);
 }
 
 // Ranks a workgroup of the row kernel takes: one, until there are workgroups
@@ -733,16 +786,14 @@ void launch_shrink_blocks(const ShrinkArgs& a, int cb, dim3 grid, hipStream_t st
     shrink_blocks_kernel<kXP, 4><<<grid, kShrinkThreads, 0, stream>>>(a);
 }
 
-template <int kXP>
-void launch_shrink_rows(const ShrinkArgs& a, int R, int n_sets, hipStream_t stream) {
-  const int q = shrink_quota(static_cast<size_t>(a.M) * R * n_sets);
-  const dim3 grid(a.M, (R + q - 1) / q, n_sets);
+template <int kXP, int kP>
+void launch_head_q(const ShrinkArgs& a, const PrepArgs& p, int q, unsigned blocks, hipStream_t stream) {
   if (q == 4)
-    shrink_rows_kernel<kXP, 4><<<grid, 256, 0, stream>>>(a);
+    head_kernel<kXP, kP, 4><<<blocks, 256, 0, stream>>>(a, p);
   else if (q == 2)
-    shrink_rows_kernel<kXP, 2><<<grid, 256, 0, stream>>>(a);
+    head_kernel<kXP, kP, 2><<<blocks, 256, 0, stream>>>(a, p);
   else
-    shrink_rows_kernel<kXP, 1><<<grid, 256, 0, stream>>>(a);
+    head_kernel<kXP, kP, 1><<<blocks, 256, 0, stream>>>(a, p);
 }
 
 }  // namespace
@@ -757,29 +808,57 @@ ShrinkShape shrink_shape(int M, int K, int R) {
   return sh;
 }
 
-w4a16_status_t launch_lora_shrink(const void* x, w4a16_dtype_t xt, int M, int K, const int* ids, const LoraSet* sets,
-                                  int n_sets, const ShrinkShape& sh, hipStream_t stream) {
-  int R = 0;
+// The sets that are there, and the largest of their ranks.
+static int live_sets(const LoraSet* sets, int n_sets, ShrinkArgs& a, int& R) {
+  int n = 0;
+  R = 0;
+  for (int i = 0; i < n_sets; ++i)
+    if (sets[i].a != nullptr) {
+      a.s[n++] = sets[i];
+      R = std::max(R, sets[i].R);
+    }
+  return n;
+}
+
+w4a16_status_t launch_lora_head(const void* x, w4a16_dtype_t xt, int M, int K, const int* ids, const LoraSet* sets,
+                                int n_sets, const ShrinkShape& sh, const LoraPrep& prep, hipStream_t stream) {
   ShrinkArgs a{};
   a.x = x;
   a.ids = ids;
   a.M = M;
   a.K = K;
   a.splits = sh.splits;
-  int n = 0;
-  for (int i = 0; i < n_sets; ++i)
-    if (sets[i].a != nullptr) {
-      a.s[n++] = sets[i];
-      R = std::max(R, sets[i].R);
-    }
-  if (n == 0 || M == 0) return W4A16_OK;
+  int R;
+  const int n = live_sets(sets, n_sets, a, R);
+  if (M == 0) return W4A16_OK;
   if (sh.rows) {
+    PrepArgs p{};
+    p.pieces = prep.pieces;
+    p.rows = prep.rows;
+    p.stream = prep.stream;
+    p.rshift = prep.rshift;
+    p.tiles = prep.tiles;
+    p.rs = prep.rs;
+    const int q = shrink_quota(static_cast<size_t>(M) * R * n);
+    a.chunks = std::max(1, (R + q - 1) / q);
+    const size_t blocks = static_cast<size_t>(p.rows) + static_cast<size_t>(n) * a.chunks * M;
+    if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+    const unsigned g = static_cast<unsigned>(blocks);
+    if (g == 0) return W4A16_OK;
     if (xt == W4A16_BF16)
-      launch_shrink_rows<1>(a, R, n, stream);
+      launch_head_q<1, 1>(a, p, q, g, stream);
+    else if (p.pieces == 2)
+      launch_head_q<2, 2>(a, p, q, g, stream);
     else
-      launch_shrink_rows<2>(a, R, n, stream);
+      launch_head_q<2, 1>(a, p, q, g, stream);  // h of a bf16 layer
     return launch_status();
   }
+  if (prep.rows > 0) {
+    const w4a16_status_t st = launch_mfma_prep(x, xt, M, prep.rows, K, prep.pieces, nullptr, 0, nullptr, prep.tiles,
+                                               prep.rs, stream);
+    if (st != W4A16_OK) return st;
+  }
+  if (n == 0) return W4A16_OK;
   const int cb = shrink_cols(R);
   a.chunks = (R + 16 * cb - 1) / (16 * cb);
   const size_t blocks = (static_cast<size_t>(M) + 63) / 64 * a.chunks * a.splits;
@@ -794,10 +873,10 @@ w4a16_status_t launch_lora_shrink(const void* x, w4a16_dtype_t xt, int M, int K,
 
 w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return W4A16_OK;
-  if (a.base0.S > kFinishSplits || a.base1.S > kFinishSplits) return W4A16_ERR_UNSUPPORTED;
   const bool glu = a.base1.p != nullptr;
   if (a.rows) {
-    const dim3 grid(a.M, (a.N + 4 * kFinishThreads - 1) / (4 * kFinishThreads));
+    const int cols = kFinishThreads * kFinishCols;
+    const dim3 grid(a.M, (a.N + cols - 1) / cols);
     if (glu)
       finish_rows_kernel<true><<<grid, kFinishThreads, 0, stream>>>(a);
     else
@@ -822,9 +901,14 @@ w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
 }
 
 // Picks waves, column blocks, K parts and splits by an estimate of the launch's
-// time: the weights at 6.5 TB/s or, with few groups in flight, 0.35 us a group
-// of a wave; 2.5 us for staging and start; 2.5 us for splits to meet, and 0.1
-// us for each.
+// time, fitted to a sweep of all of them over eight shapes (1 to 16 rows, 256 x
+// 512 to 18432 x 7168): the weights of the fullest CU at 6 TB/s among the CUs
+// at work, at most 33 GB/s each, and at least 0.35 us a group of a wave; a
+// start that grows with the workgroup; the splits' meeting.  It finds about
+// one workgroup of 8 waves per CU, within 5 % of the best of the sweep: four
+// float32 rows through 18432 x 7168 take 19.3 us (4.3 TB/s; 21.4 us with 16
+// waves, 23 us with 4), sixteen bf16 rows through 7168 x 4096 11.3 us (14.2 us
+// with half the CUs).
 LoraStreamPlan plan_lora_stream(int M, int pieces, int N, int mats, int K) {
   LoraStreamPlan best;
   const int G = K / kGroup, blocks = N / 64;
@@ -839,11 +923,11 @@ LoraStreamPlan plan_lora_stream(int M, int pieces, int N, int mats, int K) {
         if (splits > 1 && (splits - 1) * parts * gpp >= G) break;  // an empty split
         if (((parts * gpp * 4) << rshift) > waves * kLoraUnits) continue;  // the window
         if (splits > 1 && tiles * sizeof(int) > kCounterBytes) continue;
-        const double wgs = static_cast<double>(tiles) * splits, room = 256.0 * (16 / waves);
-        const double rounds = std::ceil(wgs / room);
-        const double bytes = wgs * waves * gpp * 1280.0;
-        const double us = std::max(bytes / 6.5e6, rounds * gpp * 0.35) + rounds * 2.5 +
-                          (splits > 1 ? 2.5 + 0.1 * splits : 0.0);
+        const double wgs = static_cast<double>(tiles) * splits, cus = std::min(wgs, 256.0);
+        const double per_cu = std::ceil(wgs / 256.0);
+        const double rate = std::min(6.0e6 / cus, 33e3);  // bytes per us of a CU
+        const double us = std::max(per_cu * waves * gpp * 1280.0 / rate, gpp * 0.35) + 4.0 + 0.1 * waves +
+                          0.3 * (per_cu - 1.0) + (splits > 1 ? 1.0 + 0.15 * splits : 0.0);
         if (us < best_us) {
           best_us = us;
           best.ok = true;
@@ -872,18 +956,14 @@ w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hip
   const dim3 grid(static_cast<unsigned>(blocks)), threads(p.waves * kWave);
   const size_t lds = (static_cast<size_t>(p.waves) * kLoraUnits + kStreamLds0) * 16;
   const bool glu = a.qw1 != nullptr;
-  if (a.x_f32 && a.pieces == 2) {
-    if (glu)
-      launch_stream_mats<2, 2, 2>(a, grid, threads, lds, stream);
-    else
-      launch_stream_mats<2, 2, 1>(a, grid, threads, lds, stream);
-  } else if (a.x_f32) {
-    launch_stream_mats<2, 1, 1>(a, grid, threads, lds, stream);  // h of a bf16 layer
-  } else if (glu) {
-    launch_stream_mats<1, 1, 2>(a, grid, threads, lds, stream);
-  } else {
-    launch_stream_mats<1, 1, 1>(a, grid, threads, lds, stream);
-  }
+  if (a.pieces == 2 && glu)
+    launch_stream_mats<2, 2>(a, grid, threads, lds, stream);
+  else if (a.pieces == 2)
+    launch_stream_mats<2, 1>(a, grid, threads, lds, stream);
+  else if (glu)
+    launch_stream_mats<1, 2>(a, grid, threads, lds, stream);
+  else
+    launch_stream_mats<1, 1>(a, grid, threads, lds, stream);
   return launch_status();
 }
 
@@ -910,7 +990,7 @@ size_t t_bytes(const w4a16_lora_t* l, int M, const ShrinkShape& sh) {
 // the tiles' split sums, or their output, are finished.
 struct LinearPlan {
   bool stream = false, pair = false;  // pair: gate and up as two plain products
-  int pieces = 1;
+  int pieces = 1, rshift = 0;
   LoraStreamPlan st;
   MfmaPlan mf;
   size_t ap_off = 0, rs_off = 0, partials_off = 0, base0_off = 0, base1_off = 0;
@@ -930,7 +1010,11 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
     p.stream = p.st.ok;  // (else K is too long for the windows of 32 splits)
   }
   if (p.stream) {
+    p.rshift = p.pieces - 1;
+    while ((1 << (p.rshift - p.pieces + 1)) < M) ++p.rshift;
     c.take(p.partials_off, p.st.partial_bytes);
+    c.take(p.ap_off, (static_cast<size_t>(K / 8) << p.rshift) * 16);
+    c.take(p.rs_off, static_cast<size_t>(M) * 4);
     p.bytes = c.cursor;
     return p;
   }
@@ -953,14 +1037,31 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
   return p;
 }
 
+// What the launch before a projection prepares for it.
+LoraPrep linear_prep(const LinearPlan& p, int M, char* ws) {
+  LoraPrep r{};
+  if (p.pair) return r;  // (w4a16_gemm prepares its own)
+  r.pieces = p.pieces;
+  r.rs = reinterpret_cast<float*>(ws + p.rs_off);
+  if (p.stream) {
+    r.rows = M;
+    r.stream = reinterpret_cast<uint4*>(ws + p.ap_off);
+    r.rshift = p.rshift;
+  } else {
+    r.rows = p.mf.Mp;
+    r.tiles = reinterpret_cast<_Float16*>(ws + p.ap_off);
+  }
+  return r;
+}
+
 w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt, int M, const w4a16_weight_t* w0,
                            const w4a16_weight_t* w1, const LoraSet& s0, const LoraSet& s1, const int* ids,
                            const ShrinkShape& sh, void* out, w4a16_dtype_t ot, char* ws, hipStream_t stream) {
   const int K = w0->K, N = w0->N;
   if (p.stream) {
     LoraStreamArgs a{};
-    a.x = x;
-    a.x_f32 = xt == W4A16_F32;
+    a.xs = reinterpret_cast<const uint4*>(ws + p.ap_off);
+    a.rs = reinterpret_cast<const float*>(ws + p.rs_off);
     a.pieces = p.pieces;
     a.M = M;
     a.K = K;
@@ -1004,8 +1105,6 @@ w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt,
   }
   _Float16* ap = reinterpret_cast<_Float16*>(ws + p.ap_off);
   float* rs = reinterpret_cast<float*>(ws + p.rs_off);
-  st = launch_mfma_prep(x, xt, M, p.mf.Mp, K, p.mf.P, nullptr, 0, nullptr, ap, rs, stream);
-  if (st != W4A16_OK) return st;
   MfmaArgs a = mfma_dense_args(p.mf, M, w0, w1, w1 != nullptr ? 1 : 0, ap, rs, ws, p.partials_off, 0);
   if (p.mf.wide || p.mf.S == 1) {
     a.out = base0;
@@ -1099,7 +1198,8 @@ extern "C" w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
   const LoraSet set = lora_set(lora, reinterpret_cast<float*>(b + p.t_off));
-  if ((st = launch_lora_shrink(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, stream)) != W4A16_OK) return st;
+  st = launch_lora_head(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, linear_prep(p.lin, M, b), stream);
+  if (st != W4A16_OK) return st;
   return lora_linear(p.lin, x, xt, M, w, nullptr, set, LoraSet{}, adapter_ids, p.sh, y, yt, b, stream);
 }
 
@@ -1138,10 +1238,12 @@ extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt,
   const LoraSet gu[2] = {lora_set(lora_gate, reinterpret_cast<float*>(b + p.tg_off)),
                          lora_set(lora_up, reinterpret_cast<float*>(b + p.tu_off))};
   const LoraSet d = lora_set(lora_down, reinterpret_cast<float*>(b + p.td_off));
-  if ((st = launch_lora_shrink(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, stream)) != W4A16_OK) return st;
+  st = launch_lora_head(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, linear_prep(p.gu, M, b), stream);
+  if (st != W4A16_OK) return st;
   if ((st = lora_linear(p.gu, x, xt, M, gate, up, gu[0], gu[1], adapter_ids, p.sh_gu, h, W4A16_F32, b, stream)) !=
       W4A16_OK)
     return st;
-  if ((st = launch_lora_shrink(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, stream)) != W4A16_OK) return st;
+  st = launch_lora_head(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, linear_prep(p.dn, M, b), stream);
+  if (st != W4A16_OK) return st;
   return lora_linear(p.dn, h, W4A16_F32, M, down, nullptr, d, LoraSet{}, adapter_ids, p.sh_d, y, yt, b, stream);
 }

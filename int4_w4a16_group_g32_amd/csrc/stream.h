@@ -79,19 +79,25 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
 
-// Eight values (already scaled) as pieces: units u and, of two pieces, u + 1.
+// Eight values (already scaled) as pieces, in the order codes_f16 expands to.
 template <int kP>
-__device__ __forceinline__ void stream_put(uint4* lds, int u, const float v[8]) {
-  half8 p0, p1;
+__device__ __forceinline__ void stream_pieces(const float v[8], half8 p[2]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = v[kCodeOrder[i]];
     const _Float16 h = static_cast<_Float16>(t);
-    p0[i] = h;
-    if (kP == 2) p1[i] = static_cast<_Float16>(t - static_cast<float>(h));
+    p[0][i] = h;
+    if (kP == 2) p[1][i] = static_cast<_Float16>(t - static_cast<float>(h));
   }
-  *reinterpret_cast<half8*>(lds + u) = p0;
-  if (kP == 2) *reinterpret_cast<half8*>(lds + u + 1) = p1;
+}
+
+// The pieces to units u and, of two pieces, u + 1.
+template <int kP>
+__device__ __forceinline__ void stream_put(uint4* lds, int u, const float v[8]) {
+  half8 p[2];
+  stream_pieces<kP>(v, p);
+#pragma unroll
+  for (int j = 0; j < kP; ++j) *reinterpret_cast<half8*>(lds + u + j) = p[j];
 }
 template <int kP>
 __device__ __forceinline__ void stream_put_zero(uint4* lds, int u) {
