@@ -113,7 +113,27 @@ struct ShrinkArgs {
   const int* ids;
   LoraSet s[2];
   int M, K, splits, chunks;  // chunks: of a workgroup's ranks, over the larger R
+  int sets;
+  int slots;  // by blocks: workgroups that share the adapters of 64 rows
 };
+
+constexpr int kMaxShrinkSplits = 8;
+// Runs of rows seldom end more than three times in 64 rows; 2048 rows of 8
+// adapters in runs, K 7168, rank 64: 34 us with one slot, 29 with two, 23 with four.
+constexpr int kShrinkSlots = 4;
+constexpr int kXcds = 8;  // the hardware deals workgroup b to XCD b % 8
+
+// Workgroup b of a grid over (row, part): the parts go round the XCDs, and all
+// rows of a part to one, whose L2 then holds what the rows of an adapter share.
+__device__ __forceinline__ bool xcd_place(int b, int rows, int parts, int& row, int& part) {
+  const int r = b / kXcds;
+  row = r % rows;
+  part = r / rows * kXcds + b % kXcds;
+  return part < parts;
+}
+inline size_t xcd_blocks(int rows, int parts) {
+  return static_cast<size_t>((parts + kXcds - 1) / kXcds * kXcds) * rows;
+}
 
 // The rows of x as f16 pieces for the base product: scaled by one power of two
 // a row (2^-e to rs), in the order codes_f16 expands to.
@@ -183,11 +203,10 @@ __global__ __launch_bounds__(256) void head_kernel(const ShrinkArgs a, const Pre
     return;
   }
   __shared__ float red[4][kQ];
-  int b = blockIdx.x - p.rows;
-  const int m = b % a.M;
-  b /= a.M;
-  const int r0 = b % a.chunks * kQ;
-  const LoraSet s = a.s[b / a.chunks];
+  int m, c;
+  if (!xcd_place(blockIdx.x - p.rows, a.M, a.chunks * a.sets, m, c)) return;
+  const int r0 = c % a.chunks * kQ;
+  const LoraSet s = a.s[c / a.chunks];
   const int id = adapter_of(a.ids, m, a.M, s.n);
   if (id < 0 || r0 >= rank_of(s, id)) return;
   const int wv = wave_id(), lane = lane_id();
@@ -322,21 +341,20 @@ __device__ __forceinline__ void base_sum(const LoraBase& b, int m, int n, int N,
   }
 }
 
-// Four adjacent columns, one plane after another.
-__device__ __forceinline__ f32x4 base_sum_loop(const LoraBase& b, int m, int n) {
-  const float* p = b.p + static_cast<size_t>(m) * b.ld + n;
-  f32x4 t = *reinterpret_cast<const f32x4*>(p);
-  for (int s = 1; s < b.S; ++s) t += *reinterpret_cast<const f32x4*>(p + s * b.split_stride);
-  return b.rs != nullptr ? t * b.rs[m] : t;
-}
-
-__device__ __forceinline__ void store4(void* out, int bf16, size_t at, f32x4 v) {
-  if (bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-        make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
-                   f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
-  else
+// Eight adjacent columns.
+__device__ __forceinline__ void store8(void* out, int bf16, size_t at, f32x4 v, f32x4 w) {
+  if (bf16) {
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      d[i] = f32_to_bf16(v[2 * i]) | static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16;
+      d[2 + i] = f32_to_bf16(w[2 * i]) | static_cast<uint32_t>(f32_to_bf16(w[2 * i + 1])) << 16;
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(d[0], d[1], d[2], d[3]);
+  } else {
     *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at + 4) = w;
+  }
 }
 
 // One row; a thread takes two columns 64 apart, so that a wave reads adjacent
@@ -346,7 +364,10 @@ constexpr int kFinishCols = 2;
 template <bool kGlu>
 __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(const LoraFinishArgs a) {
   __shared__ __attribute__((aligned(16))) float t[2][kLoraMaxRank];
-  const int m = blockIdx.x, n = (blockIdx.y * 4 + wave_id()) * 64 * kFinishCols + lane_id();
+  int m, part;
+  if (!xcd_place(blockIdx.x, a.M, (a.N + kFinishThreads * kFinishCols - 1) / (kFinishThreads * kFinishCols), m, part))
+    return;
+  const int n = (part * 4 + wave_id()) * 64 * kFinishCols + lane_id();
   int id[2], rank[2];
 #pragma unroll
   for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
@@ -390,16 +411,21 @@ constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWaves = kShrinkThreads / kWave;
 
 // One workgroup: 64 rows, one chunk of 16 kCB ranks, one K split, one
-// projection.  The four waves take quarters of the split's K and meet in LDS.
+// projection, every slots-th adapter of those rows.  The four waves take
+// quarters of the split's K and meet in LDS.
 template <int kXP, int kCB>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_blocks_kernel(const ShrinkArgs a) {
-  constexpr int kRB = 4, kU = 2;
+  constexpr int kRB = 4, kU = kXP == 1 ? 4 : 2;  // k steps in flight
   __shared__ float red[kShrinkWaves][kRB * kLoraRows][kCB * 16];
   int b = blockIdx.x;
   const int split = b % a.splits;
   b /= a.splits;
   const int chunk = b % a.chunks;
-  const int block = b / a.chunks;
+  b /= a.chunks;
+  // (slots outermost: neighbouring workgroups, which go to different CUs, have
+  // work; those of the last slots mostly leave at once)
+  const int blocks = (a.M + kRB * kLoraRows - 1) / (kRB * kLoraRows);
+  const int block = b % blocks, slot = b / blocks;
   const LoraSet s = a.s[blockIdx.y];
   const int r0 = chunk * 16 * kCB;
   if (s.a == nullptr || r0 >= s.R) return;
@@ -419,10 +445,11 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_blocks_kernel(const Shr
              (static_cast<size_t>(min(m0 + rb * kLoraRows + lc, a.M - 1)) * a.K + 8 * kb) * (kXP == 1 ? 2 : 4);
 
   uint64_t todo = __ballot(mine >= 0);
-  while (todo != 0) {
+  for (int turn = 0; todo != 0; turn = turn + 1 == a.slots ? 0 : turn + 1) {
     const int id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
     const uint64_t rows = __ballot(mine == id);
     todo &= ~rows;
+    if (turn != slot) continue;
     f32x4 acc[kRB][kCB];
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
@@ -490,24 +517,32 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_blocks_kernel(const Shr
 
 // ---------------------------------------------------------------- by blocks: t B^T
 
-// t of 16 rows and one chunk of ranks as bf16 pieces in LDS; rows are padded
+// t of 16 kRB rows and one chunk of ranks as bf16 pieces in LDS; rows are padded
 // so that the 16 rows of one fragment read spread over the banks.
 constexpr int kTPad = kLoraChunk + 8;
+template <int kRB>
 struct TPieces {
-  uint16_t p[3][kLoraRows][kTPad];
+  uint16_t p[3][kRB * kLoraRows][kTPad];
 };
 
-// Summed splits of the rows m0 .. m0 + 15, ranks r0 .. r0 + 63, as pieces.
-// Ranks the row's adapter does not use, and rows without one, are zero.
-__device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M, int m0, int r0, int splits,
-                                        int tid, int nthreads, TPieces& tp) {
-  for (int e = tid; e < kLoraRows * kLoraChunk; e += nthreads) {
+// Summed splits of the rows from m0 on, ranks r0 .. r0 + 63, as pieces.  Ranks
+// the row's adapter does not use, and rows without one, are zero.
+template <int kRB>
+__device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M, int m0, int r0, int splits, int tid,
+                                        int nthreads, TPieces<kRB>& tp) {
+  for (int e = tid; e < kRB * kLoraRows * kLoraChunk; e += nthreads) {
     const int m = e / kLoraChunk, r = e % kLoraChunk;
     const int id = adapter_of(ids, m0 + m, M, s.n);
     float v = 0.0f;
     if (id >= 0 && r0 + r < rank_of(s, id)) {
       const float* t = s.t + static_cast<size_t>(m0 + m) * s.R + r0 + r;
-      for (int i = 0; i < splits; ++i) v += t[static_cast<size_t>(i) * M * s.R];
+      float q[kMaxShrinkSplits];
+#pragma unroll
+      for (int i = 0; i < kMaxShrinkSplits; ++i)
+        if (i < splits) q[i] = t[static_cast<size_t>(i) * M * s.R];
+#pragma unroll
+      for (int i = 0; i < kMaxShrinkSplits; ++i)
+        if (i < splits) v += q[i];
     }
     uint16_t p[3];
     split3(v, p);
@@ -516,83 +551,146 @@ __device__ __forceinline__ void stage_t(const LoraSet& s, const int* ids, int M,
   }
 }
 
-// One workgroup: 16 rows x 64 kNB columns, 16 kNB columns a wave.  B enters as
-// the MFMA's row operand and t as its column operand, so a lane's four
-// results are four adjacent columns of one row.
-template <int kNB, bool kGlu>
-__global__ __launch_bounds__(kFinishThreads) void finish_blocks_kernel(const LoraFinishArgs a) {
-  __shared__ TPieces tp[kGlu ? 2 : 1];
-  const int blocks = (a.M + kLoraRows - 1) / kLoraRows;
-  const int m0 = static_cast<int>(blockIdx.x % blocks) * kLoraRows;
-  const int n0 = (static_cast<int>(blockIdx.x / blocks) * 4 + wave_id()) * 16 * kNB;
+// The first column, within a wave's 64, of the four that lane kb = 0 holds of
+// block nb.
+constexpr __device__ int block_col(int nb) { return 32 * (nb >> 1) + 4 * (nb & 1); }
+
+// One workgroup: 16 kRB rows x 64 columns a wave.  B enters as the MFMA's row
+// operand and t as its column operand, with the columns placed so that a lane's
+// results of two blocks are eight adjacent columns of one row; the sums start
+// from the base's.  An adapter's rows of B are loaded while the one before it
+// is used, once for all the rows.
+template <int kRB, bool kGlu>
+__global__ __launch_bounds__(512) void finish_blocks_kernel(const LoraFinishArgs a) {
+  constexpr int kNB = 4, kKS = kLoraChunk / 32;
+  __shared__ TPieces<kRB> tp;
+  const int waves = blockDim.x / kWave;
+  const int blocks = (a.M + kRB * kLoraRows - 1) / (kRB * kLoraRows);
+  const int m0 = static_cast<int>(blockIdx.x % blocks) * kRB * kLoraRows;
+  const int n0 = (static_cast<int>(blockIdx.x / blocks) * waves + wave_id()) * 16 * kNB;
   const int lane = lane_id();
   const int lc = lane & 15, kb = lane >> 4;
-  const int row = m0 + lc;
 
-  f32x4 sum[2][kNB];
+  f32x4 sum[kGlu ? 2 : 1][kRB][kNB];
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
+    const LoraBase& base = w == 0 ? a.base0 : a.base1;
+    // (rows and columns past the end read the last ones and are not stored)
+    const float* p[kRB];
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb) sum[w][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int r_max = max(a.s0.R, kGlu ? a.s1.R : 0);
+    for (int rb = 0; rb < kRB; ++rb)
+      p[rb] = base.p + static_cast<size_t>(min(m0 + rb * kLoraRows + lc, a.M - 1)) * base.ld;
+    for (int i = 0; i < base.S; ++i)  // one plane after another
+#pragma unroll
+      for (int rb = 0; rb < kRB; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(p[rb] + i * base.split_stride +
+                                                          min(n0 + block_col(nb) + 8 * kb, a.N - 4));
+          sum[w][rb][nb] = i == 0 ? v : sum[w][rb][nb] + v;
+        }
+    if (base.rs != nullptr) {
+#pragma unroll
+      for (int rb = 0; rb < kRB; ++rb) {
+        const float f = base.rs[min(m0 + rb * kLoraRows + lc, a.M - 1)];
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) sum[w][rb][nb] *= f;
+      }
+    }
+  }
+  const int r_max = max(a.s0.b != nullptr ? a.s0.R : 0, kGlu && a.s1.b != nullptr ? a.s1.R : 0);
   for (int r0 = 0; r0 < r_max; r0 += kLoraChunk) {
-    __syncthreads();
-    if (a.s0.b != nullptr && r0 < a.s0.R)
-      stage_t(a.s0, a.ids, a.M, m0, r0, a.splits, threadIdx.x, kFinishThreads, tp[0]);
-    if (kGlu && a.s1.b != nullptr && r0 < a.s1.R)
-      stage_t(a.s1, a.ids, a.M, m0, r0, a.splits, threadIdx.x, kFinishThreads, tp[kGlu ? 1 : 0]);
-    __syncthreads();
 #pragma unroll
     for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
       const LoraSet& s = w == 0 ? a.s0 : a.s1;
       if (s.b == nullptr || r0 >= s.R) continue;
-      const int mine = adapter_of(a.ids, row, a.M, s.n);
+      // lane l knows the adapter of row m0 + l
+      const int mine = lane < kRB * kLoraRows ? adapter_of(a.ids, m0 + lane, a.M, s.n) : -1;
       uint64_t todo = __ballot(mine >= 0);
-      while (todo != 0) {
-        const int id = __builtin_amdgcn_readlane(mine, __ffsll(static_cast<unsigned long long>(todo)) - 1);
-        todo &= ~__ballot(mine == id);
+      if (todo == 0) continue;  // (the same in every wave)
+      auto load = [&](int id, uint4 bf[kKS][kNB]) {
         const int rank = rank_of(s, id);
-        f32x4 acc[kNB];
 #pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) acc[nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int ks = 0; ks < kLoraChunk / 32; ++ks) {
-          if (r0 + 32 * ks >= rank) break;
-          uint4 bf[kNB];
+        for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
           for (int nb = 0; nb < kNB; ++nb) {
-            const int n = min(n0 + 16 * nb + lc, a.N - 1);  // columns past N are not stored
-            bf[nb] = load_b8(s.b + (static_cast<size_t>(id) * a.N + n) * s.R, r0 + 32 * ks + 8 * kb, rank);
+            const int n = n0 + block_col(nb) + 8 * (lc >> 2) + (lc & 3);
+            bf[ks][nb] = load_b8(s.b + (static_cast<size_t>(id) * a.N + min(n, a.N - 1)) * s.R,
+                                 r0 + 32 * ks + 8 * kb, rank);
           }
+      };
+      int id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
+      uint4 bf[kKS][kNB];
+      load(id, bf);
+      __syncthreads();  // the sums before are done with the pieces
+      stage_t<kRB>(s, a.ids, a.M, m0, r0, a.splits, threadIdx.x, blockDim.x, tp);
+      __syncthreads();
+      while (todo != 0) {
+        const uint64_t rows = __ballot(mine == id);
+        todo &= ~rows;
+        const int id_next = todo != 0 ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo)) : id;
+        uint4 bn[kKS][kNB];
+        if (todo != 0) load(id_next, bn);
 #pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            const uint4 tf = *reinterpret_cast<const uint4*>(&tp[kGlu ? w : 0].p[j][lc][32 * ks + 8 * kb]);
+        for (int rb = 0; rb < kRB; ++rb) {
+          if (((rows >> (rb * kLoraRows)) & 0xffffu) == 0) continue;  // (wave-uniform)
+          f32x4 acc[kNB];
 #pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) acc[nb] = mfma_bf16(bf[nb], tf, acc[nb]);
+          for (int nb = 0; nb < kNB; ++nb) acc[nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              const uint4 tf =
+                  *reinterpret_cast<const uint4*>(&tp.p[j][rb * kLoraRows + lc][32 * ks + 8 * kb]);
+#pragma unroll
+              for (int nb = 0; nb < kNB; ++nb) acc[nb] = mfma_bf16(bf[ks][nb], tf, acc[nb]);
+            }
+          // element i of lane (lc, kb): column block_col(nb) + 8kb + i, row lc
+          if ((rows >> (rb * kLoraRows + lc)) & 1) {
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) sum[w][rb][nb] += acc[nb];
           }
         }
-        // element i of lane (lc, kb): column 4kb + i, row lc
-        if (mine == id) {
+        if (todo != 0) {
 #pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) sum[w][nb] += acc[nb];
+          for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) bf[ks][nb] = bn[ks][nb];
         }
+        id = id_next;
       }
     }
   }
-  if (row >= a.M) return;
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
-    const int n = n0 + 16 * nb + 4 * kb;
-    if (n >= a.N) break;
-    const size_t at = static_cast<size_t>(row) * a.N + n;
-    f32x4 v = base_sum_loop(a.base0, row, n) + sum[0][nb];
-    if (kGlu) {
-      const f32x4 u = base_sum_loop(a.base1, row, n) + sum[1][nb];
+  for (int rb = 0; rb < kRB; ++rb) {
+    const int row = m0 + rb * kLoraRows + lc;
+    if (row >= a.M) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
+    for (int nb = 0; nb < kNB; nb += 2) {
+      const int n = n0 + block_col(nb) + 8 * kb;
+      if (n >= a.N) continue;
+      f32x4 v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = sum[0][rb][nb + j];
+        if (kGlu) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] = silu(v[j][i]) * sum[kGlu ? 1 : 0][rb][nb + j][i];
+        }
+      }
+      store8(a.out, a.out_bf16, static_cast<size_t>(row) * a.N + n, v[0], v[1]);
     }
-    store4(a.out, a.out_bf16, at, v);
   }
+}
+
+template <int kRB, bool kGlu>
+w4a16_status_t launch_finish_blocks(const LoraFinishArgs& a, int waves, hipStream_t stream) {
+  const int rows = kRB * kLoraRows, cols = waves * 64;
+  const size_t blocks = static_cast<size_t>((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols);
+  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+  finish_blocks_kernel<kRB, kGlu><<<static_cast<unsigned>(blocks), waves * kWave, 0, stream>>>(a);
+  return launch_status();
 }
 
 // ---------------------------------------------------------------- a few rows, one launch
@@ -800,11 +898,18 @@ void launch_head_q(const ShrinkArgs& a, const PrepArgs& p, int q, unsigned block
 
 ShrinkShape shrink_shape(int M, int K, int R) {
   ShrinkShape sh;
-  sh.rows = static_cast<size_t>(M) * R <= 4096;
+  // Rows by themselves read an adapter again for every row, blocks of rows once
+  // for all the rows of an adapter but do the work of 16 for one.  Adapters of
+  // 7168 x 4096, bf16, rows / blocks: 64 rows of 64 adapters of rank 64 41 / 151
+  // us, 128 of 64 62 / 160, 256 of 64 107 / 185, 1024 of 64 (rank 16) 138 / 250;
+  // runs of rows that share one of four, 128 (rank 32) 44 / 53, 256 (rank 64)
+  // 100 / 81, 1024 (rank 16) 137 / 119, 2000 (8 of rank 8) 220 / 169.  Which of
+  // the two the ids are the host does not know; many rows are taken for runs.
+  sh.rows = M <= 512 && static_cast<size_t>(M) * R <= 16384;
   if (sh.rows) return sh;
   const int blocks = (M + 63) / 64, chunks = (R + 16 * shrink_cols(R) - 1) / (16 * shrink_cols(R));
   // about one workgroup per CU, a wave keeping at least four k steps
-  sh.splits = std::max(1, std::min({8, 256 / (blocks * chunks), K / 32 / (4 * kShrinkWaves)}));
+  sh.splits = std::max(1, std::min({kMaxShrinkSplits, 256 / (blocks * chunks), K / 32 / (4 * kShrinkWaves)}));
   return sh;
 }
 
@@ -841,7 +946,8 @@ w4a16_status_t launch_lora_head(const void* x, w4a16_dtype_t xt, int M, int K, c
     p.rs = prep.rs;
     const int q = shrink_quota(static_cast<size_t>(M) * R * n);
     a.chunks = std::max(1, (R + q - 1) / q);
-    const size_t blocks = static_cast<size_t>(p.rows) + static_cast<size_t>(n) * a.chunks * M;
+    a.sets = n;
+    const size_t blocks = static_cast<size_t>(p.rows) + xcd_blocks(M, n * a.chunks);
     if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
     const unsigned g = static_cast<unsigned>(blocks);
     if (g == 0) return W4A16_OK;
@@ -861,7 +967,8 @@ w4a16_status_t launch_lora_head(const void* x, w4a16_dtype_t xt, int M, int K, c
   if (n == 0) return W4A16_OK;
   const int cb = shrink_cols(R);
   a.chunks = (R + 16 * cb - 1) / (16 * cb);
-  const size_t blocks = (static_cast<size_t>(M) + 63) / 64 * a.chunks * a.splits;
+  a.slots = kShrinkSlots;
+  const size_t blocks = (static_cast<size_t>(M) + 63) / 64 * a.chunks * a.splits * a.slots;
   if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n));
   if (xt == W4A16_BF16)
@@ -876,28 +983,20 @@ w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
   const bool glu = a.base1.p != nullptr;
   if (a.rows) {
     const int cols = kFinishThreads * kFinishCols;
-    const dim3 grid(a.M, (a.N + cols - 1) / cols);
+    const size_t blocks = xcd_blocks(a.M, (a.N + cols - 1) / cols);
+    if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(blocks));
     if (glu)
       finish_rows_kernel<true><<<grid, kFinishThreads, 0, stream>>>(a);
     else
       finish_rows_kernel<false><<<grid, kFinishThreads, 0, stream>>>(a);
     return launch_status();
   }
-  // 64 columns a wave once there are rows to fill the chip with; else 16
-  const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{1} << 21);
-  const int cols = tall ? 256 : 64;
-  const size_t blocks = (static_cast<size_t>(a.M) + kLoraRows - 1) / kLoraRows * ((a.N + cols - 1) / cols);
-  if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (glu && tall)
-    finish_blocks_kernel<4, true><<<grid, kFinishThreads, 0, stream>>>(a);
-  else if (glu)
-    finish_blocks_kernel<1, true><<<grid, kFinishThreads, 0, stream>>>(a);
-  else if (tall)
-    finish_blocks_kernel<4, false><<<grid, kFinishThreads, 0, stream>>>(a);
-  else
-    finish_blocks_kernel<1, false><<<grid, kFinishThreads, 0, stream>>>(a);
-  return launch_status();
+  // tall blocks, which read B and t for more rows and columns at once, where
+  // they still fill the chip
+  const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{1} << 22);
+  if (glu) return tall ? launch_finish_blocks<2, true>(a, 8, stream) : launch_finish_blocks<1, true>(a, 4, stream);
+  return tall ? launch_finish_blocks<4, false>(a, 8, stream) : launch_finish_blocks<1, false>(a, 4, stream);
 }
 
 // Picks waves, column blocks, K parts and splits by an estimate of the launch's
