@@ -43,14 +43,15 @@ struct ShrinkShape {
 ShrinkShape shrink_shape(int M, int K, int R);
 
 // What a projection needs of x beside t: f16 pieces, each row scaled by a power
-// of two (2^-e to rs), for the streamed product (units [K/32][4][2^rshift] of
-// 16 bytes) or for the tiles ([pieces][rows][K], rows past M zero); rows 0:
+// of two (2^-e to rs).  Chunk c of 8 values of row m, piece j, is the 16 bytes
+// at unit (c / 4) * group + (c % 4) * chunk + m * row + j * piece, for chunks c <
+// chunks (those past K are zeros) and m < rows (those past M are zeros); rows 0:
 // nothing.
 struct LoraPrep {
-  int pieces, rows;
-  uint4* stream;
-  int rshift;
-  _Float16* tiles;
+  int pieces, rows, chunks;
+  size_t group, chunk, row, piece;
+  uint4* out;
+  _Float16* tiles;  // out, where it is laid out as the 64-row tiles' pieces
   float* rs;
 };
 
@@ -109,5 +110,26 @@ struct LoraStreamArgs {
   int out_bf16;
 };
 w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hipStream_t stream);
+
+// The base product of up to 64 rows, in K splits whose sums are left in planes
+// [splits][M][mats * N] for the finish.
+struct LoraTilePlan {
+  bool ok = false;
+  int parts = 2, splits = 1, gpp = 4, tiles = 1;
+  size_t groups = 0;  // of the prepared rows: parts * gpp * splits, past K zeros
+  size_t plane_bytes = 0;
+};
+LoraTilePlan plan_lora_tiles(int M, int pieces, int N, int mats, int K);
+struct LoraTileArgs {
+  const uint4* xs;  // the prepared rows
+  int pieces;
+  int M, K, N, mats;
+  const u32x4 *qw0, *qw1;
+  const float *sc0, *sc1;
+  int gshift;
+  int splits, gpp;  // the plan
+  float* planes;
+};
+w4a16_status_t launch_lora_tiles(LoraTileArgs a, const LoraTilePlan& p, hipStream_t stream);
 
 }  // namespace w4

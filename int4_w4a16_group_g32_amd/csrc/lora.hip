@@ -137,13 +137,7 @@ inline size_t xcd_blocks(int rows, int parts) {
 
 // The rows of x as f16 pieces for the base product: scaled by one power of two
 // a row (2^-e to rs), in the order codes_f16 expands to.
-struct PrepArgs {
-  int pieces, rows;  // rows: M, or the tiles' padded count (the rest are zeros)
-  uint4* stream;     // units [K/32][4][2^rshift] as stream.h stages them, or
-  int rshift;
-  _Float16* tiles;   // [pieces][rows][K]
-  float* rs;
-};
+using PrepArgs = LoraPrep;
 
 template <int kXP, int kP>
 __device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p, int m) {
@@ -178,19 +172,18 @@ __device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p,
     for (int i = 0; i < 8; ++i) v[i] = mx != 0 ? v[i] * scale : 0.0f;
     half8 h[2];
     stream_pieces<kP>(v, h);
+    uint4* o = p.out + (c / 4 * p.group + c % 4 * p.chunk + m * p.row);
 #pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      uint4* o = p.stream != nullptr
-                     ? p.stream + ((static_cast<size_t>(c) << p.rshift) + m * kP + j)
-                     : reinterpret_cast<uint4*>(p.tiles + (static_cast<size_t>(j) * p.rows + m) * a.K + 8 * static_cast<size_t>(c));
-      *o = __builtin_bit_cast(uint4, h[j]);
-    }
+    for (int j = 0; j < kP; ++j) o[j * p.piece] = __builtin_bit_cast(uint4, h[j]);
   };
 #pragma unroll
   for (int i = 0; i < kHold; ++i)
     if (tid + i * 256 < nc) put(tid + i * 256, x[i]);
   for (int c = tid + kHold * 256; c < nc; c += 256)
     put(c, stream_load_x<kXP>(a.x, xrow + 8 * static_cast<size_t>(c)));
+  for (int c = nc + tid; c < p.chunks; c += 256)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) p.out[c / 4 * p.group + c % 4 * p.chunk + m * p.row + j * p.piece] = make_uint4(0, 0, 0, 0);
 }
 
 // What comes before the base product, in one launch.  The first workgroups
@@ -309,6 +302,9 @@ __device__ __forceinline__ void row_dots(const float* t, const uint16_t* const b
 }
 
 constexpr int kFinishThreads = 256;
+constexpr int kTileWaves = 8, kTileThreads = kTileWaves * kWave;
+template <int kP, int kRT>
+constexpr int kTileOcc = 4;  // waves a SIMD
 constexpr int kLoraUnits = 512;  // LDS units (16 bytes) per wave of the streamed product
 
 // kC columns of base, 64 apart: rs * the sum of the planes, in split order, 16
@@ -867,6 +863,194 @@ void launch_stream_mats(const LoraStreamArgs& a, dim3 grid, dim3 threads, size_t
     lora_stream_kernel<kP, 4 / kP, kMats><<<grid, threads, lds, stream>>>(a);
 }
 
+// ---------------------------------------------------------------- up to 64 rows: the base product
+
+// In LDS the four k blocks of row r of 16 trade places by an exclusive or with
+// 0, 2, 3, 1 for r / 4 = 0 .. 3: a 16-byte read takes lanes 0-3, 12-15 and 20-27
+// (and the like) together, which then lie in different banks.
+__device__ __forceinline__ int tile_turn(int r) { return 0x78 >> (r >> 2 << 1) & 3; }
+
+// 17 to 64 rows (9 to 64 in two pieces) of the base product.  A workgroup of 8
+// waves takes kCols blocks of 64 columns (gate's, then up's) and one K split;
+// its kParts K parts meet in LDS.  A wave takes all the rows, so that codes are
+// expanded once: kRT blocks of 16 rows and 64 columns, a lane's 16 kRT sums,
+// within 128 registers (two workgroups a CU, four waves a SIMD, which cover
+// each other's waits).  The rows are staged in windows, two buffers in turn: a
+// step loads, two steps ahead, its group of codes and its share of the next
+// window, and writes the share that has arrived, so that nothing waits for the
+// last load.
+//
+// 64 bf16 rows through gate and up of 7168 x 18432: 55 us, 3.0 TB/s of weights.
+// The vector units bound it: 64 scalings of 16 results, 36 steps of expansion
+// and 16 products a wave and group take 45 us with no loads at all.
+template <int kP, int kRT, int kParts>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(kTileOcc<kP, kRT>)))
+void lora_tiles_kernel(const LoraTileArgs a) {
+  constexpr int kCols = kTileWaves / kParts, kRows = 16 * kRT;
+  constexpr int kGU = 4 * kP * kRows;                   // units of a group: [piece][row][k block]
+  constexpr int kW = 8 / (kParts * kP);                 // groups of a part's window
+  constexpr int kPU = kW * kGU, kWU = kParts * kPU;     // units of a part's window, of all
+  constexpr int kPer = kWU / kTileThreads;              // units a thread stages of a window
+  constexpr int kS = (kPer + kW - 1) / kW;              // and of a step
+  constexpr int kV = kW > 1 ? 1 : 2;                    // windows a turn of the loop
+  constexpr int kCB = kRT * kP >= 3 ? 2 : 4;            // columns a lane expands at once (registers)
+  static_assert(kWU % kTileThreads == 0 && kW * kV % 2 == 0, "");
+  extern __shared__ uint4 lds[];
+  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
+  const int tid = threadIdx.x, wv = wave_id(), lane = lane_id();
+  const int lc = lane & 15, kb = lane >> 4;
+  const int col = wv % kCols, part = wv / kCols;
+  const int nb = a.N / 64, block = tile * kCols + col;
+  const bool wave_ok = block < a.mats * nb;
+  const int mat = wave_ok && block >= nb ? 1 : 0;
+  const int n0 = wave_ok ? (block - mat * nb) * 64 : 0;  // (a wave past the last column streams the first)
+  const int G = a.K / kGroup, groups = kParts * a.gpp, g_wg = split * groups;
+
+  // this thread's units of window 0; the next window's are kPU further
+  const int to = tid ^ tile_turn(tid >> 2 & 15);
+  // (through a buffer resource: one 32-bit offset a lane, the rest is scalar)
+  const __amdgpu_buffer_rsrc_t xw =
+      stream_rsrc(uniform_at(a.xs, static_cast<uint64_t>(g_wg) * kGU * 16), groups * kGU * 16);
+  constexpr bool kWhole = kPU % kTileThreads == 0;  // the threads' unit i belongs to one part
+  int xo[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int u = i * kTileThreads + tid;
+    xo[i] = (u / kPU * a.gpp * kGU + u % kPU) * 16;
+  }
+  auto unit = [&](int v, int i) {  // of window v
+    const int at = kWhole ? i * kTileThreads / kPU * a.gpp * kGU + i * kTileThreads % kPU : 0;
+    return __builtin_bit_cast(
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(xw, kWhole ? tid * 16 : xo[i], (v * kPU + at) * 16, 0));
+  };
+  u32x4* window0 = reinterpret_cast<u32x4*>(lds);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) window0[i * kTileThreads + to] = unit(0, i);
+  const int wins = a.gpp / kW;
+
+  const StreamLane off = stream_lane(n0, lane);
+  const u32x4* qw = mat ? a.qw1 : a.qw0;
+  const float* sc = mat ? a.sc1 : a.sc0;
+  int g = min(g_wg + part * a.gpp, G - 1);
+  const int g_last = max(g, min(g_wg + (part + 1) * a.gpp, G) - 1);
+  const uint32_t magic = magic_vgpr();
+  StreamCodes ring[2];
+  u32x4 xr[2][kS];
+  // the loads of a step: its share j of window v, and its codes
+  auto next = [&](int j, int v, StreamCodes& c, u32x4 (&x)[kS]) {
+#pragma unroll
+    for (int s = 0; s < kS; ++s)
+      if (j * kS + s < kPer) x[s] = unit(min(v, wins - 1), j * kS + s);
+    stream_codes(uniform_at(qw, static_cast<uint64_t>(g) * a.N * 16),
+                 uniform_at(sc, static_cast<uint64_t>(g >> a.gshift) * a.N * 4), a.N, off, c);
+    g = min(g + 1, g_last);
+  };
+#pragma unroll
+  for (int t = 0; t < 2; ++t) next(t % kW, t / kW + 1, ring[t], xr[t]);
+  __syncthreads();
+
+  f32x4 acc[kRT][4];
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb) acc[rt][cb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int frag = part * kPU + 4 * lc + (kb ^ tile_turn(lc));
+  for (int v0 = 0; v0 < wins; v0 += kV) {
+#pragma unroll
+    for (int vv = 0; vv < kV; ++vv) {
+      const int v = v0 + vv;
+      const uint4* cur = lds + (v & 1) * kWU + frag;
+      uint4* other = lds + (~v & 1) * kWU + to;
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const int slot = (vv * kW + j) & 1;
+#pragma unroll
+        for (int c0 = 0; c0 < 4; c0 += kCB) {
+          half8 bq[kCB];
+#pragma unroll
+          for (int cb = 0; cb < kCB; ++cb) bq[cb] = codes_f16(ring[slot].w[c0 + cb], magic);
+#pragma unroll
+          for (int rt = 0; rt < kRT; ++rt) {
+            f32x4 d[kCB];
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+              const half8 af = *reinterpret_cast<const half8*>(cur + (j * kGU + 4 * (p * kRows + rt * 16)));
+#pragma unroll
+              for (int cb = 0; cb < kCB; ++cb)
+                d[cb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    af, bq[cb], p == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : d[cb], 0, 0, 0);
+            }
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[rt][c0 + cb][i] = fmaf(ring[slot].s[c0 + cb], d[cb][i], acc[rt][c0 + cb][i]);
+          }
+          if (kCB < 4) __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+          if (j * kS + s < kPer) *reinterpret_cast<u32x4*>(other + (j * kS + s) * kTileThreads) = xr[slot][s];
+        next((j + 2) % kW, v + (j + 2) / kW + 1, ring[slot], xr[slot]);
+      }
+      __syncthreads();  // this window is consumed, the next one staged
+    }
+  }
+
+  // the parts' sums, by halves
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int h = kParts / 2; h >= 1; h /= 2) {
+    if (part >= h && part < 2 * h) {
+#pragma unroll
+      for (int q = 0; q < 4 * kRT; ++q) red[((wv - h * kCols) * 4 * kRT + q) * kWave + lane] = acc[q / 4][q % 4];
+    }
+    __syncthreads();
+    if (part < h) {
+#pragma unroll
+      for (int q = 0; q < 4 * kRT; ++q) acc[q / 4][q % 4] += red[(wv * 4 * kRT + q) * kWave + lane];
+    }
+    __syncthreads();
+  }
+  if (part > 0 || !wave_ok) return;
+  // element i of lane (lc, kb): row 4 kb + i, column 4 lc + cb
+  const int ld = a.mats * a.N;
+  float* o = a.planes + static_cast<size_t>(split) * a.M * ld + mat * a.N + n0 + 4 * lc;
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = 16 * rt + 4 * kb + i;
+      if (m < a.M)
+        *reinterpret_cast<f32x4*>(o + static_cast<size_t>(m) * ld) =
+            f32x4{acc[rt][0][i], acc[rt][1][i], acc[rt][2][i], acc[rt][3][i]};
+    }
+}
+
+template <int kP, int kRT>
+void launch_tiles_parts(const LoraTileArgs& a, const LoraTilePlan& p, hipStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(p.tiles * p.splits);
+  const size_t lds = static_cast<size_t>(2 * kTileThreads) * kRT * 16;
+  if constexpr (4 * kP * 16 * kRT <= 384) {
+    if (p.parts == 4) {
+      lora_tiles_kernel<kP, kRT, 4><<<grid, kTileThreads, lds, stream>>>(a);
+      return;
+    }
+  }
+  lora_tiles_kernel<kP, kRT, 2><<<grid, kTileThreads, lds, stream>>>(a);
+}
+template <int kP>
+void launch_tiles_rows(const LoraTileArgs& a, const LoraTilePlan& p, hipStream_t stream) {
+  if (a.M <= 16)
+    launch_tiles_parts<kP, 1>(a, p, stream);
+  else if (a.M <= 32)
+    launch_tiles_parts<kP, 2>(a, p, stream);
+  else if (a.M <= 48)
+    launch_tiles_parts<kP, 3>(a, p, stream);
+  else
+    launch_tiles_parts<kP, 4>(a, p, stream);
+}
+
 // Ranks a workgroup of the row kernel takes: one, until there are workgroups
 // enough that sharing the reads of x is worth more.
 int shrink_quota(size_t dots) { return dots >= 2048 ? 4 : (dots >= 1024 ? 2 : 1); }
@@ -905,7 +1089,7 @@ ShrinkShape shrink_shape(int M, int K, int R) {
   // runs of rows that share one of four, 128 (rank 32) 44 / 53, 256 (rank 64)
   // 100 / 81, 1024 (rank 16) 137 / 119, 2000 (8 of rank 8) 220 / 169.  Which of
   // the two the ids are the host does not know; many rows are taken for runs.
-  sh.rows = M <= 512 && static_cast<size_t>(M) * R <= 16384;
+  sh.rows = M <= 64 || (M <= 512 && static_cast<size_t>(M) * R <= 16384);
   if (sh.rows) return sh;
   const int blocks = (M + 63) / 64, chunks = (R + 16 * shrink_cols(R) - 1) / (16 * shrink_cols(R));
   // about one workgroup per CU, a wave keeping at least four k steps
@@ -937,13 +1121,7 @@ w4a16_status_t launch_lora_head(const void* x, w4a16_dtype_t xt, int M, int K, c
   const int n = live_sets(sets, n_sets, a, R);
   if (M == 0) return W4A16_OK;
   if (sh.rows) {
-    PrepArgs p{};
-    p.pieces = prep.pieces;
-    p.rows = prep.rows;
-    p.stream = prep.stream;
-    p.rshift = prep.rshift;
-    p.tiles = prep.tiles;
-    p.rs = prep.rs;
+    const PrepArgs& p = prep;
     const int q = shrink_quota(static_cast<size_t>(M) * R * n);
     a.chunks = std::max(1, (R + q - 1) / q);
     a.sets = n;
@@ -997,6 +1175,56 @@ w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
   const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{1} << 22);
   if (glu) return tall ? launch_finish_blocks<2, true>(a, 8, stream) : launch_finish_blocks<1, true>(a, 4, stream);
   return tall ? launch_finish_blocks<4, false>(a, 8, stream) : launch_finish_blocks<1, false>(a, 4, stream);
+}
+
+// Picks K parts and splits by an estimate of the launch's time, fitted to a
+// sweep of all of them over twelve shapes (12 to 64 rows, 1024 x 8192 to 7168 x
+// 36864): for the workgroups of a CU, their group steps (expanding the codes,
+// each block's scalings and products, staging the rows); a further workgroup on
+// a CU; the planes' way to memory and back.  It finds the best of the sweep
+// within 4 %.  64 bf16 rows through 7168 x 4096 take 24.4 us with 4 parts and 7
+// splits (27 us with 2 parts and 7, 28 us with 4 and 4), through 18432 x 7168
+// 43.8 us with 2 and 9 (48 us with 4 and 4), head and finish included.
+LoraTilePlan plan_lora_tiles(int M, int pieces, int N, int mats, int K) {
+  LoraTilePlan best;
+  const int G = K / kGroup, blocks = mats * (N / 64), rt = (M + 15) / 16, rows = 16 * rt;
+  double best_us = 1e30;
+  for (int parts = 2; parts <= 4; parts *= 2) {
+    const int cols = kTileWaves / parts, tiles = (blocks + cols - 1) / cols;
+    if (parts * pieces * rows > 384) continue;  // (the staged shares no longer fit the registers)
+    const int step = std::max(2, 8 / (parts * pieces));
+    for (int splits = 1; splits <= kMaxSplits; ++splits) {
+      const int gpp = (G + splits * parts * step - 1) / (splits * parts * step) * step;
+      if (splits > 1 && (splits - 1) * parts * gpp >= G) continue;  // an empty split
+      const size_t groups = static_cast<size_t>(parts) * gpp * splits;
+      if (groups / splits * 4 * pieces * rows * 16 >= (size_t{1} << 31)) continue;  // (32-bit offsets)
+      const double per_cu = std::ceil(tiles * splits / 256.0);
+      const double us = per_cu * gpp * (0.2 + rt * (0.041 + pieces * (0.0126 + 0.0107 * parts))) +
+                        0.94 * (per_cu - 1) + 0.084 * splits + static_cast<double>(splits) * M * mats * N * 8 / 10.5e6;
+      if (us < best_us) {
+        best_us = us;
+        best.ok = true;
+        best.parts = parts;
+        best.splits = splits;
+        best.gpp = gpp;
+        best.tiles = tiles;
+        best.groups = groups;
+        best.plane_bytes = static_cast<size_t>(splits) * M * mats * N * 4;
+      }
+    }
+  }
+  return best;
+}
+
+w4a16_status_t launch_lora_tiles(LoraTileArgs a, const LoraTilePlan& p, hipStream_t stream) {
+  a.splits = p.splits;
+  a.gpp = p.gpp;
+  if (static_cast<size_t>(p.tiles) * p.splits > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
+  if (a.pieces == 2)
+    launch_tiles_rows<2>(a, p, stream);
+  else
+    launch_tiles_rows<1>(a, p, stream);
+  return launch_status();
 }
 
 // Picks waves, column blocks, K parts and splits by an estimate of the launch's
@@ -1088,9 +1316,11 @@ size_t t_bytes(const w4a16_lora_t* l, int M, const ShrinkShape& sh) {
 // a few rows in one streamed launch, more on the tiles with the product where
 // the tiles' split sums, or their output, are finished.
 struct LinearPlan {
-  bool stream = false, pair = false;  // pair: gate and up as two plain products
+  // up to 16 rows; up to 64; else the 64-row tiles, or gate and up as two plain products
+  bool stream = false, rows64 = false, pair = false;
   int pieces = 1, rshift = 0;
   LoraStreamPlan st;
+  LoraTilePlan tl;
   MfmaPlan mf;
   size_t ap_off = 0, rs_off = 0, partials_off = 0, base0_off = 0, base1_off = 0;
   size_t bytes = 0;  // from the workspace's start, counters included
@@ -1118,6 +1348,17 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
     return p;
   }
   p.pieces = mfma_pieces(lt);
+  if (M <= 64) {
+    p.tl = plan_lora_tiles(M, p.pieces, N, w1 != nullptr ? 2 : 1, K);
+    p.rows64 = p.tl.ok;
+  }
+  if (p.rows64) {
+    c.take(p.partials_off, p.tl.plane_bytes);
+    c.take(p.ap_off, p.tl.groups * 4 * p.pieces * ((M + 15) / 16 * 16) * 16);
+    c.take(p.rs_off, static_cast<size_t>(M) * 4);
+    p.bytes = c.cursor;
+    return p;
+  }
   p.mf = plan_mfma(M, N, w1 != nullptr ? 1 : 0, K, lt, w1 == nullptr);
   if (w1 != nullptr && p.mf.S == 1) {
     p.pair = true;
@@ -1137,17 +1378,34 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
 }
 
 // What the launch before a projection prepares for it.
-LoraPrep linear_prep(const LinearPlan& p, int M, char* ws) {
+LoraPrep linear_prep(const LinearPlan& p, int M, int K, char* ws) {
   LoraPrep r{};
   if (p.pair) return r;  // (w4a16_gemm prepares its own)
   r.pieces = p.pieces;
   r.rs = reinterpret_cast<float*>(ws + p.rs_off);
-  if (p.stream) {
+  r.out = reinterpret_cast<uint4*>(ws + p.ap_off);
+  const size_t rows = (M + 15) / 16 * 16;
+  if (p.stream) {  // [group][k block][row][piece], the rows of a power of two
     r.rows = M;
-    r.stream = reinterpret_cast<uint4*>(ws + p.ap_off);
-    r.rshift = p.rshift;
-  } else {
+    r.chunks = K / 8;
+    r.chunk = size_t{1} << p.rshift;
+    r.group = 4 * r.chunk;
+    r.row = p.pieces;
+    r.piece = 1;
+  } else if (p.rows64) {  // [group][piece][row][k block]
+    r.rows = M;
+    r.chunks = static_cast<int>(p.tl.groups * 4);
+    r.chunk = 1;
+    r.group = p.pieces * rows * 4;
+    r.row = 4;
+    r.piece = rows * 4;
+  } else {  // [piece][row][group][k block]
     r.rows = p.mf.Mp;
+    r.chunks = K / 8;
+    r.chunk = 1;
+    r.group = 4;
+    r.row = K / 8;
+    r.piece = static_cast<size_t>(p.mf.Mp) * (K / 8);
     r.tiles = reinterpret_cast<_Float16*>(ws + p.ap_off);
   }
   return r;
@@ -1202,8 +1460,32 @@ w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt,
     f.base1 = LoraBase{base1, 1, M, N, 0, nullptr};
     return launch_lora_finish(f, stream);
   }
-  _Float16* ap = reinterpret_cast<_Float16*>(ws + p.ap_off);
   float* rs = reinterpret_cast<float*>(ws + p.rs_off);
+  if (p.rows64) {
+    LoraTileArgs a{};
+    a.xs = reinterpret_cast<const uint4*>(ws + p.ap_off);
+    a.pieces = p.pieces;
+    a.M = M;
+    a.K = K;
+    a.N = N;
+    a.mats = w1 != nullptr ? 2 : 1;
+    a.qw0 = reinterpret_cast<const u32x4*>(w0->qw);
+    a.sc0 = w0->scales;
+    if (w1 != nullptr) {
+      a.qw1 = reinterpret_cast<const u32x4*>(w1->qw);
+      a.sc1 = w1->scales;
+    }
+    a.gshift = group_shift(w0);
+    a.planes = reinterpret_cast<float*>(ws + p.partials_off);
+    if ((st = launch_lora_tiles(a, p.tl, stream)) != W4A16_OK) return st;
+    f.base0 = LoraBase{a.planes, p.tl.splits, M, a.mats * N, static_cast<size_t>(M) * a.mats * N, rs};
+    if (w1 != nullptr) {
+      f.base1 = f.base0;
+      f.base1.p += N;
+    }
+    return launch_lora_finish(f, stream);
+  }
+  _Float16* ap = reinterpret_cast<_Float16*>(ws + p.ap_off);
   MfmaArgs a = mfma_dense_args(p.mf, M, w0, w1, w1 != nullptr ? 1 : 0, ap, rs, ws, p.partials_off, 0);
   if (p.mf.wide || p.mf.S == 1) {
     a.out = base0;
@@ -1297,7 +1579,7 @@ extern "C" w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   char* b = static_cast<char*>(ws);
   const LoraSet set = lora_set(lora, reinterpret_cast<float*>(b + p.t_off));
-  st = launch_lora_head(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, linear_prep(p.lin, M, b), stream);
+  st = launch_lora_head(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, linear_prep(p.lin, M, w->K, b), stream);
   if (st != W4A16_OK) return st;
   return lora_linear(p.lin, x, xt, M, w, nullptr, set, LoraSet{}, adapter_ids, p.sh, y, yt, b, stream);
 }
@@ -1337,12 +1619,12 @@ extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt,
   const LoraSet gu[2] = {lora_set(lora_gate, reinterpret_cast<float*>(b + p.tg_off)),
                          lora_set(lora_up, reinterpret_cast<float*>(b + p.tu_off))};
   const LoraSet d = lora_set(lora_down, reinterpret_cast<float*>(b + p.td_off));
-  st = launch_lora_head(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, linear_prep(p.gu, M, b), stream);
+  st = launch_lora_head(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, linear_prep(p.gu, M, H, b), stream);
   if (st != W4A16_OK) return st;
   if ((st = lora_linear(p.gu, x, xt, M, gate, up, gu[0], gu[1], adapter_ids, p.sh_gu, h, W4A16_F32, b, stream)) !=
       W4A16_OK)
     return st;
-  st = launch_lora_head(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, linear_prep(p.dn, M, b), stream);
+  st = launch_lora_head(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, linear_prep(p.dn, M, I, b), stream);
   if (st != W4A16_OK) return st;
   return lora_linear(p.dn, h, W4A16_F32, M, down, nullptr, d, LoraSet{}, adapter_ids, p.sh_d, y, yt, b, stream);
 }

@@ -159,7 +159,7 @@ def test_no_adapters_is_the_plain_gemm(M, dtype):
     base = torch.empty((M, N), device="cuda")
     L.gemm(x, w, base, L.new_workspace(L.gemm_workspace_bytes(M, w, _code(dtype))))
     torch.cuda.synchronize()
-    if M > 16:  # the same tiles
+    if M > 64:  # the same tiles
         assert torch.equal(y, base)
     else:       # other orders of the same sums
         qw, sc = codes(K, N, 18)
