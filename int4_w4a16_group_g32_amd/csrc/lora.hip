@@ -263,41 +263,56 @@ __device__ __forceinline__ uint4 load_b8(const uint16_t* row, int r, int rank) {
   return v;
 }
 
-// v[i] += t . row i of b (kC of them), ranks below `rank` in ascending order;
-// 32 ranks' loads in flight together.  t is read up to the next
-// multiple of 8.
+// Ranks r0 .. r0 + 31 of kC rows of B, all loads in flight together.
 template <int kC>
-__device__ __forceinline__ void row_dots(const float* t, const uint16_t* const b[kC], int rank, float v[kC]) {
-  for (int r0 = 0; r0 < rank; r0 += 32) {
-    uint4 w[kC][4];
-    float4 tv[4][2];
+struct BRows {
+  uint4 w[kC][4];
+};
+template <int kC>
+__device__ __forceinline__ void load_rows(const uint16_t* const b[kC], int r0, int rank, BRows<kC>& f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + 8 * j;
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < kC; ++i) w[i][j] = load_b8(b[i], r, rank);
-      if (r < rank) {
-        tv[j][0] = *reinterpret_cast<const float4*>(t + r);
-        tv[j][1] = *reinterpret_cast<const float4*>(t + r + 4);
-      }
+    for (int i = 0; i < kC; ++i) f.w[i][j] = load_b8(b[i], r0 + 8 * j, rank);
+}
+
+// v[i] += t . those ranks of row i, ranks below `rank` in ascending order.  t is
+// read up to the next multiple of 8.
+template <int kC>
+__device__ __forceinline__ void dot_rows(const float* t, int r0, int rank, const BRows<kC>& f, float v[kC]) {
+  float4 tv[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (r0 + 8 * j < rank) {
+      tv[j][0] = *reinterpret_cast<const float4*>(t + r0 + 8 * j);
+      tv[j][1] = *reinterpret_cast<const float4*>(t + r0 + 8 * j + 4);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = rank - r0 - 8 * j;
-      if (n <= 0) break;
-      float tj[8] = {tv[j][0].x, tv[j][0].y, tv[j][0].z, tv[j][0].w, tv[j][1].x, tv[j][1].y, tv[j][1].z, tv[j][1].w};
+  for (int j = 0; j < 4; ++j) {
+    const int n = rank - r0 - 8 * j;
+    if (n <= 0) break;
+    float tj[8] = {tv[j][0].x, tv[j][0].y, tv[j][0].z, tv[j][0].w, tv[j][1].x, tv[j][1].y, tv[j][1].z, tv[j][1].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tj[e] = e < n ? tj[e] : 0.0f;  // (what was never written)
+    for (int e = 0; e < 8; ++e) tj[e] = e < n ? tj[e] : 0.0f;  // (what was never written)
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        const uint32_t d[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+    for (int i = 0; i < kC; ++i) {
+      const uint32_t d[4] = {f.w[i][j].x, f.w[i][j].y, f.w[i][j].z, f.w[i][j].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[i] = fmaf(tj[2 * e], __uint_as_float(d[e] << 16), v[i]);
-          v[i] = fmaf(tj[2 * e + 1], __uint_as_float(d[e] & 0xffff0000u), v[i]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        v[i] = fmaf(tj[2 * e], __uint_as_float(d[e] << 16), v[i]);
+        v[i] = fmaf(tj[2 * e + 1], __uint_as_float(d[e] & 0xffff0000u), v[i]);
       }
     }
+  }
+}
+
+// v[i] += t . row i of b.
+template <int kC>
+__device__ __forceinline__ void row_dots(const float* t, const uint16_t* const b[kC], int rank, float v[kC], int r0 = 0) {
+  for (; r0 < rank; r0 += 32) {
+    BRows<kC> f;
+    load_rows<kC>(b, r0, rank, f);
+    dot_rows<kC>(t, r0, rank, f, v);
   }
 }
 
@@ -307,33 +322,46 @@ template <int kP, int kRT>
 constexpr int kTileOcc = 4;  // waves a SIMD
 constexpr int kLoraUnits = 512;  // LDS units (16 bytes) per wave of the streamed product
 
-// kC columns of base, 64 apart: rs * the sum of the planes, in split order, 16
-// planes' loads in flight together.
+// kC columns of base, 64 apart, of the first planes: loads that nothing waits for yet.
+constexpr int kBaseAhead = 4;
 template <int kC>
-__device__ __forceinline__ void base_sum(const LoraBase& b, int m, int n, int N, float v[kC]) {
-  constexpr int kB = 16;
+struct BaseAhead {
+  float q[kC][kBaseAhead];
+};
+template <int kC>
+__device__ __forceinline__ void base_load(const LoraBase& b, int m, int n, int N, BaseAhead<kC>& f) {
   const float* p = b.p + static_cast<size_t>(m) * b.ld;
 #pragma unroll
-  for (int i = 0; i < kC; ++i) v[i] = 0.0f;
-  for (int s0 = 0; s0 < b.S; s0 += kB) {
+  for (int s = 0; s < kBaseAhead; ++s)
+#pragma unroll
+    for (int i = 0; i < kC; ++i) f.q[i][s] = p[min(s, b.S - 1) * b.split_stride + min(n + 64 * i, N - 1)];
+}
+// rs * the sum of the planes, in split order, 8 more planes' loads in flight together.
+template <int kC>
+__device__ __forceinline__ void base_sum(const LoraBase& b, int m, int n, int N, const BaseAhead<kC>& f, float v[kC]) {
+  constexpr int kB = 8;
+  const float* p = b.p + static_cast<size_t>(m) * b.ld;
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    v[i] = f.q[i][0];
+#pragma unroll
+    for (int s = 1; s < kBaseAhead; ++s) v[i] = s < b.S ? v[i] + f.q[i][s] : v[i];
+  }
+  for (int s0 = kBaseAhead; s0 < b.S; s0 += kB) {
     float q[kC][kB];
 #pragma unroll
     for (int s = 0; s < kB; ++s)
-      if (s0 + s < b.S) {
 #pragma unroll
-        for (int i = 0; i < kC; ++i) q[i][s] = p[(s0 + s) * b.split_stride + min(n + 64 * i, N - 1)];
-      }
+      for (int i = 0; i < kC; ++i) q[i][s] = p[min(s0 + s, b.S - 1) * b.split_stride + min(n + 64 * i, N - 1)];
 #pragma unroll
     for (int s = 0; s < kB; ++s)
-      if (s0 + s < b.S) {
 #pragma unroll
-        for (int i = 0; i < kC; ++i) v[i] += q[i][s];
-      }
+      for (int i = 0; i < kC; ++i) v[i] = s0 + s < b.S ? v[i] + q[i][s] : v[i];
   }
   if (b.rs != nullptr) {
-    const float f = b.rs[m];
+    const float r = b.rs[m];
 #pragma unroll
-    for (int i = 0; i < kC; ++i) v[i] *= f;
+    for (int i = 0; i < kC; ++i) v[i] *= r;
   }
 }
 
@@ -364,29 +392,38 @@ __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(const LoraF
   if (!xcd_place(blockIdx.x, a.M, (a.N + kFinishThreads * kFinishCols - 1) / (kFinishThreads * kFinishCols), m, part))
     return;
   const int n = (part * 4 + wave_id()) * 64 * kFinishCols + lane_id();
-  int id[2], rank[2];
+  constexpr int kMats = kGlu ? 2 : 1;
+  BaseAhead<kFinishCols> ahead[kMats];
 #pragma unroll
-  for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
+  for (int w = 0; w < kMats; ++w) base_load<kFinishCols>(w == 0 ? a.base0 : a.base1, m, n, a.N, ahead[w]);
+  __builtin_amdgcn_sched_barrier(0);
+  int rank[kMats];
+  const uint16_t* rows[kMats][kFinishCols];
+  BRows<kFinishCols> first[kMats];
+#pragma unroll
+  for (int w = 0; w < kMats; ++w) {
     const LoraSet& s = w == 0 ? a.s0 : a.s1;
-    id[w] = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
-    rank[w] = id[w] >= 0 ? rank_of(s, id[w]) : 0;
+    const int id = s.b != nullptr ? adapter_of(a.ids, m, a.M, s.n) : -1;
+    rank[w] = id >= 0 ? rank_of(s, id) : 0;
+#pragma unroll
+    for (int i = 0; i < kFinishCols; ++i)
+      rows[w][i] = s.b + (static_cast<size_t>(max(id, 0)) * a.N + min(n + 64 * i, a.N - 1)) * s.R;
+    load_rows<kFinishCols>(rows[w], 0, rank[w], first[w]);
     // (ranks up to the next multiple of 8 are read, and dropped)
     for (int r = threadIdx.x; r < rank[w]; r += kFinishThreads) t[w][r] = s.t[static_cast<size_t>(m) * s.R + r];
   }
   __syncthreads();
   float v[kFinishCols];
 #pragma unroll
-  for (int w = 0; w < (kGlu ? 2 : 1); ++w) {
-    const LoraSet& s = w == 0 ? a.s0 : a.s1;
+  for (int w = 0; w < kMats; ++w) {
     float d[kFinishCols], b[kFinishCols];
-    base_sum<kFinishCols>(w == 0 ? a.base0 : a.base1, m, n, a.N, b);
-    const uint16_t* rows[kFinishCols];
+    base_sum<kFinishCols>(w == 0 ? a.base0 : a.base1, m, n, a.N, ahead[w], b);
 #pragma unroll
-    for (int i = 0; i < kFinishCols; ++i) {
-      d[i] = 0.0f;
-      rows[i] = s.b + (static_cast<size_t>(max(id[w], 0)) * a.N + min(n + 64 * i, a.N - 1)) * s.R;
+    for (int i = 0; i < kFinishCols; ++i) d[i] = 0.0f;
+    if (rank[w] > 0) {
+      dot_rows<kFinishCols>(t[w], 0, rank[w], first[w], d);
+      row_dots<kFinishCols>(t[w], rows[w], rank[w], d, 32);
     }
-    if (rank[w] > 0) row_dots<kFinishCols>(t[w], rows, rank[w], d);
 #pragma unroll
     for (int i = 0; i < kFinishCols; ++i) v[i] = w == 0 ? b[i] + d[i] : silu(v[i]) * (b[i] + d[i]);
   }
