@@ -293,15 +293,18 @@ W4A16_API size_t w4a16_gemm_lora_workspace_bytes(int32_t M, const w4a16_weight_t
 /*
  * w4a16_gemm with an adapter for each row: y[M][N] as above, of type yt
  * (float32, or bf16 rounded once, to nearest even).  x, W and the first term
- * are as in w4a16_gemm.  The adapters' products run on bf16 matrix-core
- * operands with float32 sums; a float32 x, and x a^T, enter as three bf16
- * pieces (24 significant bits).  adapter_ids is int32 [M], in any order;
- * rows of one adapter that stand together share its reads.  Rows do not
- * affect one another: an infinity or NaN in x[m] or in one adapter reaches
- * the rows that use it only.  Deterministic.
+ * are as in w4a16_gemm (to its accuracy, not bitwise).  The adapters' products
+ * keep every bit of x, a, b and x a^T and sum in float32: row by row in fused
+ * multiply-adds for up to 64 rows, and up to 512 while M * rank <= 16384;
+ * above that in blocks of 64 rows on the matrix cores, where a float32 x, and
+ * x a^T, enter as three bf16 pieces.  adapter_ids is int32 [M], in any order;
+ * in blocks, rows of one adapter that stand together share its reads.  Rows
+ * do not affect one another: an infinity or NaN in x[m] or in one adapter
+ * reaches the rows that use it only.  Deterministic.  M = 0 does nothing.
  * Errors: as w4a16_gemm, plus INVALID_ARG for a null lora, a, b, scale or
  * adapter_ids, misaligned pointers, rank < 1, num_adapters < 1 or an unknown
- * yt, and UNSUPPORTED for a rank that is not a multiple of 8 or above 256.
+ * yt, and UNSUPPORTED for a rank that is not a multiple of 8 or above 256 and
+ * for K or N of 2^26 or more.
  */
 W4A16_API w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_weight_t* w,
                                          const w4a16_lora_t* lora, const int32_t* adapter_ids, void* y,
@@ -319,8 +322,9 @@ W4A16_API size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t 
  * up, and y is h Wd with its adapter term (of h), of type yt.  lora_gate,
  * lora_up and lora_down may each be NULL (no adapters on that projection) and
  * may differ in rank and number of adapters; one adapter_ids [M] serves all
- * three.  h stays float32 between the projections, and enters the adapters'
- * product in three bf16 pieces.
+ * three.  h stays float32 between the projections; the adapters' product takes
+ * it whole, the down product as f16 pieces scaled by a power of two per row
+ * (one with bf16 x and more than 8 rows, else two: 22 significant bits).
  * Errors: as w4a16_swiglu_mlp and w4a16_gemm_lora (but a null lora is none).
  */
 W4A16_API w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt, int32_t M,

@@ -1333,6 +1333,9 @@ w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hip
 
 namespace {
 
+// The kernels' 32-bit row bytes.
+bool sizes_fit(const w4a16_weight_t* w) { return w->K < 1 << 26 && w->N < 1 << 26; }
+
 w4a16_status_t check_lora(const w4a16_lora_t* l) {
   if (l == nullptr) return W4A16_OK;  // no adapters on this projection
   if (l->a == nullptr || l->b == nullptr || l->scale == nullptr) return W4A16_ERR_INVALID_ARG;
@@ -1593,7 +1596,7 @@ using namespace w4;
 
 extern "C" size_t w4a16_gemm_lora_workspace_bytes(int32_t M, const w4a16_weight_t* w, w4a16_dtype_t xt,
                                                   const w4a16_lora_t* lora) {
-  if (M <= 0 || check_dense_grouped(w) != W4A16_OK || !known_type(xt)) return 0;
+  if (M <= 0 || check_dense_grouped(w) != W4A16_OK || !sizes_fit(w) || !known_type(xt)) return 0;
   if (lora == nullptr || check_lora(lora) != W4A16_OK) return 0;
   return plan_lora_gemm(M, w, xt, lora).bytes;
 }
@@ -1603,6 +1606,7 @@ extern "C" w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32
                                           w4a16_dtype_t yt, void* ws, size_t ws_bytes, hipStream_t stream) {
   w4a16_status_t st = check_dense_grouped(w);
   if (st != W4A16_OK) return st;
+  if (!sizes_fit(w)) return W4A16_ERR_UNSUPPORTED;
   if (lora == nullptr) return W4A16_ERR_INVALID_ARG;
   if ((st = check_lora(lora)) != W4A16_OK) return st;
   if (M < 0 || !known_type(xt) || !known_type(yt)) return W4A16_ERR_INVALID_ARG;
@@ -1625,7 +1629,7 @@ extern "C" size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t
                                                         const w4a16_weight_t* up, const w4a16_weight_t* down,
                                                         const w4a16_lora_t* lora_gate, const w4a16_lora_t* lora_up,
                                                         const w4a16_lora_t* lora_down) {
-  if (M <= 0 || check_mlp(gate, up, down) != W4A16_OK || !known_type(xt)) return 0;
+  if (M <= 0 || check_mlp(gate, up, down) != W4A16_OK || !sizes_fit(gate) || !known_type(xt)) return 0;
   for (const w4a16_lora_t* l : {lora_gate, lora_up, lora_down})
     if (check_lora(l) != W4A16_OK) return 0;
   return plan_lora_mlp(M, xt, gate, up, down, lora_gate, lora_up, lora_down).bytes;
@@ -1639,6 +1643,7 @@ extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt,
                                                 size_t ws_bytes, hipStream_t stream) {
   w4a16_status_t st = check_mlp(gate, up, down);
   if (st != W4A16_OK) return st;
+  if (!sizes_fit(gate)) return W4A16_ERR_UNSUPPORTED;
   for (const w4a16_lora_t* l : {lora_gate, lora_up, lora_down})
     if ((st = check_lora(l)) != W4A16_OK) return st;
   if (M < 0 || !known_type(xt) || !known_type(yt)) return W4A16_ERR_INVALID_ARG;

@@ -1,8 +1,8 @@
 """Element-wise bounds and inputs for the low-rank-adapter tests (no test functions).
 
 The base term keeps the bound of w4a16_gemm (oracle_pool).  The adapters' term: bf16
-operands, and float32 ones as three bf16 pieces (exact), so a product is exact in the
-matrix cores' float32 and every error is a rounding of a running sum, at most
+operands, and float32 ones as three bf16 pieces (exact) or in fused multiply-adds, so a
+product is exact before it is added and every error is a rounding of a running sum, at most
 u = 2^-24 of the sum of the terms' magnitudes each.  A sum of K terms, however it is
 grouped, has at most K roundings: |error of t| <= K u sum |x||a|.  t is scaled (one
 rounding), and its product with B sums 3 R terms, so |error| <= |s| (err(t) |b| +

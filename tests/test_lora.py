@@ -191,3 +191,27 @@ def test_binding_rejects_bad_ids_and_outputs(monkeypatch):
         L.gemm_lora(x, w, lo, ids, y[:, :64], ws)
     with pytest.raises(ValueError):
         L.swiglu_mlp_lora(x, w, w, _w(128, 64), None, None, _lo(), ids, torch.zeros((2, 64)), ws)  # down is [128 -> 64]
+
+
+@pytest.mark.parametrize("K,N", [(2 ** 26, 64), (64, 2 ** 26)])
+def test_sizes_past_32_bit_row_bytes_are_refused(lib, K, N):
+    r = ctypes.byref
+    big, d, lo = _desc(K, N), _desc(N, K), _ldesc()
+    assert lib.w4a16_gemm_lora_workspace_bytes(4, r(big), L.BF16, r(lo)) == 0
+    assert lib.w4a16_gemm_lora(_p(0x1000), L.BF16, 4, r(big), r(lo), _p(0x2000), _p(0x8000), L.F32, _p(0x10000),
+                               1 << 40, None) == L.ERR_UNSUPPORTED
+    assert lib.w4a16_swiglu_mlp_lora_workspace_bytes(4, L.BF16, r(big), r(big), r(d), r(lo), None, None) == 0
+    assert lib.w4a16_swiglu_mlp_lora(_p(0x1000), L.BF16, 4, r(big), r(big), r(d), r(lo), None, None, _p(0x2000),
+                                     _p(0x8000), L.F32, _p(0x10000), 1 << 40, None) == L.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 17, 33, 64, 65, 513])
+@pytest.mark.parametrize("xt", [L.F32, L.BF16])
+def test_a_smaller_batch_needs_no_more_than_its_own_workspace(lib, M, xt):
+    """The size is that of the call: exactly it is enough, one byte less is refused."""
+    r = ctypes.byref
+    w, lo = _desc(2048, 448), _ldesc()
+    need = lib.w4a16_gemm_lora_workspace_bytes(M, r(w), xt, r(lo))
+    assert need > 0 and need % 256 == 0
+    assert lib.w4a16_gemm_lora(_p(0x1000), xt, M, r(w), r(lo), _p(0x2000), _p(0x800000), L.F32, _p(0x10000),
+                               need - 1, None) == L.ERR_WORKSPACE
