@@ -758,22 +758,32 @@ MdPlan plan_md(int M, int k, const w4a16_weight_t* gate, bool shared) {
   MdPlan p;
   const int H = gate->K, I = gate->N, G = H / kGroup;
   p.items = std::min(M * k, gate->num_experts) + (shared ? 1 : 0);
-  // Gate and up: workgroups of 4 waves, and of 8 or 16 (more K parts), at last
-  // of half the columns, while the launch would leave waves of the chip unused
-  // and a part keeps a ring of groups.
+  // Gate and up: workgroups of 4 waves, and of 8 (more K parts), at last of half
+  // the columns, while the launch would leave waves of the chip unused and a
+  // part keeps a ring of groups.  Sixteen waves start later than they stream
+  // faster: one token through 8 of 64 experts of 7168 x 2048 50.5 us with 8,
+  // 51.7 with 16 (both kernels), four through 2048 x 1024 30.2 and 31.8.
   auto wgs = [&](int cols) { return static_cast<size_t>(p.items) * ((I / 64 + cols - 1) / cols); };
-  while (p.waves < 16 && wgs(p.cols) * p.waves < 16 * kMdCus && G / (p.waves / p.cols) >= kStreamRing) p.waves *= 2;
-  if (p.waves == 16 && wgs(2) < kMdCus && G / 8 >= kStreamRing) p.cols = 1;
+  if (wgs(p.cols) * p.waves < 16 * kMdCus && G / (p.waves / p.cols) >= kStreamRing) p.waves = 8;
+  if (p.waves == 8 && wgs(2) < kMdCus && G / 4 >= kStreamRing) p.cols = 1;
   p.tiles = (I / 64 + p.cols - 1) / p.cols;
   p.parts = p.waves / (2 * p.cols);
   p.gpp = (G + p.parts * kStreamRing - 1) / (p.parts * kStreamRing) * kStreamRing;
   // Down: workgroups of 16 waves, one per CU, while each of the four parts has
-  // a ring of groups or more.
+  // a ring of groups or more; where they have few, of 8 with twice the splits
+  // (three tokens through 128 x 256 15.8 us for 19, one through 1408 x 4096
+  // 31.7 for 33.2; sixteen through 2048 x 7168, 200 groups a part, 221 for 190).
   p.dtiles = (H + kMdCols - 1) / kMdCols;
   const int total = p.items * (I / kGroup);
-  p.dwaves = total >= 16 ? 16 : 4;
-  const int parts = p.dwaves / 4;
-  p.dsplits = std::max(1, std::min({kMdCus / p.dtiles, total / (4 * parts), kMdMaxSplits}));
+  auto splits = [&](int parts, int most) {
+    return std::max(1, std::min({kMdCus / p.dtiles, total / (kStreamRing * parts), most}));
+  };
+  p.dwaves = 16;
+  p.dsplits = splits(4, kMdMaxSplits);
+  if (total <= 16 * 4 * p.dsplits) {
+    p.dwaves = total >= 2 * kStreamRing ? 8 : 4;
+    p.dsplits = splits(p.dwaves / 4, kMdMaxSplits / 2);
+  }
   const size_t pairs = static_cast<size_t>(M) * k + (shared ? M : 0);
   Carve c;
   size_t counters;
