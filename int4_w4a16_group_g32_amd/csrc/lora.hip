@@ -188,7 +188,9 @@ __device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p,
 
 // What comes before the base product, in one launch.  The first workgroups
 // each prepare a row; the others take one row and kQ ranks of t, their four
-// waves quarters of K, all of a step's loads in flight together.
+// waves quarters of K, all of a step's loads in flight together.  One launch
+// instead of two (a launch of either alone takes 4 us); 64 rows of as many
+// adapters, K 7168, rank 32: 8 us, 3.7 TB/s of adapters.
 template <int kXP, int kP, int kQ>
 __global__ __launch_bounds__(256) void head_kernel(const ShrinkArgs a, const PrepArgs p) {
   if (static_cast<int>(blockIdx.x) < p.rows) {
@@ -384,7 +386,9 @@ __device__ __forceinline__ void store8(void* out, int bf16, size_t at, f32x4 v, 
 // One row; a thread takes two columns 64 apart, so that a wave reads adjacent
 // rows of B together.  The row's t is the workgroup's.
 constexpr int kFinishCols = 2;
-
+// The base's planes and B are asked for before t is waited for: gate and up of
+// 64 rows x 18432 columns, three splits, rank 16: 17 us for 52 MB (20.8 us with
+// t first).
 template <bool kGlu>
 __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(const LoraFinishArgs a) {
   __shared__ __attribute__((aligned(16))) float t[2][kLoraMaxRank];
@@ -445,7 +449,9 @@ constexpr int kShrinkWaves = kShrinkThreads / kWave;
 
 // One workgroup: 64 rows, one chunk of 16 kCB ranks, one K split, one
 // projection, every slots-th adapter of those rows.  The four waves take
-// quarters of the split's K and meet in LDS.
+// quarters of the split's K and meet in LDS.  2048 bf16 rows, K 7168, rank 64:
+// 23 us for 29 MB of x, bound by the chain of loads (ids, then x and A) of the
+// blocks that hold several adapters.
 template <int kXP, int kCB>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_blocks_kernel(const ShrinkArgs a) {
   constexpr int kRB = 4, kU = kXP == 1 ? 4 : 2;  // k steps in flight
@@ -592,7 +598,8 @@ constexpr __device__ int block_col(int nb) { return 32 * (nb >> 1) + 4 * (nb & 1
 // operand and t as its column operand, with the columns placed so that a lane's
 // results of two blocks are eight adjacent columns of one row; the sums start
 // from the base's.  An adapter's rows of B are loaded while the one before it
-// is used, once for all the rows.
+// is used, once for all the rows.  2048 rows x 4096 columns, rank 64: 24 us for
+// 54 MB (40 us with 16 rows and 64 columns a workgroup).
 template <int kRB, bool kGlu>
 __global__ __launch_bounds__(512) void finish_blocks_kernel(const LoraFinishArgs a) {
   constexpr int kNB = 4, kKS = kLoraChunk / 32;
@@ -737,6 +744,8 @@ w4a16_status_t launch_finish_blocks(const LoraFinishArgs& a, int waves, hipStrea
 // (agent-scope stores, an arrival counter, the last workgroup sums in split
 // order); then a thread takes a row and two columns: their sums, their
 // adapter's dot products and, with gate and up, silu(gate) * up.
+// Four float32 rows through gate and up of 7168 x 18432: 34 us, 4.9 TB/s of
+// weights; the start (rows, ring) and the meeting are about 8 us of it.
 template <int kP, int kI, int kMats>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4)))
 void lora_stream_kernel(const LoraStreamArgs a) {

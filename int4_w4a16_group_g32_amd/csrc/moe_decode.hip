@@ -293,6 +293,10 @@ constexpr int kMdChoiceUnits = static_cast<int>((sizeof(MdChoice) + 15) / 16);
 // Where all tokens' rows fit the window they are staged while the choice is
 // made, as A rows in token order, and the results of tokens that did not
 // choose the expert are dropped; else the expert's own rows are, afterwards.
+//
+// 8 of 384 experts of 7168 x 2048 for one bf16 token: 29.3 us, 5.0 TB/s of
+// weights, of which the choice and the items are 4 us before the first load;
+// 32 experts for four float32 tokens 94 us, 6.2 TB/s (a plain read: 6.7).
 template <int kP, int kI>
 __global__ __launch_bounds__(kMdMaxThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void md_gate_up_kernel(const MdArgs a) {
@@ -478,6 +482,9 @@ void md_gate_up_kernel(const MdArgs a) {
 // quads of waves.  Groups are numbered through the experts: group f belongs to
 // item f / G.  A window may span experts, and the code ring runs on across
 // them.
+// 8 experts of 2048 x 7168 for one bf16 token: 20.2 us, 3.6 TB/s (5 us before
+// the stream starts, 3 us for the meeting); 32 experts for four float32 tokens
+// 54 us, 5.4 TB/s.
 template <int kP, int kI>
 __global__ __launch_bounds__(kMdMaxThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void md_down_kernel(const MdArgs a) {
