@@ -336,7 +336,7 @@ __device__ __forceinline__ void base_load(const LoraBase& b, int m, int n, int N
 #pragma unroll
   for (int s = 0; s < kBaseAhead; ++s)
 #pragma unroll
-    for (int i = 0; i < kC; ++i) f.q[i][s] = p[min(s, b.S - 1) * b.split_stride + min(n + 64 * i, N - 1)];
+    for (int i = 0; i < kC; ++i) f.q[i][s] = s < b.S ? p[s * b.split_stride + min(n + 64 * i, N - 1)] : 0.0f;
 }
 // rs * the sum of the planes, in split order, 8 more planes' loads in flight together.
 template <int kC>
