@@ -1217,8 +1217,10 @@ w4a16_status_t launch_lora_finish(const LoraFinishArgs& a, hipStream_t stream) {
     return launch_status();
   }
   // tall blocks, which read B and t for more rows and columns at once, where
-  // they still fill the chip
-  const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{1} << 22);
+  // they still fill the chip: calls of 2048 x 4096 (K 1024, 8 adapters of rank
+  // 64 in runs) 69 us for 80 without, 1000 x 4096 in random order 90 for 102,
+  // 1500 x 2048 (rank 32, runs) 74 for 66
+  const bool tall = static_cast<size_t>(a.M) * a.N >= (size_t{15} << 18);
   if (glu) return tall ? launch_finish_blocks<2, true>(a, 8, stream) : launch_finish_blocks<1, true>(a, 4, stream);
   return tall ? launch_finish_blocks<4, false>(a, 8, stream) : launch_finish_blocks<1, false>(a, 4, stream);
 }
@@ -1365,13 +1367,13 @@ size_t t_bytes(const w4a16_lora_t* l, int M, const ShrinkShape& sh) {
 // a few rows in one streamed launch, more on the tiles with the product where
 // the tiles' split sums, or their output, are finished.
 struct LinearPlan {
-  // up to 16 rows; up to 64; else the 64-row tiles, or gate and up as two plain products
+  // up to 16 rows; up to 64; else the 64-row tiles, gate and up in a launch each where those do not split K
   bool stream = false, rows64 = false, pair = false;
   int pieces = 1, rshift = 0;
   LoraStreamPlan st;
   LoraTilePlan tl;
   MfmaPlan mf;
-  size_t ap_off = 0, rs_off = 0, partials_off = 0, base0_off = 0, base1_off = 0;
+  size_t ap_off = 0, rs_off = 0, partials_off = 0, partials1_off = 0, base0_off = 0, base1_off = 0;
   size_t bytes = 0;  // from the workspace's start, counters included
 };
 
@@ -1411,17 +1413,15 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
   p.mf = plan_mfma(M, N, w1 != nullptr ? 1 : 0, K, lt, w1 == nullptr);
   if (w1 != nullptr && p.mf.S == 1) {
     p.pair = true;
-    p.bytes = plan_gemm(M, w0, lt).bytes;
-    c.cursor = round_up(p.bytes, 256);
-    c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
-    c.take(p.base1_off, static_cast<size_t>(M) * N * 4);
-    p.bytes = c.cursor;
-    return p;
+    p.mf = plan_mfma(M, N, 0, K, lt, true);
   }
   c.take(p.ap_off, static_cast<size_t>(p.mf.P) * p.mf.Mp * K * 2 + (p.mf.wide ? 256 : 0));
   c.take(p.rs_off, static_cast<size_t>(p.mf.Mp) * 4);
+  const bool summed = p.mf.S == 1 || p.mf.wide;  // the tiles' result is whole, else planes
   c.take(p.partials_off, mfma_partial_bytes(p.mf));
-  if (p.mf.S == 1 || p.mf.wide) c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
+  if (p.pair && !summed) c.take(p.partials1_off, mfma_partial_bytes(p.mf));
+  if (summed) c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
+  if (p.pair && summed) c.take(p.base1_off, static_cast<size_t>(M) * N * 4);
   p.bytes = c.cursor;
   return p;
 }
@@ -1429,7 +1429,6 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
 // What the launch before a projection prepares for it.
 LoraPrep linear_prep(const LinearPlan& p, int M, int K, char* ws) {
   LoraPrep r{};
-  if (p.pair) return r;  // (w4a16_gemm prepares its own)
   r.pieces = p.pieces;
   r.rs = reinterpret_cast<float*>(ws + p.rs_off);
   r.out = reinterpret_cast<uint4*>(ws + p.ap_off);
@@ -1498,17 +1497,7 @@ w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt,
   f.N = N;
   f.out = out;
   f.out_bf16 = ot == W4A16_BF16;
-  float* base0 = reinterpret_cast<float*>(ws + p.base0_off);
   w4a16_status_t st;
-  if (p.pair) {
-    float* base1 = reinterpret_cast<float*>(ws + p.base1_off);
-    const size_t gemm_bytes = plan_gemm(M, w0, xt).bytes;
-    if ((st = w4a16_gemm(x, xt, M, w0, base0, ws, gemm_bytes, stream)) != W4A16_OK) return st;
-    if ((st = w4a16_gemm(x, xt, M, w1, base1, ws, gemm_bytes, stream)) != W4A16_OK) return st;
-    f.base0 = LoraBase{base0, 1, M, N, 0, nullptr};
-    f.base1 = LoraBase{base1, 1, M, N, 0, nullptr};
-    return launch_lora_finish(f, stream);
-  }
   float* rs = reinterpret_cast<float*>(ws + p.rs_off);
   if (p.rows64) {
     LoraTileArgs a{};
@@ -1534,21 +1523,26 @@ w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt,
     }
     return launch_lora_finish(f, stream);
   }
-  _Float16* ap = reinterpret_cast<_Float16*>(ws + p.ap_off);
-  MfmaArgs a = mfma_dense_args(p.mf, M, w0, w1, w1 != nullptr ? 1 : 0, ap, rs, ws, p.partials_off, 0);
-  if (p.mf.wide || p.mf.S == 1) {
-    a.out = base0;
-    st = p.mf.wide ? launch_wide(a, p.mf.tasks * p.mf.S, stream) : launch_mfma(a, p.mf.P, p.mf.tasks, stream);
-    f.base0 = LoraBase{base0, 1, M, N, 0, nullptr};
-  } else {
-    defer_split_k(a, p.mf);
-    st = launch_mfma(a, p.mf.P, p.mf.tasks * p.mf.S, stream);
-    const size_t plane = static_cast<size_t>(a.plane_rows) * a.plane_ld;
-    f.base0 = LoraBase{a.planes, a.S, a.plane_rows, a.plane_ld, plane * (w1 != nullptr ? 2 : 1), rs};
-    if (w1 != nullptr) {
-      f.base1 = f.base0;
-      f.base1.p += plane;
+  // gate and up in one launch (split sums, which the finish joins), or one projection
+  auto tiles = [&](const w4a16_weight_t* a0, const w4a16_weight_t* a1, size_t partials, size_t out, LoraBase& base) {
+    MfmaArgs a = mfma_dense_args(p.mf, M, a0, a1, a1 != nullptr ? 1 : 0, reinterpret_cast<_Float16*>(ws + p.ap_off), rs,
+                                 ws, partials, 0);
+    if (p.mf.wide || p.mf.S == 1) {
+      a.out = reinterpret_cast<float*>(ws + out);
+      base = LoraBase{a.out, 1, M, N, 0, nullptr};
+      return p.mf.wide ? launch_wide(a, p.mf.tasks * p.mf.S, stream) : launch_mfma(a, p.mf.P, p.mf.tasks, stream);
     }
+    defer_split_k(a, p.mf);
+    const size_t plane = static_cast<size_t>(a.plane_rows) * a.plane_ld;
+    base = LoraBase{a.planes, a.S, a.plane_rows, a.plane_ld, plane * (a1 != nullptr ? 2 : 1), rs};
+    return launch_mfma(a, p.mf.P, p.mf.tasks * p.mf.S, stream);
+  };
+  st = tiles(w0, p.pair ? nullptr : w1, p.partials_off, p.base0_off, f.base0);
+  if (st == W4A16_OK && p.pair) {
+    st = tiles(w1, nullptr, p.partials1_off, p.base1_off, f.base1);
+  } else if (w1 != nullptr) {
+    f.base1 = f.base0;
+    f.base1.p += static_cast<size_t>(f.base0.plane_rows) * f.base0.ld;
   }
   if (st != W4A16_OK) return st;
   return launch_lora_finish(f, stream);
