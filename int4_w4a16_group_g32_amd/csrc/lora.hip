@@ -1419,6 +1419,7 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
   c.take(p.rs_off, static_cast<size_t>(p.mf.Mp) * 4);
   const bool summed = p.mf.S == 1 || p.mf.wide;  // the tiles' result is whole, else planes
   c.take(p.partials_off, mfma_partial_bytes(p.mf));
+  p.partials1_off = p.partials_off;  // (wide tiles are done with theirs)
   if (p.pair && !summed) c.take(p.partials1_off, mfma_partial_bytes(p.mf));
   if (summed) c.take(p.base0_off, static_cast<size_t>(M) * N * 4);
   if (p.pair && summed) c.take(p.base1_off, static_cast<size_t>(M) * N * 4);

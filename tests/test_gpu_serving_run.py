@@ -253,3 +253,45 @@ def test_expert_stacks_past_32_bit_offsets(M):
         bound = moe_bound_from(pool.bounds, want_ids, want_w)
     bound = bound + HALF_STEP[torch.float32] * (np.abs(ref) + bound)
     check_elementwise(y.double().cpu().numpy(), ref, bound, f"moe_decode E={E} M={M}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,H,I,kind", [
+    (300, 1024, 1024, "random"),     # bf16: wide tiles that split K, gate and up one after the other
+    (600, 2048, 512, "segments"),    # the same before the finish by blocks
+    (180, 512, 4096, "random"),      # 64-row tiles: gate and up in a launch each
+    (70, 2048, 1024, "random"),      # and in one
+    (520, 1088, 704, "segments"),    # K the wide tiles do not take
+])
+def test_mlp_lora_launch_shapes_and_one_workspace(M, H, I, kind, dtype):
+    """The base products' launch shapes; repeated calls on one workspace give the same bits."""
+    shapes = [(H, I), (H, I), (I, H)]
+    ws3 = [codes(K, N, 101 + i) for i, (K, N) in enumerate(shapes)]
+    los = [adapters(6, 16, K, N, 104 + i) for i, (K, N) in enumerate(shapes)]
+    ids = id_pattern(kind, M, 6, 107)
+    x = _x(M, H, dtype, 108)
+    dw, dlo, di = [device_weight(w) for w in ws3], [device_lora(l) for l in los], torch.from_numpy(ids).cuda()
+    ws = L.new_workspace(L.swiglu_mlp_lora_workspace_bytes(M, _code(dtype), *dw, *dlo))
+    first = _mlp(x, dw, dlo, di, torch.float32, ws)
+    xv = x_values(x)
+    _check(first, O.swiglu_mlp_lora64(xv, *ws3, *los, ids), mlp_lora_bound(xv, *ws3, *los, ids, dtype, torch.float32),
+           f"mlp_lora M={M} H={H} I={I} {dtype}", dtype)
+    for _ in range(3):
+        assert torch.equal(_mlp(x, dw, dlo, di, torch.float32, ws), first)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(300, 4096, 256), (600, 2048, 512), (80, 4096, 128), (1100, 1024, 1024)])
+def test_gemm_lora_launch_shapes_and_one_workspace(M, K, N, dtype):
+    """Base products that split K, by rows and by blocks of the finish."""
+    w, lo = codes(K, N, 111), adapters(6, 16, K, N, 112)
+    ids = id_pattern("random", M, 6, 113)
+    x = _x(M, K, dtype, 114)
+    dw, dlo, di = device_weight(w), device_lora(lo), torch.from_numpy(ids).cuda()
+    ws = L.new_workspace(L.gemm_lora_workspace_bytes(M, dw, _code(dtype), dlo))
+    first = _gemm(x, dw, dlo, di, torch.float32, ws)
+    xv = x_values(x)
+    _check(first, O.gemm_lora64(xv, w, lo, ids), gemm_lora_bound(xv, w, lo, ids, dtype, torch.float32),
+           f"gemm_lora M={M} K={K} N={N} {dtype}", dtype)
+    for _ in range(3):
+        assert torch.equal(_gemm(x, dw, dlo, di, torch.float32, ws), first)
