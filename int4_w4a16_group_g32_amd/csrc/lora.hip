@@ -141,7 +141,9 @@ using PrepArgs = LoraPrep;
 
 template <int kXP, int kP>
 __device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p, int m) {
-  constexpr int kHold = 4;  // chunks a thread keeps in registers
+  // chunks a thread keeps in registers; few float32 rows of a long K are read
+  // once (four rows of 18432: 7.4 -> 6.0 us), many rows want the occupancy
+  constexpr int kHold = kP == 2 ? 10 : 4;
   __shared__ uint32_t amax;
   const int tid = threadIdx.x, nc = a.K / 8;
   const size_t xrow = static_cast<size_t>(min(m, a.M - 1)) * a.K;
@@ -926,9 +928,10 @@ __device__ __forceinline__ int tile_turn(int r) { return 0x78 >> (r >> 2 << 1) &
 // window, and writes the share that has arrived, so that nothing waits for the
 // last load.
 //
-// 64 bf16 rows through gate and up of 7168 x 18432: 55 us, 3.0 TB/s of weights.
+// 64 bf16 rows through gate and up of 7168 x 18432: 55 to 62 us from box to
+// box, 2.7 to 3.0 TB/s of weights.
 // The vector units bound it: 64 scalings of 16 results, 36 steps of expansion
-// and 16 products a wave and group take 45 us with no loads at all.
+// and 16 products a wave and group take 45 of the 55 with no loads at all.
 template <int kP, int kRT, int kParts>
 __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(kTileOcc<kP, kRT>)))
 void lora_tiles_kernel(const LoraTileArgs a) {
