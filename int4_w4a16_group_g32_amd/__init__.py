@@ -145,13 +145,13 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (the signatures' c_void_p takes an int)
 
 
 def _stream(stream):
     if stream is None:  # the current stream's handle, without a Stream object around it (0.4 us for 2.9)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dtype_code(x: torch.Tensor) -> int:
@@ -174,14 +174,14 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _on_device(**tensors):
     """Every tensor the library reads or writes must be device memory."""
     for name, t in tensors.items():
-        if t is not None and t.device.type != "cuda":
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor, got {t.device}")
 
 
