@@ -123,16 +123,30 @@ constexpr int kMaxShrinkSplits = 8;
 constexpr int kShrinkSlots = 4;
 constexpr int kXcds = 8;  // the hardware deals workgroup b to XCD b % 8
 
-// Workgroup b of a grid over (row, part): the parts go round the XCDs, and all
+// Workgroup b of a grid over (row, part).  The parts go round the XCDs, and all
 // rows of a part to one, whose L2 then holds what the rows of an adapter share.
+// Above 64 rows a part's rows are cut into segments, so that 32 of them or more
+// go round (181 rows of an MLP 1536/640, rank 40: 75 -> 61 us); fewer rows are
+// not worth the divisions.
+__device__ __host__ inline int xcd_segments(int rows, int parts) {
+  return rows <= 64 ? 1 : (32 + parts - 1) / parts;
+}
 __device__ __forceinline__ bool xcd_place(int b, int rows, int parts, int& row, int& part) {
-  const int r = b / kXcds;
-  row = r % rows;
-  part = r / rows * kXcds + b % kXcds;
-  return part < parts;
+  const int segs = xcd_segments(rows, parts), per = segs == 1 ? rows : (rows + segs - 1) / segs;
+  const int r = b / kXcds, unit = r / per * kXcds + b % kXcds;
+  if (segs == 1) {
+    part = unit;
+    row = r % per;
+    return part < parts;
+  }
+  part = unit / segs;
+  row = unit % segs * per + r % per;
+  return part < parts && row < rows;
 }
 inline size_t xcd_blocks(int rows, int parts) {
-  return static_cast<size_t>((parts + kXcds - 1) / kXcds * kXcds) * rows;
+  if (parts == 0) return 0;
+  const int segs = xcd_segments(rows, parts), per = (rows + segs - 1) / segs;
+  return (static_cast<size_t>(parts) * segs + kXcds - 1) / kXcds * kXcds * per;
 }
 
 // The rows of x as f16 pieces for the base product: scaled by one power of two
@@ -1141,8 +1155,9 @@ ShrinkShape shrink_shape(int M, int K, int R) {
   sh.rows = M <= 64 || (M <= 512 && static_cast<size_t>(M) * R <= 16384);
   if (sh.rows) return sh;
   const int blocks = (M + 63) / 64, chunks = (R + 16 * shrink_cols(R) - 1) / (16 * shrink_cols(R));
-  // about one workgroup per CU, a wave keeping at least four k steps
-  sh.splits = std::max(1, std::min({kMaxShrinkSplits, 256 / (blocks * chunks), K / 32 / (4 * kShrinkWaves)}));
+  // about one workgroup per CU, a wave keeping a k step (four: 601 rows, K 896,
+  // rank 64, float32 88 us for 57)
+  sh.splits = std::max(1, std::min({kMaxShrinkSplits, 256 / (blocks * chunks), K / 32 / kShrinkWaves}));
   return sh;
 }
 
