@@ -11,7 +11,7 @@ namespace w4 {
 // carry 22 significant bits; bf16 activations fit in one.  Within every block
 // of 8 consecutive k the pieces are stored in the order k = 0,4,1,5,2,6,3,7,
 // the order in which one packed code word expands into f16 pairs.
-// Layout: ap[p][Mp][K] f16, rs[Mp] = 2^-e (0 for an all-zero or absent row).
+// Layout: ap[p][Mp][K] f16, rs[Mp] = 2^-e (0 for an absent row).
 inline int mfma_pieces(w4a16_dtype_t xt) { return xt == W4A16_F32 ? 2 : 1; }
 
 constexpr int kMfmaRows = 64;     // rows per tile

@@ -60,6 +60,9 @@ __device__ __forceinline__ void load8<uint16_t>(const uint16_t* xr, int b, float
 // One workgroup per row.  Pass 1: the row's largest magnitude; pass 2: pieces
 // of x * 2^e, each block of 8 in the order 0,4,1,5,2,6,3,7.  A thread takes
 // blocks of 8 consecutive activations (one or two 16-byte loads).
+// Absent rows have the scale 0.  A row whose largest magnitude is 0 keeps the
+// scale 1: fmaxf passes over NaNs, so it may be a row of zeros or of NaNs, and
+// has to stay either.
 template <typename XT, int P>
 __global__ __launch_bounds__(kPrepThreads) void mfma_prep_kernel(const XT* __restrict__ x, int R, int Mp,
                                                                  int K, const int* __restrict__ gather,
@@ -98,7 +101,7 @@ __global__ __launch_bounds__(kPrepThreads) void mfma_prep_kernel(const XT* __res
     lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
     e = 14 - lg;
   }
-  const float scale = (src >= 0 && amax > 0.0f) ? ldexpf(1.0f, e) : 0.0f;
+  const float scale = src >= 0 ? ldexpf(1.0f, e) : 0.0f;
   if (threadIdx.x == 0) rs[row] = scale > 0.0f ? ldexpf(1.0f, -e) : 0.0f;
   for (int b = threadIdx.x; b < nb; b += kPrepThreads) {
     float v[8];
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(kPrepWaveThreads) void mfma_prep_wave_kernel(const 
     lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
     e = 14 - lg;
   }
-  const float scale = (src >= 0 && amax > 0.0f) ? ldexpf(1.0f, e) : 0.0f;
+  const float scale = src >= 0 ? ldexpf(1.0f, e) : 0.0f;
   if (lane == 0) rs[row] = scale > 0.0f ? ldexpf(1.0f, -e) : 0.0f;
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
@@ -176,7 +179,7 @@ __global__ __launch_bounds__(kPrepWaveThreads) void mfma_prep_wave_kernel(const 
     half8 h0, h1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // a row without a nonzero value stores +0 pieces, as the workgroup form does
+      // an absent row stores +0 pieces, as the workgroup form does
       const float t = scale != 0.0f ? v[i][kCodeOrder[j]] * scale : 0.0f;
       const _Float16 hi = static_cast<_Float16>(t);
       h0[j] = hi;
@@ -764,7 +767,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_planes_kernel(const float* 
     lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
     e = 14 - lg;
   }
-  const float scale = (row < M && amax > 0.0f) ? ldexpf(1.0f, e) : 0.0f;
+  const float scale = row < M ? ldexpf(1.0f, e) : 0.0f;
   if (threadIdx.x == 0) rs[row] = scale > 0.0f ? ldexpf(1.0f, -e) : 0.0f;
   for (int b = threadIdx.x; b < nb; b += kPrepThreads) {
     float v[8];
@@ -867,7 +870,7 @@ __global__ __launch_bounds__(kSplitPrepThreads) void prep_split_pieces_kernel(
     lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
     e = 14 - lg;
   }
-  const float scale = amax > 0.0f ? ldexpf(1.0f, e) : 0.0f;
+  const float scale = row < M ? ldexpf(1.0f, e) : 0.0f;
   if (tid == 0) rs[static_cast<size_t>(c) * Mp + row] = scale > 0.0f ? ldexpf(1.0f, -e) : 0.0f;
 #pragma unroll
   for (int i = 0; i < kSplitPrepBlocks; ++i) {
