@@ -158,7 +158,7 @@ __device__ __forceinline__ void convert_window(GemvLds& lds, int nw, int nrows, 
     int e_win = kNoExp;
     if (amax > 0.0f) {
       int lg = ilogbf(amax);
-      lg = lg > 120 ? 120 : (lg < -112 ? -112 : lg);  // 2^e stays a normal float
+      lg = lg > 127 ? 127 : (lg < -112 ? -112 : lg);  // 2^e and 2^-e stay normal floats
       e_win = 14 - lg;
     }
     const int e_old = first ? kNoExp : lds.e[m];  // (all lanes read before lane 0 writes)

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kPrepThreads) void mfma_prep_kernel(const XT* __res
   int e = 0;
   if (amax > 0.0f) {
     int lg = ilogbf(amax);
-    lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
+    lg = lg > 127 ? 127 : (lg < -112 ? -112 : lg);  // 2^e and 2^-e stay normal floats
     e = 14 - lg;
   }
   const float scale = src >= 0 ? ldexpf(1.0f, e) : 0.0f;
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kPrepWaveThreads) void mfma_prep_wave_kernel(const 
   int e = 0;
   if (amax > 0.0f) {
     int lg = ilogbf(amax);
-    lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
+    lg = lg > 127 ? 127 : (lg < -112 ? -112 : lg);  // 2^e and 2^-e stay normal floats
     e = 14 - lg;
   }
   const float scale = src >= 0 ? ldexpf(1.0f, e) : 0.0f;
@@ -764,7 +764,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_planes_kernel(const float* 
   int e = 0;
   if (amax > 0.0f) {
     int lg = ilogbf(amax);
-    lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
+    lg = lg > 127 ? 127 : (lg < -112 ? -112 : lg);  // 2^e and 2^-e stay normal floats
     e = 14 - lg;
   }
   const float scale = row < M ? ldexpf(1.0f, e) : 0.0f;
@@ -867,7 +867,7 @@ __global__ __launch_bounds__(kSplitPrepThreads) void prep_split_pieces_kernel(
   int e = 0;
   if (amax > 0.0f) {
     int lg = ilogbf(amax);
-    lg = lg > 120 ? 120 : (lg < -120 ? -120 : lg);
+    lg = lg > 127 ? 127 : (lg < -112 ? -112 : lg);  // 2^e and 2^-e stay normal floats
     e = 14 - lg;
   }
   const float scale = row < M ? ldexpf(1.0f, e) : 0.0f;
