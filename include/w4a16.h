@@ -453,7 +453,7 @@ W4A16_API size_t w4a16_moe_decode_workspace_bytes(int32_t M, int32_t top_k, w4a1
  * An expert of weight 0 is not read.  topk_ids and topk_w [M][top_k] receive
  * the choice, each unless NULL.
  * Rows do not affect one another: an infinity or NaN in x[t] reaches y[t]
- * only.
+ * only, one in an expert's scales the tokens that chose it.
  * Errors: as w4a16_moe_grouped_shared (INVALID_ARG also where one or two of
  * the shared descriptors are NULL, and for an unknown yt), plus UNSUPPORTED
  * for more tokens than above, more than 1024 experts or top_k above 32.

@@ -478,6 +478,51 @@ void md_gate_up_kernel(const MdArgs a) {
   }
 }
 
+// A wave's sums of md_down_kernel over groups [f0, f1) of the long axis again,
+// for column block `block`, every group for the tokens that chose its expert
+// alone.  Operands and order are those of the streamed form, so that sums which
+// meet finite scales only keep their bits; the operands come from memory, since
+// the streamed form's windows are gone.
+template <int kP, int kI>
+__device__ __forceinline__ void md_down_apart(const MdArgs& a, const MdItems& rt, const uint32_t* amax, int routed,
+                                              int f0, int f1, int block, uint32_t magic, float acc[4][kI]) {
+  const int lane = lane_id(), lc = lane & 15, kb = lane >> 4, G = a.I / kGroup;
+  const int m = kP == 2 ? (lc >> 2) + 4 * ((lc >> 1) & 1) : (lc >> 2) + 4 * (lc & 3);  // the lane's A row
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+    for (int i = 0; i < kI; ++i) acc[cb][i] = 0.0f;
+#pragma unroll 1
+  for (int f = f0; f < f1; ++f) {
+    const int item = f / G, g = f % G;
+    const bool is_shared = item >= routed;
+    const uint32_t who = is_shared ? (1u << a.M) - 1u : rt.tokens[item];
+    const size_t e = is_shared ? 0 : static_cast<size_t>(rt.experts[item]) * G;
+    const u32x4 w = ((is_shared ? a.xqd : a.qd) + (e + g) * a.H)[block * 64 + lane];
+    const f32x4 sc = reinterpret_cast<const f32x4*>((is_shared ? a.xsd : a.sd) + ((e + g) >> a.dshift) * a.H +
+                                                    block * 64)[lc];
+    half8 p[2] = {half8{}, half8{}};
+    if (m < a.M && ((who >> m) & 1)) {
+      const int pair = is_shared ? a.M * a.k + m : md_pair(rt, item, m);
+      float v[8];
+      stream_x_values<2>(stream_load_x<2>(a.h, static_cast<size_t>(pair) * a.I + g * kGroup + 8 * kb), v);
+      const float scale = ldexpf(1.0f, stream_exp(__uint_as_float(amax[m])));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      stream_pieces<kP>(v, p);
+    }
+    const half8 af = kP == 2 && (lc & 1) ? p[1] : p[0];
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb) {
+      const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, codes_f16(w[cb], magic),
+                                                             f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+        if ((who >> (kb + 4 * i)) & 1) acc[cb][i] = fmaf(sc[cb], kP == 2 ? d[2 * i] + d[2 * i + 1] : d[i], acc[cb][i]);
+    }
+  }
+}
+
 // One tile of 256 output columns, one piece of the long axis, its K parts over
 // quads of waves.  Groups are numbered through the experts: group f belongs to
 // item f / G.  A window may span experts, and the code ring runs on across
@@ -665,6 +710,18 @@ void md_down_kernel(const MdArgs a) {
       __syncthreads();  // this window is consumed, the next one staged
       odd ^= 1;
     }
+    // A scale that is not finite makes NaNs of the zeros of the tokens that did
+    // not choose its expert.  Sums that are not finite are taken again without
+    // them.  (Clearing those tokens' scales in the stream itself cost one token 5 %
+    // of the layer and sixteen 6 %.)
+    bool finite = true;
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+      for (int i = 0; i < kI; ++i) finite &= fabsf(acc[cb][i]) <= FLT_MAX;
+    if (__builtin_expect(wave_ok && __ballot(!finite) != 0, 0))
+      md_down_apart<kP, kI>(a, rt, amax, routed, piece_lo + part * gpp,
+                            min(piece_hi, piece_lo + (part + 1) * gpp), block, magic, acc);
   }
 
   // the parts' sums, in order
