@@ -54,6 +54,10 @@ MfmaPlan plan_mfma(int rows, int N, int mode, int K, w4a16_dtype_t xt, bool allo
   m.tiles = (N + per_tile - 1) / per_tile;
   m.tasks = m.items * m.tiles;
   const int G = K / kGroup;
+  if (m.tasks == 0) {  // no columns: nothing is launched
+    m.gps = G;
+    return m;
+  }
   // Split K to balance the grid over the resident workgroups: the kernel holds
   // two workgroups per CU (its registers allow two waves per SIMD), 512 on
   // the chip, and every workgroup of a launch streams the same number of

@@ -821,6 +821,10 @@ struct MdPlan {
 MdPlan plan_md(int M, int k, const w4a16_weight_t* gate, bool shared) {
   MdPlan p;
   const int H = gate->K, I = gate->N, G = H / kGroup;
+  if (H == 0 || I == 0) {  // nothing is launched
+    p.bytes = kCounterBytes;
+    return p;
+  }
   p.items = std::min(M * k, gate->num_experts) + (shared ? 1 : 0);
   // Gate and up: workgroups of 4 waves, and of 8 (more K parts), at last of half
   // the columns, while the launch would leave waves of the chip unused and a
