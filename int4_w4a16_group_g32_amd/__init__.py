@@ -179,9 +179,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
 
 
 def _on_device(**tensors):
-    """Every tensor the library reads or writes must be device memory."""
+    """Every tensor the library reads or writes must be device memory, a Weight's codes and scales too."""
     for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
+        if isinstance(t, Weight):
+            if not (t.qw.is_cuda and t.scales.is_cuda):
+                raise ValueError(f"{name} must be on the device, got {t.qw.device}, {t.scales.device}")
+        elif isinstance(t, torch.Tensor) and not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor, got {t.device}")
 
 
@@ -295,7 +298,7 @@ def gemm(x: torch.Tensor, w: Weight, y: torch.Tensor, ws: torch.Tensor, stream=N
     _need_x(x, w.K)
     _need(y, "y", torch.float32, (x.shape[0], w.N))
     _need(ws, "ws", torch.uint8)
-    _on_device(x=x, y=y, ws=ws)
+    _on_device(x=x, w=w, y=y, ws=ws)
     _check(load_library().w4a16_gemm(_ptr(x), _dtype_code(x), x.shape[0], _dref(w), _ptr(y), _ptr(ws),
                                      ws.numel() * ws.element_size(), _stream(stream)), "w4a16_gemm")
 
@@ -309,7 +312,7 @@ def swiglu_mlp(x: torch.Tensor, gate: Weight, up: Weight, down: Weight, y: torch
     _need_x(x, gate.K)
     _need(y, "y", torch.float32, (x.shape[0], down.N))
     _need(ws, "ws", torch.uint8)
-    _on_device(x=x, y=y, ws=ws)
+    _on_device(x=x, gate=gate, up=up, down=down, y=y, ws=ws)
     _check(load_library().w4a16_swiglu_mlp(_ptr(x), _dtype_code(x), x.shape[0], _dref(gate), _dref(up),
                                            _dref(down), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
                                            _stream(stream)), "w4a16_swiglu_mlp")
@@ -319,7 +322,7 @@ def swiglu_mlp_static(x: torch.Tensor, gate: Weight, up: Weight, down: Weight, y
     """swiglu_mlp on the library's static per-GPU scratch (no workspace, no allocation)."""
     _need_x(x, gate.K)
     _need(y, "y", torch.float32, (x.shape[0], down.N))
-    _on_device(x=x, y=y)
+    _on_device(x=x, gate=gate, up=up, down=down, y=y)
     _check(load_library().w4a16_swiglu_mlp_static(_ptr(x), _dtype_code(x), x.shape[0], _dref(gate), _dref(up),
                                                   _dref(down), _ptr(y), _stream(stream)), "w4a16_swiglu_mlp_static")
 
@@ -348,7 +351,7 @@ def gemm_lora(x: torch.Tensor, w: Weight, lora: Lora, adapter_ids: torch.Tensor,
     _need_ids(adapter_ids, x.shape[0])
     yt = _need_y(y, (x.shape[0], w.N))
     _need(ws, "ws", torch.uint8)
-    _on_device(x=x, y=y, ws=ws)
+    _on_device(x=x, w=w, y=y, ws=ws)
     _check(load_library().w4a16_gemm_lora(_ptr(x), _dtype_code(x), x.shape[0], _dref(w), _lref(lora),
                                           _ptr(adapter_ids), _ptr(y), yt, _ptr(ws), _nbytes(ws), _stream(stream)),
            "w4a16_gemm_lora")
@@ -371,7 +374,7 @@ def swiglu_mlp_lora(x: torch.Tensor, gate: Weight, up: Weight, down: Weight, lor
     _need_ids(adapter_ids, x.shape[0])
     yt = _need_y(y, (x.shape[0], down.N))
     _need(ws, "ws", torch.uint8)
-    _on_device(x=x, y=y, ws=ws)
+    _on_device(x=x, gate=gate, up=up, down=down, y=y, ws=ws)
     _check(load_library().w4a16_swiglu_mlp_lora(_ptr(x), _dtype_code(x), x.shape[0], _dref(gate), _dref(up),
                                                 _dref(down), _lref(lora_gate), _lref(lora_up), _lref(lora_down),
                                                 _ptr(adapter_ids), _ptr(y), yt, _ptr(ws), _nbytes(ws),
@@ -414,7 +417,7 @@ def moe_shared_workspace_bytes(M: int, top_k: int, xt: int, gate: Weight, up: We
                                                            _dref(shared_down))
 
 
-def _check_moe_args(x, topk_ids, topk_w, gate: Weight, down: Weight, y, ws):
+def _check_moe_args(x, topk_ids, topk_w, gate: Weight, up: Weight, down: Weight, y, ws):
     """topk_ids int32 [M][k] (torch.topk's int64 ids must be converted), topk_w
     float32 [M][k], x [M][H], y float32 [M][H]; returns (M, k)."""
     _need(topk_ids, "topk_ids", torch.int32)
@@ -427,14 +430,15 @@ def _check_moe_args(x, topk_ids, topk_w, gate: Weight, down: Weight, y, ws):
         raise ValueError(f"x has {x.shape[0]} rows, topk_ids {M}")
     _need(y, "y", torch.float32, (M, down.N))
     _need(ws, "ws", torch.uint8)
-    _on_device(x=x, topk_ids=topk_ids, topk_w=topk_w, y=y, ws=ws)
+    _on_device(x=x, topk_ids=topk_ids, topk_w=topk_w, gate=gate, up=up, down=down, y=y, ws=ws)
     return M, k
 
 
 def moe_grouped_shared(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, gate: Weight, up: Weight,
                        down: Weight, shared_gate: Weight, shared_up: Weight, shared_down: Weight, y: torch.Tensor,
                        ws: torch.Tensor, stream=None):
-    M, k = _check_moe_args(x, topk_ids, topk_w, gate, down, y, ws)
+    M, k = _check_moe_args(x, topk_ids, topk_w, gate, up, down, y, ws)
+    _on_device(shared_gate=shared_gate, shared_up=shared_up, shared_down=shared_down)
     _check(load_library().w4a16_moe_grouped_shared(_ptr(x), _dtype_code(x), M, _ptr(topk_ids), _ptr(topk_w), k,
                                                    _dref(gate), _dref(up), _dref(down), _dref(shared_gate),
                                                    _dref(shared_up), _dref(shared_down), _ptr(y), _ptr(ws),
@@ -444,7 +448,7 @@ def moe_grouped_shared(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Te
 
 def moe_grouped(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, gate: Weight, up: Weight,
                 down: Weight, y: torch.Tensor, ws: torch.Tensor, stream=None):
-    M, k = _check_moe_args(x, topk_ids, topk_w, gate, down, y, ws)
+    M, k = _check_moe_args(x, topk_ids, topk_w, gate, up, down, y, ws)
     _check(load_library().w4a16_moe_grouped(_ptr(x), _dtype_code(x), M, _ptr(topk_ids), _ptr(topk_w), k,
                                             _dref(gate), _dref(up), _dref(down), _ptr(y), _ptr(ws),
                                             ws.numel() * ws.element_size(), _stream(stream)),
@@ -472,8 +476,9 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate: Weight, 
         _need(topk_ids, "topk_ids", torch.int32, (M, top_k))
     if topk_w is not None:
         _need(topk_w, "topk_w", torch.float32, (M, top_k))
-    _on_device(x=x, logits=logits, y=y, ws=ws, topk_ids=topk_ids, topk_w=topk_w)
     sg, su, sd = shared if shared is not None else (None, None, None)
+    _on_device(x=x, logits=logits, gate=gate, up=up, down=down, shared_gate=sg, shared_up=su, shared_down=sd, y=y,
+               ws=ws, topk_ids=topk_ids, topk_w=topk_w)
     _check(load_library().w4a16_moe_decode(_ptr(x), _dtype_code(x), M, _ptr(logits), top_k, _dref(gate), _dref(up),
                                            _dref(down), _dref(sg), _dref(su), _dref(sd), _ptr(topk_ids), _ptr(topk_w),
                                            _ptr(y), yt, _ptr(ws), _nbytes(ws), _stream(stream)), "w4a16_moe_decode")
