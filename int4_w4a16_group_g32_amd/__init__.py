@@ -151,6 +151,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:  # the current stream's handle, without a Stream object around it (0.4 us for 2.9)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream.device_index != _current_device():
+        raise ValueError(f"stream is of device {stream.device_index}, the current device is {_current_device()}")
     return stream.cuda_stream
 
 
@@ -178,14 +180,26 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _on_device(**tensors):
-    """Every tensor the library reads or writes must be device memory, a Weight's codes and scales too."""
-    for name, t in tensors.items():
-        if isinstance(t, Weight):
-            if not (t.qw.is_cuda and t.scales.is_cuda):
-                raise ValueError(f"{name} must be on the device, got {t.qw.device}, {t.scales.device}")
-        elif isinstance(t, torch.Tensor) and not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    """Every tensor the library reads or writes, a Weight's codes and scales too, must be memory of the
+    current device: the calls launch there, on one of its streams."""
+    dev = None
+    for name, v in tensors.items():
+        for t in (v.qw, v.scales) if isinstance(v, Weight) else (v,):
+            if not isinstance(t, torch.Tensor):
+                continue
+            d = t.get_device()
+            if d == dev:
+                continue
+            if d < 0:
+                raise ValueError(f"{name} must be a device tensor, got {t.device}")
+            dev = _current_device()
+            if d != dev:
+                raise ValueError(f"{name} is on device {d}, the current device is {dev}")
 
 
 def _need_x(x: torch.Tensor, K: int):
@@ -247,6 +261,7 @@ def _dref(w):
 # ---------------------------------------------------------------- format
 
 def workspace_init(ws: torch.Tensor, stream=None):
+    _on_device(ws=ws)
     _check(load_library().w4a16_workspace_init(_ptr(ws), ws.numel() * ws.element_size(),
                                                 _stream(stream)), "w4a16_workspace_init")
 
@@ -489,7 +504,8 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate: Weight, 
 def new_workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
     """A zero-filled workspace of at least `nbytes` bytes (16-byte aligned by torch)."""
     ws = torch.empty(max(16, (int(nbytes) + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    workspace_init(ws, stream)
+    with torch.cuda.device(ws.device):
+        workspace_init(ws, stream)
     return ws
 
 

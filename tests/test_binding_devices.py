@@ -1,6 +1,8 @@
-"""CPU checks that the Python binding hands the library device memory only: weights, codes and
-scales too, on every compute call.  The tensors that are in order are host tensors that
-answer as device ones, and the library must not be reached."""
+"""CPU checks that the Python binding hands the library memory of the current device only:
+weights, codes and scales too, on every compute call.  The tensors that are in order are
+host tensors that answer as device ones, and the library must not be reached."""
+import types
+
 import pytest
 import torch
 
@@ -12,9 +14,14 @@ H, I, E, M, K_TOP = 64, 128, 4, 3, 2
 class OnDevice(torch.Tensor):
     """A host tensor that says it is on device 0."""
     is_cuda = property(lambda self: True)
+    index = 0
 
     def get_device(self):
-        return 0
+        return self.index
+
+
+class OnAnother(OnDevice):
+    index = 1
 
 
 def _t(shape, dtype=torch.float32):
@@ -84,18 +91,47 @@ def _variants(args, change):
             yield name, dict(args, **{name: change(v)})
 
 
-@pytest.mark.parametrize("name", list(_calls()))
-def test_host_memory_is_refused(name, monkeypatch):
+def _refuses(name, change, monkeypatch, current=0):
+    """The call goes through as it is, and refuses any one tensor changed."""
     monkeypatch.setattr(L, "load_library", _reached)
     monkeypatch.setattr(L, "_stream", lambda stream: 0)
+    monkeypatch.setattr(L, "_current_device", lambda: current, raising=False)
     call, args = _calls()[name]
     with pytest.raises(Reached):
         call(**args)
-    for what, bad in _variants(args, lambda t: t.as_subclass(torch.Tensor)):
+    for what, bad in _variants(args, change):
         try:
             call(**bad)
         except ValueError:
             continue
         except Reached:
             pass
-        pytest.fail(f"{name}: {what} in host memory went through")
+        pytest.fail(f"{name}: {what} went through")
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_host_memory_is_refused(name, monkeypatch):
+    _refuses(name, lambda t: t.as_subclass(torch.Tensor), monkeypatch)
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_memory_of_another_device_is_refused(name, monkeypatch):
+    _refuses(name, lambda t: t.as_subclass(OnAnother), monkeypatch)
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_a_device_that_is_not_current_is_refused(name, monkeypatch):
+    monkeypatch.setattr(L, "load_library", _reached)
+    monkeypatch.setattr(L, "_stream", lambda stream: 0)
+    monkeypatch.setattr(L, "_current_device", lambda: 1, raising=False)
+    call, args = _calls()[name]
+    with pytest.raises(ValueError):
+        call(**args)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(L, "_current_device", lambda: 1, raising=False)
+    of = lambda d: types.SimpleNamespace(device_index=d, cuda_stream=0x70)  # noqa: E731
+    assert L._stream(of(1)) == 0x70
+    with pytest.raises(ValueError):
+        L._stream(of(0))
