@@ -293,7 +293,11 @@ W4A16_API size_t w4a16_gemm_lora_workspace_bytes(int32_t M, const w4a16_weight_t
 /*
  * w4a16_gemm with an adapter for each row: y[M][N] as above, of type yt
  * (float32, or bf16 rounded once, to nearest even).  x, W and the first term
- * are as in w4a16_gemm (to its accuracy, not bitwise).  The adapters' products
+ * are as in w4a16_gemm, not bitwise; x enters it as f16 pieces scaled by one
+ * power of two per row at every row count, as in that call's tiles (its few-row
+ * form follows the row in windows): float32 values to within 2^-22 of
+ * themselves plus 2^-39 of the row's largest magnitude, bf16 values exactly
+ * from 2^-31 of it on and to within 2^-39 of it below.  The adapters' products
  * keep every bit of x, a, b and x a^T and sum in float32: row by row in fused
  * multiply-adds for up to 64 rows, and up to 512 while M * rank <= 16384;
  * above that in blocks of 64 rows on the matrix cores, where a float32 x, and
@@ -443,9 +447,11 @@ W4A16_API size_t w4a16_moe_decode_workspace_bytes(int32_t M, int32_t top_k, w4a1
  * summed in ascending expert index, the shared expert last; y is of type yt
  * (float32, or bf16 rounded once, to nearest even).  The weights are streamed
  * once whatever the tokens choose, and the choice needs no launch of its own.
- * h = silu(gate) up stays float32 until the down projection takes it, times
- * its gate weight, as f16 pieces (two with float32 x, one with bf16 x) scaled
- * by a power of two.  Deterministic, but not bitwise w4a16_moe_grouped.
+ * x enters the gate and up projections as in w4a16_gemm_lora.  h = silu(gate)
+ * up stays float32 until the down projection takes it, times its gate weight,
+ * as f16 pieces (two with float32 x: 22 significant bits, one with bf16 x: 11)
+ * scaled by one power of two per token over all its experts.  Deterministic,
+ * but not bitwise w4a16_moe_grouped.
  * logits [M][E] float32: a NaN counts as -infinity.  The k largest, ties in
  * ascending expert index, as in w4a16_moe_topk, also where they are infinite:
  * an expert at -infinity has weight 0, +infinity counts as the largest finite

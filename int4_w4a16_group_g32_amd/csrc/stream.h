@@ -8,7 +8,9 @@
 //
 // Rows are staged in LDS as f16 pieces of x * 2^e, with one power of two per
 // row that puts its largest magnitude in [2^14, 2^15): two pieces for float32
-// values (22 significant bits), one for bf16 ones (exact).  Row m of x is A
+// values (22 significant bits), one for bf16 ones (all 8; f16's smallest is
+// 2^-24, so both hold values to within 2^-39 of the row's largest at best, and
+// bf16 ones exactly from 2^-31 of it on).  Row m of x is A
 // row 4 (m & 3) + (m >> 2), or with two pieces 4 (m & 3) + 2 (m >> 2) + piece,
 // so that element i of a lane's result (A row 4 (lane >> 4) + i) belongs to
 // row (lane >> 4) + 4 i: up to four rows need one accumulator per column and
