@@ -1402,8 +1402,9 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
   Carve c;
   size_t counters;
   c.take(counters, kCounterBytes);
+  // (h of a bf16 layer keeps two pieces up to 8 rows)
+  p.pieces = x_f32 && M <= kMaxGemvRows ? 2 : mfma_pieces(lt);
   if (M <= gemv_rows(lt)) {
-    p.pieces = x_f32 && M <= kMaxGemvRows ? 2 : 1;
     p.st = plan_lora_stream(M, p.pieces, N, w1 != nullptr ? 2 : 1, K);
     p.stream = p.st.ok;  // (else K is too long for the windows of 32 splits)
   }
@@ -1416,7 +1417,6 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
     p.bytes = c.cursor;
     return p;
   }
-  p.pieces = mfma_pieces(lt);
   if (M <= 64) {
     p.tl = plan_lora_tiles(M, p.pieces, N, w1 != nullptr ? 2 : 1, K);
     p.rows64 = p.tl.ok;
@@ -1428,6 +1428,7 @@ LinearPlan plan_linear(int M, w4a16_dtype_t lt, bool x_f32, const w4a16_weight_t
     p.bytes = c.cursor;
     return p;
   }
+  p.pieces = mfma_pieces(lt);
   p.mf = plan_mfma(M, N, w1 != nullptr ? 1 : 0, K, lt, w1 == nullptr);
   if (w1 != nullptr && p.mf.S == 1) {
     p.pair = true;
