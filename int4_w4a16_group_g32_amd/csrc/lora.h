@@ -103,7 +103,7 @@ struct LoraStreamArgs {
   int gshift;
   LoraSet s0, s1;
   const int* ids;
-  int cols, parts, splits, gpp, tiles;  // the plan
+  int cols, parts, splits, gpp;  // the plan
   float* partials;
   int* counters;
   void* out;

@@ -155,8 +155,11 @@ using PrepArgs = LoraPrep;
 
 template <int kXP, int kP>
 __device__ __forceinline__ void prep_row(const ShrinkArgs& a, const PrepArgs& p, int m) {
-  // chunks a thread keeps in registers; few float32 rows of a long K are read
-  // once (four rows of 18432: 7.4 -> 6.0 us), many rows want the occupancy
+  // Chunks a thread keeps in registers, by the number of pieces alone.  With ten,
+  // float32 rows of up to 20480 are read once (the head of four rows of 18432:
+  // 7.4 -> 6.0 us).  Many or short rows would want four: calls of 512 rows of
+  // 1024 values (rank 16) 28.8 against 27.2 us, of 7168 values 67.0 against 65.8,
+  // 64 rows the same.
   constexpr int kHold = kP == 2 ? 10 : 4;
   __shared__ uint32_t amax;
   const int tid = threadIdx.x, nc = a.K / 8;
@@ -336,7 +339,6 @@ __device__ __forceinline__ void row_dots(const float* t, const uint16_t* const b
 
 constexpr int kFinishThreads = 256;
 constexpr int kTileWaves = 8, kTileThreads = kTileWaves * kWave;
-template <int kP, int kRT>
 constexpr int kTileOcc = 4;  // waves a SIMD
 constexpr int kLoraUnits = 512;  // LDS units (16 bytes) per wave of the streamed product
 
@@ -947,7 +949,7 @@ __device__ __forceinline__ int tile_turn(int r) { return 0x78 >> (r >> 2 << 1) &
 // The vector units bound it: 64 scalings of 16 results, 36 steps of expansion
 // and 16 products a wave and group take 45 of the 55 with no loads at all.
 template <int kP, int kRT, int kParts>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(kTileOcc<kP, kRT>)))
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(kTileOcc)))
 void lora_tiles_kernel(const LoraTileArgs a) {
   constexpr int kCols = kTileWaves / kParts, kRows = 16 * kRT;
   constexpr int kGU = 4 * kP * kRows;                   // units of a group: [piece][row][k block]
@@ -1343,7 +1345,6 @@ w4a16_status_t launch_lora_stream(LoraStreamArgs a, const LoraStreamPlan& p, hip
   a.parts = p.parts;
   a.splits = p.splits;
   a.gpp = p.gpp;
-  a.tiles = p.tiles;
   const size_t blocks = static_cast<size_t>(p.tiles) * p.splits;
   if (blocks > 0x7fffffffu) return W4A16_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks)), threads(p.waves * kWave);
@@ -1479,9 +1480,9 @@ LoraPrep linear_prep(const LinearPlan& p, int M, int K, char* ws) {
   return r;
 }
 
-w4a16_status_t lora_linear(const LinearPlan& p, const void* x, w4a16_dtype_t xt, int M, const w4a16_weight_t* w0,
-                           const w4a16_weight_t* w1, const LoraSet& s0, const LoraSet& s1, const int* ids,
-                           const ShrinkShape& sh, void* out, w4a16_dtype_t ot, char* ws, hipStream_t stream) {
+w4a16_status_t lora_linear(const LinearPlan& p, int M, const w4a16_weight_t* w0, const w4a16_weight_t* w1,
+                           const LoraSet& s0, const LoraSet& s1, const int* ids, const ShrinkShape& sh, void* out,
+                           w4a16_dtype_t ot, char* ws, hipStream_t stream) {
   const int K = w0->K, N = w0->N;
   if (p.stream) {
     LoraStreamArgs a{};
@@ -1645,7 +1646,7 @@ extern "C" w4a16_status_t w4a16_gemm_lora(const void* x, w4a16_dtype_t xt, int32
   const LoraSet set = lora_set(lora, reinterpret_cast<float*>(b + p.t_off));
   st = launch_lora_head(x, xt, M, w->K, adapter_ids, &set, 1, p.sh, linear_prep(p.lin, M, w->K, b), stream);
   if (st != W4A16_OK) return st;
-  return lora_linear(p.lin, x, xt, M, w, nullptr, set, LoraSet{}, adapter_ids, p.sh, y, yt, b, stream);
+  return lora_linear(p.lin, M, w, nullptr, set, LoraSet{}, adapter_ids, p.sh, y, yt, b, stream);
 }
 
 extern "C" size_t w4a16_swiglu_mlp_lora_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_weight_t* gate,
@@ -1686,10 +1687,9 @@ extern "C" w4a16_status_t w4a16_swiglu_mlp_lora(const void* x, w4a16_dtype_t xt,
   const LoraSet d = lora_set(lora_down, reinterpret_cast<float*>(b + p.td_off));
   st = launch_lora_head(x, xt, M, H, adapter_ids, gu, 2, p.sh_gu, linear_prep(p.gu, M, H, b), stream);
   if (st != W4A16_OK) return st;
-  if ((st = lora_linear(p.gu, x, xt, M, gate, up, gu[0], gu[1], adapter_ids, p.sh_gu, h, W4A16_F32, b, stream)) !=
-      W4A16_OK)
-    return st;
+  st = lora_linear(p.gu, M, gate, up, gu[0], gu[1], adapter_ids, p.sh_gu, h, W4A16_F32, b, stream);
+  if (st != W4A16_OK) return st;
   st = launch_lora_head(h, W4A16_F32, M, I, adapter_ids, &d, 1, p.sh_d, linear_prep(p.dn, M, I, b), stream);
   if (st != W4A16_OK) return st;
-  return lora_linear(p.dn, h, W4A16_F32, M, down, nullptr, d, LoraSet{}, adapter_ids, p.sh_d, y, yt, b, stream);
+  return lora_linear(p.dn, M, down, nullptr, d, LoraSet{}, adapter_ids, p.sh_d, y, yt, b, stream);
 }
