@@ -944,10 +944,12 @@ __device__ __forceinline__ int tile_turn(int r) { return 0x78 >> (r >> 2 << 1) &
 // window, and writes the share that has arrived, so that nothing waits for the
 // last load.
 //
-// 64 bf16 rows through gate and up of 7168 x 18432: 55 to 62 us from box to
-// box, 2.7 to 3.0 TB/s of weights.
-// The vector units bound it: 64 scalings of 16 results, 36 steps of expansion
-// and 16 products a wave and group take 45 of the 55 with no loads at all.
+// 64 bf16 rows through gate and up of 7168 x 18432: 58 to 68 us in kernel
+// traces, from box to box, 2.4 to 2.8 TB/s of weights.  Issue bounds it rather
+// than loads: 64 scalings of 16 results, 36 steps of expansion and 16 products a
+// wave and group take four fifths of that with no loads at all; vector
+// instructions fill 49 % of the SIMDs' cycles, matrix ones 26 %, and waves wait
+// to issue for a third of theirs.
 template <int kP, int kRT, int kParts>
 __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(kTileOcc)))
 void lora_tiles_kernel(const LoraTileArgs a) {
