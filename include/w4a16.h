@@ -18,6 +18,8 @@
  *    16-byte aligned.  Descriptors (w4a16_weight_t) and out-descriptors are
  *    HOST pointers.  The library never allocates or frees device memory and
  *    never synchronises the stream.
+ *  - Tensors, workspace and stream belong to the current device (not checked
+ *    here; the Python binding refuses others).
  *  - Work is enqueued asynchronously on `stream`.  The returned status covers
  *    host-side argument checks and launch errors only; a fault inside a kernel
  *    surfaces at the caller's next synchronisation.
