@@ -945,7 +945,7 @@ __device__ __forceinline__ int tile_turn(int r) { return 0x78 >> (r >> 2 << 1) &
 // last load.
 //
 // 64 bf16 rows through gate and up of 7168 x 18432: 58 to 68 us in kernel
-// traces, from box to box, 2.4 to 2.8 TB/s of weights.  Issue bounds it rather
+// traces, from card to card, 2.4 to 2.8 TB/s of weights.  Issue bounds it rather
 // than loads: 64 scalings of 16 results, 36 steps of expansion and 16 products a
 // wave and group take four fifths of that with no loads at all; vector
 // instructions fill 49 % of the SIMDs' cycles, matrix ones 26 %, and waves wait
