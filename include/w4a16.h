@@ -493,6 +493,171 @@ W4A16_API w4a16_status_t w4a16_moe_grouped_timed(
     const w4a16_weight_t* down, float* y, void* ws, size_t ws_bytes, hipStream_t stream,
     hipEvent_t* events, int32_t capacity, int32_t* recorded);
 
+/*
+ * MXFP4 matrices (OCP microscaling): 4-bit floating point values E2M1 (codes
+ * 0 .. 7 are 0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 is the sign) with one scale byte
+ * E8M0 per block of 32 values along K: a value is e2m1(code) * 2^(byte - 127),
+ * and byte 255 makes its block NaN.  A matrix has `rows` rows of K values: the
+ * rows of activations, or a weight's output columns (y = x W^T, the order in
+ * which such weights are saved).
+ *  ROWS:  codes[rows][K/2], the lower k in the low half of a byte, and
+ *         scales[rows][K/32].  The interchange format: what the quantisers
+ *         write, and the only layout of activations.
+ *  TILED: what the products stream; w4a16_mx_prepack converts.  Rows are padded
+ *         to 64 and K to 128 with zeros (scale byte 127).  codes
+ *         [rows/64][K/128][4][64][16]: for 64-row tile J and step s, the 16
+ *         bytes at [c][16 b + i] are row 64 J + 16 c + i, k 128 s + 32 b .. + 31;
+ *         scales [rows/64][K/128][64][4]: byte [16 b + i][c] is that block's.
+ *         Its rows are a multiple of 16.
+ * K is a multiple of 32 and at most 2^20, rows at most 2^24, rows * K at most
+ * 2^34.  Pointers may be NULL where rows or K is 0.
+ */
+typedef enum { W4A16_MX_ROWS = 0, W4A16_MX_TILED = 1 } w4a16_mx_layout_t;
+
+typedef struct {
+  const uint8_t* codes;  /* device */
+  const uint8_t* scales; /* device */
+  int32_t rows;
+  int32_t K;
+  w4a16_mx_layout_t layout;
+} w4a16_mx_t;
+
+/* Bytes of the codes and of the scales of a matrix (0 for a shape outside the limits above). */
+W4A16_API size_t w4a16_mx_codes_bytes(int32_t rows, int32_t K, w4a16_mx_layout_t layout);
+W4A16_API size_t w4a16_mx_scales_bytes(int32_t rows, int32_t K, w4a16_mx_layout_t layout);
+
+/*
+ * Quantise x[rows][K] (float32 or bf16) to MXFP4 in the ROWS layout: per block,
+ * scale 2^(floor(log2 max|x|) - 2), at least 2^-127, and codes the value of
+ * x / scale rounded to nearest, ties to the even code, at most 6, with x's sign.
+ * A block of zeros has byte 0, one with an infinity or NaN byte 255 and codes 0.
+ * Errors: INVALID_ARG (null/misaligned pointers, rows or K < 0, unknown type,
+ * an output smaller than w4a16_mx_codes_bytes / w4a16_mx_scales_bytes),
+ * UNSUPPORTED (the limits above); nothing is enqueued then.
+ */
+W4A16_API w4a16_status_t w4a16_mx_quantize(const void* x, w4a16_dtype_t xt, int32_t rows, int32_t K, uint8_t* codes,
+                                           size_t codes_bytes, uint8_t* scales, size_t scales_bytes,
+                                           hipStream_t stream);
+
+/*
+ * The same for weights w[K][N] (float32 or bf16, the order w4a16_quantize
+ * takes): blocks run along K, and the result is the ROWS matrix of N rows.
+ */
+W4A16_API w4a16_status_t w4a16_mx_quantize_weight(const void* w, w4a16_dtype_t wt, int32_t K, int32_t N,
+                                                  uint8_t* codes, size_t codes_bytes, uint8_t* scales,
+                                                  size_t scales_bytes, hipStream_t stream);
+
+/*
+ * ROWS -> TILED, into dst_codes and dst_scales (w4a16_mx_codes_bytes and
+ * w4a16_mx_scales_bytes of the TILED layout); `out` receives the descriptor.
+ * Errors: INVALID_ARG (null/misaligned, too small, overlapping), UNSUPPORTED
+ * (src not ROWS, rows not a multiple of 16, the limits above).
+ */
+W4A16_API w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_codes, size_t dst_codes_bytes,
+                                          uint8_t* dst_scales, size_t dst_scales_bytes, w4a16_mx_t* out,
+                                          hipStream_t stream);
+
+/*
+ * out[rows][K] = the values, as float32 (exact) or bf16 (exact too, but for
+ * magnitudes above bf16's largest), from either layout.  Errors as
+ * w4a16_dequantize.
+ */
+W4A16_API w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4a16_dtype_t ot, size_t out_bytes,
+                                             hipStream_t stream);
+
+/* Bytes of workspace w4a16_mx_gemm needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_mx_gemm_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_mx_t* w);
+
+/*
+ * y[M][N] = x[M][K] W^T for a TILED weight of N rows, x float32 or bf16, y
+ * float32, or bf16 rounded once, to nearest even.  Weights and rows enter the
+ * matrix cores as exact bf16 values (a float32 value as three whose sum it is),
+ * sums are float32.  Rows do not affect one another: an infinity or NaN in x[m]
+ * reaches y[m] only (an infinity among float32 values as NaN).  Deterministic:
+ * the same inputs give bitwise the same y.
+ * Errors: INVALID_ARG (null/misaligned, M < 0, unknown type, y aliasing x),
+ * UNSUPPORTED (layout, rows % 16, the limits above, M * N above 2^34),
+ * WORKSPACE, HIP.
+ */
+W4A16_API w4a16_status_t w4a16_mx_gemm(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_mx_t* w, void* y,
+                                       w4a16_dtype_t yt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_mx_gemm_a4 needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_mx_gemm_a4_workspace_bytes(int32_t M, const w4a16_mx_t* w);
+
+/*
+ * y[M][N] = x W^T with MXFP4 rows x (ROWS, M = x->rows, x->K == w->K): both
+ * operands 4-bit on the scaled matrix-core instructions, float32 sums.  Errors
+ * as w4a16_mx_gemm.
+ */
+W4A16_API w4a16_status_t w4a16_mx_gemm_a4(const w4a16_mx_t* x, const w4a16_mx_t* w, void* y, w4a16_dtype_t yt,
+                                          void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_mx_swiglu_mlp needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_mx_swiglu_mlp_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_mx_t* gate,
+                                                     const w4a16_mx_t* up, const w4a16_mx_t* down);
+
+/*
+ * w4a16_swiglu_mlp over MXFP4 weights: y = (silu(x Wg^T) * (x Wu^T)) Wd^T, gate
+ * and up TILED with I rows of H, down with H rows of I; x and y as in
+ * w4a16_mx_gemm.  h = silu(gate) up enters the down product whole with float32
+ * x, and to within 2^-16 of each value (two bf16 pieces) with bf16 x.
+ * Errors as w4a16_mx_gemm, plus UNSUPPORTED if the three shapes do not chain.
+ */
+W4A16_API w4a16_status_t w4a16_mx_swiglu_mlp(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_mx_t* gate,
+                                             const w4a16_mx_t* up, const w4a16_mx_t* down, void* y, w4a16_dtype_t yt,
+                                             void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_mx_swiglu_mlp_a4 needs (0 for invalid arguments). */
+W4A16_API size_t w4a16_mx_swiglu_mlp_a4_workspace_bytes(int32_t M, const w4a16_mx_t* gate, const w4a16_mx_t* up,
+                                                        const w4a16_mx_t* down);
+
+/*
+ * The same with MXFP4 rows x (ROWS): h is rounded to MXFP4 rows as
+ * w4a16_mx_quantize rounds, from float32, and both products run on 4-bit
+ * operands.
+ */
+W4A16_API w4a16_status_t w4a16_mx_swiglu_mlp_a4(const w4a16_mx_t* x, const w4a16_mx_t* gate, const w4a16_mx_t* up,
+                                                const w4a16_mx_t* down, void* y, w4a16_dtype_t yt, void* ws,
+                                                size_t ws_bytes, hipStream_t stream);
+
+/* Longest row w4a16_block_norm takes. */
+#define W4A16_NORM_MAX_H 32768
+
+/*
+ * What a layer does between two blocks, in one pass over the rows:
+ *   s = r + alpha * gate * post(y),  post(y) = y / sqrt(mean(y^2) + eps) * post_w
+ *   n = s / sqrt(mean(s^2) + eps) * pre_w
+ * y is the block's output, r the residual stream, n the next block's input.
+ * s is rounded to float32 and then to r_type (r and r_out have it) before its
+ * norm is taken, stored or not.  Without post_w, post(y) = y; without gate, 1; without r, 0.
+ */
+typedef struct {
+  const void* y;         /* device: [M][H] of y_type */
+  const void* r;         /* device: [M][H] of r_type, or NULL */
+  void* r_out;           /* device: s, [M][H] of r_type, or NULL; may be r */
+  const void* post_w;    /* device: [H] of w_type, or NULL */
+  const void* pre_w;     /* device: [H] of w_type (unused without n) */
+  const void* gate;      /* device: [gate_rows][H] of w_type, or NULL */
+  int32_t gate_rows;     /* 1 (one gate for every row) or M */
+  void* n;               /* device: [M][H] of n_type, or NULL */
+  uint8_t* n_codes;      /* device: n as MXFP4 ROWS instead, as w4a16_mx_quantize rounds; */
+  uint8_t* n_scales;     /*         both or neither, and then n is NULL */
+  w4a16_dtype_t y_type, r_type, w_type, n_type;
+  double alpha, eps;
+} w4a16_norm_t;
+
+/*
+ * Means and products are float32, with MXFP4 rows float64 (their codes then do
+ * not depend on the order of a sum).  Rows do not
+ * affect one another.  Errors: INVALID_ARG (p or y NULL, pre_w NULL with n,
+ * neither r_out nor n, one of n_codes and n_scales alone or both beside n,
+ * misaligned, unknown type, gate_rows not 1 or M, an output that overlaps an
+ * input, other than r_out == r, or another output), UNSUPPORTED (H not a multiple of 8, with MXFP4 rows 32,
+ * or above W4A16_NORM_MAX_H; M above 2^24).
+ */
+W4A16_API w4a16_status_t w4a16_block_norm(const w4a16_norm_t* p, int32_t M, int32_t H, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

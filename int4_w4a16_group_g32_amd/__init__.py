@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_PKG_DIR, "libw4a16.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
 F32, BF16 = 0, 1
+MXFP4 = 2  # activations given as an MxMatrix (the binding's own code, not the library's)
+MX_ROWS, MX_TILED = 0, 1
 LAYOUT_CANONICAL, LAYOUT_GROUPED = 0, 1
 GROUP = 32
 
@@ -50,6 +52,21 @@ EXPORTS = (
     "w4a16_moe_decode_workspace_bytes",
     "w4a16_moe_decode",
     "w4a16_moe_grouped_timed",
+    "w4a16_mx_codes_bytes",
+    "w4a16_mx_scales_bytes",
+    "w4a16_mx_quantize",
+    "w4a16_mx_quantize_weight",
+    "w4a16_mx_prepack",
+    "w4a16_mx_dequantize",
+    "w4a16_mx_gemm_workspace_bytes",
+    "w4a16_mx_gemm",
+    "w4a16_mx_gemm_a4_workspace_bytes",
+    "w4a16_mx_gemm_a4",
+    "w4a16_mx_swiglu_mlp_workspace_bytes",
+    "w4a16_mx_swiglu_mlp",
+    "w4a16_mx_swiglu_mlp_a4_workspace_bytes",
+    "w4a16_mx_swiglu_mlp_a4",
+    "w4a16_block_norm",
 )
 
 
@@ -82,6 +99,37 @@ class LoraDesc(ctypes.Structure):
     ]
 
 
+class MxDesc(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("y", ctypes.c_void_p),
+        ("r", ctypes.c_void_p),
+        ("r_out", ctypes.c_void_p),
+        ("post_w", ctypes.c_void_p),
+        ("pre_w", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_rows", ctypes.c_int32),
+        ("n", ctypes.c_void_p),
+        ("n_codes", ctypes.c_void_p),
+        ("n_scales", ctypes.c_void_p),
+        ("y_type", ctypes.c_int32),
+        ("r_type", ctypes.c_int32),
+        ("w_type", ctypes.c_int32),
+        ("n_type", ctypes.c_int32),
+        ("alpha", ctypes.c_double),
+        ("eps", ctypes.c_double),
+    ]
+
+
 _lib = None
 
 
@@ -95,6 +143,7 @@ def load_library() -> ctypes.CDLL:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         dp = ctypes.POINTER(WeightDesc)
         lp = ctypes.POINTER(LoraDesc)
+        mp = ctypes.POINTER(MxDesc)
         sig = {
             "w4a16_status_string": (ctypes.c_char_p, [i32]),
             "w4a16_workspace_init": (i32, [vp, sz, vp]),
@@ -126,6 +175,21 @@ def load_library() -> ctypes.CDLL:
             "w4a16_moe_decode": (i32, [vp, i32, i32, vp, i32, dp, dp, dp, dp, dp, dp, vp, vp, vp, i32, vp, sz, vp]),
             "w4a16_moe_grouped_timed": (i32, [vp, i32, i32, vp, vp, i32, dp, dp, dp, vp, vp, sz, vp, vp,
                                               i32, ctypes.POINTER(i32)]),
+            "w4a16_mx_codes_bytes": (sz, [i32, i32, i32]),
+            "w4a16_mx_scales_bytes": (sz, [i32, i32, i32]),
+            "w4a16_mx_quantize": (i32, [vp, i32, i32, i32, vp, sz, vp, sz, vp]),
+            "w4a16_mx_quantize_weight": (i32, [vp, i32, i32, i32, vp, sz, vp, sz, vp]),
+            "w4a16_mx_prepack": (i32, [mp, vp, sz, vp, sz, mp, vp]),
+            "w4a16_mx_dequantize": (i32, [mp, vp, i32, sz, vp]),
+            "w4a16_mx_gemm_workspace_bytes": (sz, [i32, i32, mp]),
+            "w4a16_mx_gemm": (i32, [vp, i32, i32, mp, vp, i32, vp, sz, vp]),
+            "w4a16_mx_gemm_a4_workspace_bytes": (sz, [i32, mp]),
+            "w4a16_mx_gemm_a4": (i32, [mp, mp, vp, i32, vp, sz, vp]),
+            "w4a16_mx_swiglu_mlp_workspace_bytes": (sz, [i32, i32, mp, mp, mp]),
+            "w4a16_mx_swiglu_mlp": (i32, [vp, i32, i32, mp, mp, mp, vp, i32, vp, sz, vp]),
+            "w4a16_mx_swiglu_mlp_a4_workspace_bytes": (sz, [i32, mp, mp, mp]),
+            "w4a16_mx_swiglu_mlp_a4": (i32, [mp, mp, mp, mp, vp, i32, vp, sz, vp]),
+            "w4a16_block_norm": (i32, [ctypes.POINTER(NormDesc), i32, i32, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -189,7 +253,7 @@ def _on_device(**tensors):
     current device: the calls launch there, on one of its streams."""
     dev = None
     for name, v in tensors.items():
-        for t in (v.qw, v.scales) if isinstance(v, Weight) else (v,):
+        for t in (v.qw, v.scales) if isinstance(v, Weight) else (v.codes, v.scales) if isinstance(v, MxMatrix) else (v,):
             if not isinstance(t, torch.Tensor):
                 continue
             d = t.get_device()
@@ -223,6 +287,31 @@ class Weight:
     def desc(self) -> WeightDesc:
         return WeightDesc(self.qw.data_ptr(), self.scales.data_ptr(), self.K, self.N, self.group_size,
                           self.num_experts, self.layout)
+
+
+@dataclass
+class MxMatrix:
+    """An MXFP4 matrix of `rows` rows of K values: activations, or a weight's output columns."""
+    codes: torch.Tensor   # uint8, ROWS [rows][K/2] or TILED
+    scales: torch.Tensor  # uint8, ROWS [rows][K/32] or TILED
+    rows: int
+    K: int
+    layout: int = MX_ROWS
+
+    def desc(self) -> MxDesc:
+        return MxDesc(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K, self.layout)
+
+    def check(self, name: str):
+        """The tensors' dtypes, sizes and devices for the shape."""
+        _need(self.codes, f"{name}.codes", torch.uint8)
+        _need(self.scales, f"{name}.scales", torch.uint8)
+        lib = load_library()
+        need = (lib.w4a16_mx_codes_bytes(self.rows, self.K, self.layout),
+                lib.w4a16_mx_scales_bytes(self.rows, self.K, self.layout))
+        if (self.codes.numel(), self.scales.numel()) != need:
+            raise ValueError(f"{name}: codes and scales must have {need[0]} and {need[1]} bytes for {self.rows} rows of "
+                             f"{self.K}, got {self.codes.numel()} and {self.scales.numel()}")
+        _on_device(**{name: self})
 
 
 @dataclass
@@ -497,6 +586,182 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate: Weight, 
     _check(load_library().w4a16_moe_decode(_ptr(x), _dtype_code(x), M, _ptr(logits), top_k, _dref(gate), _dref(up),
                                            _dref(down), _dref(sg), _dref(su), _dref(sd), _ptr(topk_ids), _ptr(topk_w),
                                            _ptr(y), yt, _ptr(ws), _nbytes(ws), _stream(stream)), "w4a16_moe_decode")
+
+
+# ---------------------------------------------------------------- MXFP4
+
+def mx_empty(rows: int, K: int, layout: int = MX_ROWS, device="cuda") -> MxMatrix:
+    """An uninitialised MXFP4 matrix."""
+    lib = load_library()
+    nc, ns = lib.w4a16_mx_codes_bytes(rows, K, layout), lib.w4a16_mx_scales_bytes(rows, K, layout)
+    if rows < 0 or K < 0 or (rows and K and nc == 0):
+        raise ValueError(f"no MXFP4 matrix of {rows} rows of {K} in layout {layout}")
+    codes = torch.empty((rows, K // 2) if layout == MX_ROWS else (nc,), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, K // 32) if layout == MX_ROWS else (ns,), dtype=torch.uint8, device=device)
+    return MxMatrix(codes, scales, rows, K, layout)
+
+
+def _need_mx_out(out: MxMatrix, name: str, rows: int, K: int):
+    out.check(name)
+    if (out.rows, out.K, out.layout) != (rows, K, MX_ROWS):
+        raise ValueError(f"{name} must be {rows} rows of {K} in ROWS, got {out.rows} of {out.K} in layout {out.layout}")
+
+
+def mx_quantize(x: torch.Tensor, out: MxMatrix, stream=None):
+    """x float32 or bfloat16 [rows][K] -> MXFP4 (ROWS)."""
+    xt = _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows][K], got {tuple(x.shape)}")
+    _need(x, "x", x.dtype)
+    _need_mx_out(out, "out", *x.shape)
+    _on_device(x=x)
+    _check(load_library().w4a16_mx_quantize(_ptr(x), xt, x.shape[0], x.shape[1], _ptr(out.codes), _nbytes(out.codes),
+                                            _ptr(out.scales), _nbytes(out.scales), _stream(stream)),
+           "w4a16_mx_quantize")
+
+
+def mx_quantize_weight(w: torch.Tensor, out: MxMatrix, stream=None):
+    """Weights w float32 or bfloat16 [K][N] -> MXFP4 rows of the transpose (ROWS, N rows of K)."""
+    wt = _dtype_code(w)
+    if w.dim() != 2:
+        raise ValueError(f"w must be [K][N], got {tuple(w.shape)}")
+    _need(w, "w", w.dtype)
+    _need_mx_out(out, "out", w.shape[1], w.shape[0])
+    _on_device(w=w)
+    _check(load_library().w4a16_mx_quantize_weight(_ptr(w), wt, w.shape[0], w.shape[1], _ptr(out.codes),
+                                                   _nbytes(out.codes), _ptr(out.scales), _nbytes(out.scales),
+                                                   _stream(stream)), "w4a16_mx_quantize_weight")
+
+
+def mx_prepack(src: MxMatrix, dst: MxMatrix, stream=None) -> MxMatrix:
+    """ROWS -> TILED, the layout the products stream, into dst's tensors; returns dst."""
+    src.check("src")
+    dst.check("dst")
+    if (dst.rows, dst.K, dst.layout) != (src.rows, src.K, MX_TILED):
+        raise ValueError(f"dst must be {src.rows} rows of {src.K} in TILED")
+    out = MxDesc()
+    _check(load_library().w4a16_mx_prepack(ctypes.byref(src.desc()), _ptr(dst.codes), _nbytes(dst.codes),
+                                           _ptr(dst.scales), _nbytes(dst.scales), ctypes.byref(out), _stream(stream)),
+           "w4a16_mx_prepack")
+    return dst
+
+
+def mx_dequantize(m: MxMatrix, out: torch.Tensor, stream=None):
+    """The values of m [rows][K], either layout, as float32 or bfloat16."""
+    m.check("m")
+    _need(out, "out", out.dtype, (m.rows, m.K))
+    _on_device(out=out)
+    _check(load_library().w4a16_mx_dequantize(ctypes.byref(m.desc()), _ptr(out), _dtype_code(out), _nbytes(out),
+                                              _stream(stream)), "w4a16_mx_dequantize")
+
+
+def mx_quantize_to_weight(w: torch.Tensor, stream=None) -> MxMatrix:
+    """Quantize device weights [K][N] and prepack them (TILED)."""
+    K, N = w.shape
+    rows = mx_empty(N, K, MX_ROWS, w.device)
+    mx_quantize_weight(w, rows, stream)
+    return mx_prepack(rows, mx_empty(N, K, MX_TILED, w.device), stream)
+
+
+def mx_gemm_workspace_bytes(M: int, xt: int, w: MxMatrix) -> int:
+    """xt: F32, BF16, or MXFP4 for activations given as an MxMatrix."""
+    lib = load_library()
+    if xt == MXFP4:
+        return lib.w4a16_mx_gemm_a4_workspace_bytes(M, ctypes.byref(w.desc()))
+    return lib.w4a16_mx_gemm_workspace_bytes(M, xt, ctypes.byref(w.desc()))
+
+
+def mx_gemm(x, w: MxMatrix, y: torch.Tensor, ws: torch.Tensor, stream=None):
+    """y = x W^T over a TILED MXFP4 weight; x a float32 or bfloat16 tensor [M][K], or an MxMatrix (ROWS)."""
+    a4 = isinstance(x, MxMatrix)
+    w.check("w")
+    if a4:
+        x.check("x")
+    else:
+        _need_x(x, w.K)
+    M = x.rows if a4 else x.shape[0]
+    yt = _need_y(y, (M, w.rows))
+    _need(ws, "ws", torch.uint8)
+    _on_device(x=x, y=y, ws=ws)
+    lib = load_library()
+    if a4:
+        _check(lib.w4a16_mx_gemm_a4(ctypes.byref(x.desc()), ctypes.byref(w.desc()), _ptr(y), yt, _ptr(ws), _nbytes(ws),
+                                    _stream(stream)), "w4a16_mx_gemm_a4")
+    else:
+        _check(lib.w4a16_mx_gemm(_ptr(x), _dtype_code(x), M, ctypes.byref(w.desc()), _ptr(y), yt, _ptr(ws), _nbytes(ws),
+                                 _stream(stream)), "w4a16_mx_gemm")
+
+
+def mx_swiglu_mlp_workspace_bytes(M: int, xt: int, gate: MxMatrix, up: MxMatrix, down: MxMatrix) -> int:
+    """xt: F32, BF16, or MXFP4 for activations given as an MxMatrix."""
+    lib, d = load_library(), [ctypes.byref(w.desc()) for w in (gate, up, down)]
+    if xt == MXFP4:
+        return lib.w4a16_mx_swiglu_mlp_a4_workspace_bytes(M, *d)
+    return lib.w4a16_mx_swiglu_mlp_workspace_bytes(M, xt, *d)
+
+
+def mx_swiglu_mlp(x, gate: MxMatrix, up: MxMatrix, down: MxMatrix, y: torch.Tensor, ws: torch.Tensor, stream=None):
+    """The SwiGLU MLP over TILED MXFP4 weights; x as in mx_gemm (with an MxMatrix, h is MXFP4 too)."""
+    a4 = isinstance(x, MxMatrix)
+    gate.check("gate"), up.check("up"), down.check("down")
+    if a4:
+        x.check("x")
+    else:
+        _need_x(x, gate.K)
+    M = x.rows if a4 else x.shape[0]
+    yt = _need_y(y, (M, down.rows))
+    _need(ws, "ws", torch.uint8)
+    _on_device(x=x, y=y, ws=ws)
+    lib, d = load_library(), [ctypes.byref(w.desc()) for w in (gate, up, down)]
+    if a4:
+        _check(lib.w4a16_mx_swiglu_mlp_a4(ctypes.byref(x.desc()), *d, _ptr(y), yt, _ptr(ws), _nbytes(ws),
+                                          _stream(stream)), "w4a16_mx_swiglu_mlp_a4")
+    else:
+        _check(lib.w4a16_mx_swiglu_mlp(_ptr(x), _dtype_code(x), M, *d, _ptr(y), yt, _ptr(ws), _nbytes(ws),
+                                       _stream(stream)), "w4a16_mx_swiglu_mlp")
+
+
+# ---------------------------------------------------------------- norms
+
+def block_norm(y: torch.Tensor, r: torch.Tensor | None = None, r_out: torch.Tensor | None = None, n=None, *,
+               pre_w: torch.Tensor | None = None, post_w: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, stream=None):
+    """Between two blocks, one pass: r_out = r + alpha * gate * post(y), post an RMS norm with post_w (None: y);
+    n = the RMS norm of r_out with pre_w.  y, r [M][H] float32 or bfloat16, r_out of r's type (y's without r; it
+    may be r), n float32, bfloat16 or an MxMatrix (ROWS); post_w, pre_w [H] and gate [H] or [M][H] of one type."""
+    yt = _dtype_code(y)
+    if y.dim() != 2:
+        raise ValueError(f"y must be [M][H], got {tuple(y.shape)}")
+    M, H = y.shape
+    _need(y, "y", y.dtype)
+    rtype = r.dtype if r is not None else r_out.dtype if r_out is not None else y.dtype
+    for t, name in ((r, "r"), (r_out, "r_out")):
+        if t is not None:
+            _dtype_code(t)
+            _need(t, name, rtype, (M, H))
+    weights = [t for t in (pre_w, post_w, gate) if t is not None]
+    wtype = weights[0].dtype if weights else y.dtype
+    for t, name in ((pre_w, "pre_w"), (post_w, "post_w")):
+        if t is not None:
+            _dtype_code(t)
+            _need(t, name, wtype, (H,))
+    gate_rows = 1
+    if gate is not None:
+        _dtype_code(gate)
+        gate_rows = M if gate.dim() == 2 else 1
+        _need(gate, "gate", wtype, (M, H) if gate.dim() == 2 else (H,))
+    code = {torch.float32: F32, torch.bfloat16: BF16}
+    mx = isinstance(n, MxMatrix)
+    if mx:
+        _need_mx_out(n, "n", M, H)
+    elif n is not None:
+        _dtype_code(n)
+        _need(n, "n", n.dtype, (M, H))
+    _on_device(y=y, r=r, r_out=r_out, n=n, pre_w=pre_w, post_w=post_w, gate=gate)
+    d = NormDesc(_ptr(y), _ptr(r), _ptr(r_out), _ptr(post_w), _ptr(pre_w), _ptr(gate), gate_rows,
+                 None if mx else _ptr(n), _ptr(n.codes) if mx else None, _ptr(n.scales) if mx else None, yt,
+                 code[rtype], code[wtype], F32 if mx or n is None else _dtype_code(n), alpha, eps)
+    _check(load_library().w4a16_block_norm(ctypes.byref(d), M, H, _stream(stream)), "w4a16_block_norm")
 
 
 # ---------------------------------------------------------------- helpers

@@ -29,3 +29,12 @@ from .lora import (  # noqa: F401
     lora_term64,
     swiglu_mlp_lora64,
 )
+from .mx import (  # noqa: F401
+    block_norm64,
+    mx_pack,
+    mx_quantize64,
+    mx_round64,
+    mx_swiglu_mlp64,
+    mx_tiled,
+    mx_values64,
+)
