@@ -53,17 +53,16 @@ __device__ __forceinline__ void put8(void* p, size_t i, int bf16, const float v[
   }
 }
 
-__device__ __forceinline__ float to_float(double v) { return static_cast<float>(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
-
-// The float next to v on v's own side where v is no float: a later rounding to
-// fewer bits then goes as v's own would.
-__device__ __forceinline__ float sided(double v) {
+// v as a float, or where v is none, the one of its two neighbours with an odd
+// last bit: a later rounding to few bits, whose borders are even, then goes as
+// v's own would.
+__device__ __forceinline__ float rounded_to_odd(double v) {
   const float f = static_cast<float>(v);
   const double a = fabs(v), b = fabs(static_cast<double>(f));
   const uint32_t u = __float_as_uint(f);
-  return b == a || !(b <= 3.4028234663852886e38) ? f : __uint_as_float(b > a ? u - 1 : u + 1);
+  return b == a || (u & 1) || !(b <= 3.4028234663852886e38) ? f : __uint_as_float(b > a ? u - 1 : u + 1);
 }
+
 template <typename F>
 __device__ __forceinline__ F row_sum(F v, F* lds) {
 #pragma unroll
@@ -132,7 +131,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(const NormArgs a) {
     float o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      o[j] = to_float(s[c][j]);
+      o[j] = static_cast<float>(s[c][j]);
       if (a.r_bf16) o[j] = bf16_to_f32(f32_to_bf16(o[j]));
       s[c][j] = o[j];
       q += s[c][j] * s[c][j];
@@ -173,7 +172,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(const NormArgs a) {
       const double inv = __longlong_as_double(static_cast<long long>(1023 + 127 - static_cast<int>(byte)) << 52);
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = b ? 0.0f : sided(v[j] * inv);
+      for (int j = 0; j < 8; ++j) o[j] = b ? 0.0f : rounded_to_odd(v[j] * inv);
       static_cast<uint32_t*>(a.n)[base + i] = mx_codes8(o);
       if ((i & 3) == 0) a.n_scales[(base + i) >> 2] = static_cast<uint8_t>(byte);
     }

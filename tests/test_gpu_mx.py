@@ -39,6 +39,23 @@ def test_quantize_is_exact(M, K, xt):
         assert torch.equal(v.cpu(), want)
 
 
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_quantize_next_to_the_borders(xt):
+    """Each border between two codes and the values one step of the type beside it."""
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]).to(TORCH[xt])
+    it = torch.int32 if xt == "f32" else torch.int16
+    steps = [(border.view(it) + d).view(TORCH[xt]) for d in (-2, -1, 0, 1, 2)]
+    v = torch.cat(steps + [-s for s in steps])  # 80 values
+    x = torch.full((3, 96), 4.0, dtype=TORCH[xt])
+    for r, e in enumerate((0, -120, 100)):
+        x[r, :31], x[r, 32:63], x[r, 64:82] = v[:31], v[31:62], v[62:]
+        x[r] = (x[r].double() * 2.0 ** e).to(TORCH[xt])
+    q, s = O.mx_quantize64(x.double().numpy())
+    m = L.mx_empty(3, 96)
+    L.mx_quantize(x.cuda(), m)
+    assert np.array_equal(m.scales.cpu().numpy(), s) and np.array_equal(m.codes.cpu().numpy(), O.mx_pack(q))
+
+
 @pytest.mark.parametrize("wt", ["f32", "bf16"])
 @pytest.mark.parametrize("K,N", [(32, 16), (160, 80), (1056, 208)])
 def test_weights_quantize_prepack_and_come_back(K, N, wt):

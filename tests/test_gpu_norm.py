@@ -71,6 +71,25 @@ def test_norm_to_mxfp4_is_exact(M, H, yt, rt, wt, post, gate):
     assert np.array_equal(n.scales.cpu().numpy(), sc) and np.array_equal(n.codes.cpu().numpy(), O.mx_pack(q))
 
 
+@pytest.mark.parametrize("st", ["f32", "bf16"])
+def test_norm_to_mxfp4_next_to_the_borders(st):
+    """Weights that put every n within a float32 step of a code's border, on either side."""
+    rng = np.random.default_rng(11)
+    H = 2048
+    y = torch.as_tensor(rng.standard_normal((1, H)) + np.sign(rng.standard_normal((1, H)))).to(TORCH[st])
+    s = _f(y)
+    pre = 1 / np.sqrt((s * s).mean() + 1e-6)
+    border = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], (1, H))
+    border[0, ::32] = 5.0  # the block's largest lies in [4, 8): scale 1
+    w = torch.as_tensor((border / (s * pre))[0]).float()
+    n = L.mx_empty(1, H)
+    L.block_norm(y.cuda(), n=n, pre_w=w.cuda())
+    _, nv = O.block_norm64(s, pre_w=w.double().numpy())
+    assert 0.3 < (np.abs(nv) < border).mean() < 0.7
+    q, sc = O.mx_quantize64(nv)
+    assert np.array_equal(n.scales.cpu().numpy(), sc) and np.array_equal(n.codes.cpu().numpy(), O.mx_pack(q))
+
+
 def test_rows_alone_zeros_and_values_that_are_not_finite():
     x = torch.randn((4, 64), device="cuda")
     x[1] = 0
