@@ -510,7 +510,7 @@ W4A16_API w4a16_status_t w4a16_moe_grouped_timed(
  *         scales [rows/64][K/128][64][4]: byte [16 b + i][c] is that block's.
  *         Its rows are a multiple of 16.
  * K is a multiple of 32 and at most 2^20, rows at most 2^24, rows * K at most
- * 2^34.  Pointers may be NULL where rows or K is 0.
+ * 2^33.  Pointers may be NULL where rows or K is 0.
  */
 typedef enum { W4A16_MX_ROWS = 0, W4A16_MX_TILED = 1 } w4a16_mx_layout_t;
 
@@ -576,7 +576,7 @@ W4A16_API size_t w4a16_mx_gemm_workspace_bytes(int32_t M, w4a16_dtype_t xt, cons
  * reaches y[m] only (an infinity among float32 values as NaN).  Deterministic:
  * the same inputs give bitwise the same y.
  * Errors: INVALID_ARG (null/misaligned, M < 0, unknown type, y aliasing x),
- * UNSUPPORTED (layout, rows % 16, the limits above, M * N above 2^34),
+ * UNSUPPORTED (layout, rows % 16, the limits above, M * N above 2^33),
  * WORKSPACE, HIP.
  */
 W4A16_API w4a16_status_t w4a16_mx_gemm(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_mx_t* w, void* y,

@@ -19,7 +19,7 @@ constexpr int kMxTileCodes = kMxTileRows * kMxStep / 2;          // bytes of a t
 constexpr int kMxTileScales = kMxTileRows * kMxStep / kMxBlock;  // bytes of its scales
 constexpr int kMxMaxK = 1 << 20;  // offsets inside one tile, or 256 activation rows, stay below 2^31
 constexpr int kMxMaxRows = 1 << 24;
-constexpr size_t kMxMaxValues = static_cast<size_t>(1) << 34;  // a launch's threads are counted in 32 bits
+constexpr size_t kMxMaxValues = static_cast<size_t>(1) << 33;  // a launch's threads are counted in 32 bits
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -96,6 +96,66 @@ __device__ __forceinline__ float mx_scale(uint32_t dword) {
   return __uint_as_float(c == 3 ? (dword >> 24) << 23 : ((dword >> (8 * c)) & 0xffu) << 23);
 }
 
+// Four adjacent outputs from element `at`.
+__device__ __forceinline__ void mx_store4(void* y, size_t at, int bf16, const f32x4& v) {
+  if (bf16) {
+    uint2 b;
+    b.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
+    b.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = b;
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = v;
+  }
+}
+
+// 32 columns of h from column n as MXFP4: the lane's 4 columns of each half
+// (row `row`, k block kb), the other three lanes of the row 16 lanes apart.
+__device__ __forceinline__ void mx_store_h(void* codes, uint8_t* scales, int row, int N, int n, int kb, bool row_ok,
+                                           const f32x4& lo, const f32x4& hi) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    m = max(m, max(__float_as_uint(lo[e]) & 0x7fffffffu, __float_as_uint(hi[e]) & 0x7fffffffu));
+  m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+  m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+  const uint32_t byte = mx_scale_byte(m);
+  const float inv = mx_scale_inverse(byte);
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = byte == 255 ? 0.0f : lo[e] * inv;
+    v[4 + e] = byte == 255 ? 0.0f : hi[e] * inv;
+  }
+  const uint32_t q = mx_codes8(v);
+  if (!row_ok || n >= N) return;
+  const size_t r = static_cast<size_t>(row);
+  uint16_t* o = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(codes) + r * (N / 2) + n / 2);
+  o[kb] = static_cast<uint16_t>(q);
+  o[4 + kb] = static_cast<uint16_t>(q >> 16);
+  if (kb == 0) scales[r * (N / kMxBlock) + n / kMxBlock] = static_cast<uint8_t>(byte);
+}
+
+// Four adjacent values as kN bf16 planes of `plane` elements: 8 significant
+// bits each, cut off, the last rounded to nearest (of three it is exact).
+template <int kN>
+__device__ __forceinline__ void mx_store_pieces(void* planes, size_t at, size_t plane, f32x4 v) {
+#pragma unroll
+  for (int p = 0; p < kN; ++p) {
+    if (p + 1 < kN) {
+      f32x4 cut;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cut[e] = __uint_as_float(__float_as_uint(v[e]) & 0xffff0000u);
+      uint2 b;
+      b.x = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302);
+      b.y = __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(planes) + p * plane + at) = b;
+      v -= cut;
+    } else {
+      mx_store4(planes, p * plane + at, 1, v);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- products
 
 // What the activations of a product are.
@@ -119,5 +179,22 @@ struct MxArgs {
 
 // Rows in blocks of 16, the whole K inside a workgroup (mx_stream.hip).
 hipError_t launch_mx_stream(MxX xk, bool glu, const MxArgs& a, hipStream_t stream);
+constexpr int kMxStreamRows = 16;
+
+// More rows, tiles of them in LDS (mx_tile.hip).  x: [M][K] bf16, or float32
+// rows as bf16 planes [pieces][M][K], or MXFP4 rows; y as in MxArgs, or with glu
+// h as bf16 planes or MXFP4 rows.
+struct MxTileArgs : MxArgs {
+  float* planes;  // splits > 1: [splits][matrices][M][N]
+  int tiles, splits, sps;
+};
+struct MxTilePlan {
+  int bm = 0, tiles = 0, splits = 1, sps = 0;
+  size_t plane_bytes = 0;  // all splits'
+};
+MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu);
+hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream);
+// float32 values as three bf16 planes of n values
+hipError_t launch_mx_pieces(const float* x, size_t n, void* out, hipStream_t stream);
 
 }  // namespace w4

@@ -5,6 +5,22 @@
 namespace w4 {
 namespace {
 
+// Tiles of `cols` columns, `bm` rows; K is split where the tiles alone leave
+// compute units idle.
+MxTilePlan tile_plan(int M, int N, int K, int bm, int cols, bool glu, int want) {
+  MxTilePlan p;
+  p.bm = bm;
+  p.tiles = (N + cols - 1) / cols;
+  const int S = (K + kMxStep - 1) / kMxStep;
+  const int tasks = p.tiles * ((M + bm - 1) / bm);
+  const int most = std::max(1, S / 4);
+  p.splits = std::min(most, std::max(1, want / tasks));
+  p.sps = ((S + p.splits - 1) / p.splits + 1) / 2 * 2;  // (pairs of steps)
+  p.splits = (S + p.sps - 1) / p.sps;
+  if (p.splits > 1) p.plane_bytes = static_cast<size_t>(p.splits) * (glu ? 2 : 1) * M * N * 4;
+  return p;
+}
+
 w4a16_status_t check_mx_weight(const w4a16_mx_t* w) {
   const w4a16_status_t st = check_mx(w);
   if (st != W4A16_OK) return st;
@@ -75,26 +91,68 @@ MxArgs mx_args(const MxRows& r, int M, const w4a16_mx_t* w0, const w4a16_mx_t* w
   return a;
 }
 
+size_t pieces_bytes(MxX kind, size_t n) { return kind == kMxXf32 ? 6 * n : (kind == kMxXf32h ? 4 * n : 0); }
+
 struct MxGemmPlan {
-  size_t bytes = 0;
+  bool tile = false;
+  MxTilePlan t;
+  size_t x_off = 0, planes_off = 0, bytes = 0;
 };
 MxGemmPlan plan_mx_gemm(int M, const w4a16_mx_t* w, MxX kind) {
   MxGemmPlan p;
-  p.bytes = 256;
+  Carve c;
+  p.tile = M > kMxStreamRows;
+  if (p.tile) {
+    p.t = plan_mx_tile(M, w->rows, w->K, kind, false);
+    c.take(p.x_off, pieces_bytes(kind, static_cast<size_t>(M) * w->K));
+    c.take(p.planes_off, p.t.plane_bytes);
+  }
+  p.bytes = std::max<size_t>(c.cursor, 256);
   return p;
 }
 
 struct MxMlpPlan {
-  size_t h_off = 0, hs_off = 0, bytes = 0;
+  bool tile = false;
+  MxX hkind = kMxXf32;
+  MxTilePlan gu, dn;
+  size_t x_off = 0, h_off = 0, hs_off = 0, planes_off = 0, bytes = 0;
 };
 MxMlpPlan plan_mx_mlp(int M, const w4a16_mx_t* gate, MxX kind) {
   MxMlpPlan p;
   Carve c;
   const size_t n = static_cast<size_t>(M) * gate->rows;
-  c.take(p.h_off, kind == kMxXfp4 ? n / 2 : n * 4);
-  c.take(p.hs_off, kind == kMxXfp4 ? n / kMxBlock : 0);
+  p.tile = M > kMxStreamRows;
+  // h of bf16 rows keeps 16 bits, well under the rounding of its own operands
+  p.hkind = kind == kMxXbf16 ? kMxXf32h : kind;
+  if (kind == kMxXfp4) {
+    c.take(p.h_off, n / 2);
+    c.take(p.hs_off, n / kMxBlock);
+  } else {
+    c.take(p.h_off, p.tile ? pieces_bytes(p.hkind, n) : n * 4);
+  }
+  if (p.tile) {
+    p.gu = plan_mx_tile(M, gate->rows, gate->K, kind, true);
+    p.dn = plan_mx_tile(M, gate->K, gate->rows, p.hkind, false);
+    c.take(p.x_off, pieces_bytes(kind, static_cast<size_t>(M) * gate->K));
+    c.take(p.planes_off, std::max(p.gu.plane_bytes, p.dn.plane_bytes));
+  }
   p.bytes = std::max<size_t>(c.cursor, 256);
   return p;
+}
+
+// One product, streamed or in tiles; pieces: where float32 rows go as planes.
+w4a16_status_t mx_product(MxX kind, bool glu, bool tile, const MxTilePlan& t, MxArgs a, void* pieces, void* planes,
+                          hipStream_t stream) {
+  if (!tile) return launch_mx_stream(kind, glu, a, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
+  MxTileArgs ta{};
+  static_cast<MxArgs&>(ta) = a;
+  ta.planes = static_cast<float*>(planes);
+  if (pieces != nullptr && kind == kMxXf32) {
+    if (launch_mx_pieces(static_cast<const float*>(a.x), static_cast<size_t>(a.M) * a.K, pieces, stream) != hipSuccess)
+      return W4A16_ERR_HIP;
+    ta.x = pieces;
+  }
+  return launch_mx_tile(kind, glu, t, ta, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
 }
 
 w4a16_status_t mx_gemm(const MxRows& r, int M, const w4a16_mx_t* w, void* y, w4a16_dtype_t yt, void* ws,
@@ -108,7 +166,8 @@ w4a16_status_t mx_gemm(const MxRows& r, int M, const w4a16_mx_t* w, void* y, w4a
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   MxArgs a = mx_args(r, M, w, nullptr, y);
   a.y_bf16 = yt == W4A16_BF16;
-  return launch_mx_stream(r.kind, false, a, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  return mx_product(r.kind, false, p.tile, p.t, a, wsb + p.x_off, wsb + p.planes_off, stream);
 }
 
 w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, const w4a16_mx_t* up,
@@ -125,17 +184,26 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
   MxRows h;
   h.x = wsb + p.h_off;
   h.xs = wsb + p.hs_off;
-  // h of bf16 rows keeps 16 bits: the next rounding, y's or h's neighbours' sum, is coarser by far
-  h.kind = r.kind == kMxXbf16 ? kMxXf32h : r.kind;
+  h.kind = p.hkind;
   MxArgs gu = mx_args(r, M, gate, up, wsb + p.h_off);
   gu.ys = wsb + p.hs_off;
-  if (launch_mx_stream(r.kind, true, gu, stream) != hipSuccess) return W4A16_ERR_HIP;
+  st = mx_product(r.kind, true, p.tile, p.gu, gu, wsb + p.x_off, wsb + p.planes_off, stream);
+  if (st != W4A16_OK) return st;
   MxArgs dn = mx_args(h, M, down, nullptr, y);
   dn.y_bf16 = yt == W4A16_BF16;
-  return launch_mx_stream(h.kind, false, dn, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
+  return mx_product(h.kind, false, p.tile, p.dn, dn, nullptr, wsb + p.planes_off, stream);
 }
 
 }  // namespace
+
+MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu) {
+  const int cols = glu ? 128 : 256;
+  const int bm = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
+  const size_t tasks256 = static_cast<size_t>((M + 255) / 256) * ((N + cols - 1) / cols);
+  if (bm == 256 && tasks256 < 256) return tile_plan(M, N, K, 128, cols, glu, 256);
+  return tile_plan(M, N, K, bm, cols, glu, bm <= 64 ? 512 : 256);
+}
+
 }  // namespace w4
 
 using namespace w4;

@@ -204,30 +204,14 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     // h to MXFP4: 32 columns are two blocks of the four lanes of one row
     if (wv >= kNB / 2) return;
     const int c = 2 * wv;
-    float h[8];
+    f32x4 h[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const f32x4 g = sum(c + b), u = sum(kNB + c + b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[4 * b + i] = silu(g[i]) * u[i];
+      for (int i = 0; i < 4; ++i) h[b][i] = silu(g[i]) * u[i];
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-    const uint32_t byte = mx_scale_byte(m);
-    const float inv = mx_scale_inverse(byte);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = byte == 255 ? 0.0f : h[i] * inv;
-    const uint32_t q = mx_codes8(h);
-    const int n = n0 + 16 * c;
-    if (lr >= nrows || n >= a.N) return;
-    const size_t row = static_cast<size_t>(r0 + lr);
-    uint16_t* o = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.y) + row * (a.N / 2) + n / 2);
-    o[kb] = static_cast<uint16_t>(q);
-    o[4 + kb] = static_cast<uint16_t>(q >> 16);
-    if (kb == 0) a.ys[row * (a.N / kMxBlock) + n / kMxBlock] = static_cast<uint8_t>(byte);
+    mx_store_h(a.y, a.ys, r0 + lr, a.N, n0 + 16 * c, kb, lr < nrows, h[0], h[1]);
   } else {
     if (wv >= kNB) return;
     const int n = n0 + 16 * wv + 4 * kb;
@@ -238,15 +222,7 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
       for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
     }
     if (lr >= nrows || n >= a.N) return;
-    const size_t at = static_cast<size_t>(r0 + lr) * a.N + n;
-    if (a.y_bf16) {
-      uint2 b;
-      b.x = f32_to_bf16(v[0]) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16;
-      b.y = f32_to_bf16(v[2]) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = b;
-    } else {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
-    }
+    mx_store4(a.y, static_cast<size_t>(r0 + lr) * a.N + n, a.y_bf16, v);
   }
 }
 

@@ -1,0 +1,415 @@
+// Products of more than 16 rows with MXFP4 weights: tiles of rows in LDS.
+//
+// y[m][n] = sum_k x[m][k] e2m1(W[n][k]) 2^(s[n][k / 32] - 127), operands as in
+// mx_stream.hip: the weights are the matrix cores' first operand, the rows of x
+// the second, and a lane ends with four adjacent columns of one row.
+//
+// A workgroup has eight waves, kWM along the rows and kWN along the columns, a
+// wave kMB x kNB blocks of 16 x 16.  The rows of one stage of K (128 of bf16,
+// 256 of MXFP4) are staged in LDS, double-buffered, one barrier a stage; each
+// wave streams its own columns' codes into registers two steps ahead and, for
+// 16-bit rows, expands them there.  float32 rows come as bf16 planes (pieces
+// whose sum they are), staged one after another against the same codes.
+//
+// LDS rows are 16-byte chunks, chunk c of row r at c ^ (r mod chunks): the 16
+// rows a fragment read touches then lie in distinct bank groups.
+#include "mx.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kOob = 0x7fffffff;  // an offset past every buffer: the load gives 0
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes), 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off, int soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+}
+__device__ __forceinline__ i32x8 widen(const u32x4& v) {
+  return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
+}
+
+// acc += W x, both MXFP4; kA and kB: the scales' bytes.
+template <int kA, int kB>
+__device__ __forceinline__ f32x4 mma_fp4(const u32x4& w, const u32x4& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), widen(x), acc, 4, 4, kA, static_cast<int>(ws), kB,
+                                                          static_cast<int>(xs));
+}
+template <int kA>
+__device__ __forceinline__ f32x4 mma_fp4_b(int b, const u32x4& w, const u32x4& x, const f32x4& acc, uint32_t ws,
+                                           uint32_t xs) {
+  switch (b) {
+    case 0: return mma_fp4<kA, 0>(w, x, acc, ws, xs);
+    case 1: return mma_fp4<kA, 1>(w, x, acc, ws, xs);
+    case 2: return mma_fp4<kA, 2>(w, x, acc, ws, xs);
+    default: return mma_fp4<kA, 3>(w, x, acc, ws, xs);
+  }
+}
+__device__ __forceinline__ f32x4 mma_fp4_ab(int a, int b, const u32x4& w, const u32x4& x, const f32x4& acc, uint32_t ws,
+                                            uint32_t xs) {
+  switch (a) {  // (both are constants once the loops are unrolled)
+    case 0: return mma_fp4_b<0>(b, w, x, acc, ws, xs);
+    case 1: return mma_fp4_b<1>(b, w, x, acc, ws, xs);
+    case 2: return mma_fp4_b<2>(b, w, x, acc, ws, xs);
+    default: return mma_fp4_b<3>(b, w, x, acc, ws, xs);
+  }
+}
+
+__device__ __forceinline__ float scale_byte(int c, uint32_t d) {
+  return __uint_as_float(((d >> (8 * c)) & 0xffu) << 23);
+}
+
+// kP: bf16 planes of x (1 .. 3), or 0 for MXFP4 rows.
+template <int kP, int kWM, int kWN, int kMB, int kNB, bool kGlu>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void mx_tile_kernel(const MxTileArgs a) {
+  static_assert(kWM * kWN * 64 == kThreads, "eight waves");
+  constexpr bool kFp4 = kP == 0;
+  constexpr int kPlanes = kFp4 ? 1 : kP;
+  constexpr int kMats = kGlu ? 2 : 1;
+  constexpr int kNbM = kNB / kMats;                       // blocks of each matrix
+  constexpr int kBM = 16 * kMB * kWM, kCols = 16 * kNbM;  // rows of the tile; columns of a wave
+  constexpr int kBN = kCols * kWN;
+  constexpr int kChunks = kFp4 ? 8 : 16;                  // 16-byte chunks of a row and stage
+  constexpr int kSteps = kFp4 ? 2 : 1;                    // steps of 128 k in a stage
+  constexpr int kUnits = (kBM * kChunks + kThreads - 1) / kThreads;  // chunks staged by a thread
+  constexpr int kParts = kFp4 ? 2 : 4;                    // of a stage's compute, between which they are staged
+  constexpr int kScaleUnits = kFp4 ? (kBM * 8 + kThreads - 1) / kThreads : 0;  // scale bytes staged by a thread
+  struct Buffer {
+    u32x4 x[kBM * kChunks];
+    uint32_t s[kFp4 ? 2 * ((kBM + 63) / 64) * 64 : 1];  // per step: scales of four 16-row blocks
+  };
+  __shared__ Buffer lds[2];
+
+  // XCD x = b mod 8 takes a contiguous run of tasks: the tiles of one row tile
+  // (and split), which share its rows
+  const int T = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  const int xcd = b % kXcds, tq = T / kXcds, trem = T % kXcds;
+  const int task = xcd * tq + min(xcd, trem) + b / kXcds;
+  const int tile = task % a.tiles, split = task / a.tiles % a.splits, r0 = task / a.tiles / a.splits * kBM;
+  const int nrows = min(kBM, a.M - r0);
+  const int s_lo = split * a.sps, s_hi = min(a.S, s_lo + a.sps);
+
+  const int t = static_cast<int>(threadIdx.x), wv = wave_id(), lane = lane_id();
+  const int lr = lane & 15, kb = lane >> 4;
+  const int wm = wv / kWN, wn = wv % kWN;
+  const int n0 = tile * kBN + wn * kCols;  // the wave's first column
+  const int J = n0 / kMxTileRows, c0 = n0 / 16 % 4;
+  const int tiles64 = (a.N + kMxTileRows - 1) / kMxTileRows;
+  const size_t cb = static_cast<size_t>(a.S) * kMxTileCodes, sb = static_cast<size_t>(a.S) * kMxTileScales;
+
+  // (a wave past the last column streams tile 0 and stores nothing)
+  const size_t Jr = J < tiles64 ? J : 0;
+  __amdgpu_buffer_rsrc_t wr[kMats], sr[kMats];
+#pragma unroll
+  for (int m = 0; m < kMats; ++m) {
+    wr[m] = rsrc(a.wc[m] + Jr * cb, cb);
+    sr[m] = rsrc(a.ws[m] + Jr * sb, sb);
+  }
+  struct Codes {
+    u32x4 w[kMats][kNbM];
+    uint32_t s[kMats];
+  };
+  auto load_codes = [&](Codes& c, int s) {
+    s = min(s, a.S - 1);  // (past the end: read again, not used)
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) {
+#pragma unroll
+      for (int i = 0; i < kNbM; ++i) c.w[m][i] = load16(wr[m], lane * 16 + (c0 + i) * 1024, s * kMxTileCodes);
+      c.s[m] = __builtin_amdgcn_raw_buffer_load_b32(sr[m], lane * 4, s * kMxTileScales, 0);
+    }
+  };
+
+  // staging: rows past the last one and k past K read as zeros
+  const size_t xrow = kFp4 ? a.K / 2 : static_cast<size_t>(a.K) * 2;
+  const size_t plane = static_cast<size_t>(a.M) * xrow;
+  const char* xbase = static_cast<const char*>(a.x) + r0 * xrow;
+  const int G = a.K / kMxBlock;
+  const __amdgpu_buffer_rsrc_t xsr =
+      rsrc(kFp4 ? a.xs + static_cast<size_t>(r0) * G : nullptr, kFp4 ? static_cast<size_t>(nrows) * G : 0);
+  const int chunk = t % kChunks, srow = t / kChunks;
+  constexpr int kRowsAt = kThreads / kChunks;  // rows staged by one unit of all threads
+  u32x4 held[kUnits];
+  uint32_t held_s[kScaleUnits > 0 ? kScaleUnits : 1];
+  // unit i of stage q (steps q kSteps ..): 8 (bf16) or 32 values from k
+  auto stage_load = [&](int i, int s, int p) {
+    const int row = srow + i * kRowsAt;
+    const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
+    const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s < s_hi;
+    held[i] = load16(rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
+  };
+  auto stage_store = [&](Buffer& buf, int i) {
+    const int row = srow + i * kRowsAt;
+    if (kUnits * kThreads == kBM * kChunks || row < kBM) buf.x[row * kChunks + (chunk ^ (row % kChunks))] = held[i];
+  };
+  // scale bytes: byte g of row r, eight of a row (two steps)
+  auto scale_load = [&](int i, int s) {
+    const int u = t + i * kThreads, row = u / 8, g = 4 * s + u % 8;
+    held_s[i] = __builtin_amdgcn_raw_buffer_load_b8(xsr, row < nrows && g < G ? row * G + g : kOob, 0, 0);
+  };
+  auto scale_store = [&](Buffer& buf, int i) {
+    const int u = t + i * kThreads, row = u / 8, g = u % 8;
+    if (row < kBM)
+      reinterpret_cast<uint8_t*>(buf.s)[((g / 4 * ((kBM + 63) / 64) + row / 64) * 64 + 16 * (g % 4) + row % 16) * 4 +
+                                        row / 16 % 4] = static_cast<uint8_t>(held_s[i]);
+  };
+
+  f32x4 acc[kMB][kNB];
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // unit i is staged in part i * kParts / kUnits of the compute
+  auto part_of = [](int i) { return i * kParts / kUnits; };
+  auto load_part = [&](int part, int s, int p) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (part_of(i) == part) stage_load(i, s, p);
+    if constexpr (kFp4) {
+      if (part == 0)
+#pragma unroll
+        for (int i = 0; i < kScaleUnits; ++i) scale_load(i, s);
+    }
+  };
+  auto store_part = [&](Buffer& buf, int part) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (part_of(i) == part) stage_store(buf, i);
+    if constexpr (kFp4) {
+      if (part == 0)
+#pragma unroll
+        for (int i = 0; i < kScaleUnits; ++i) scale_store(buf, i);
+    }
+  };
+  auto xfrag = [&](const Buffer& buf, int i, int c) {
+    const int row = wm * 16 * kMB + 16 * i + lr;
+    return buf.x[row * kChunks + (c ^ (row % kChunks))];
+  };
+
+  Codes ring[2];
+  load_codes(ring[0], s_lo);
+  load_codes(ring[1], s_lo + 1);
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) load_part(part, s_lo, 0);
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) store_part(lds[0], part);
+
+  if constexpr (kFp4) {
+    for (int s = s_lo, q = 0; s < s_hi; s += 2, ++q) {
+      __syncthreads();
+      const Buffer& cur = lds[q & 1];
+      Buffer& nxt = lds[(q + 1) & 1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load_part(h, s + 2, 0);
+        Codes& c = ring[h];
+        if (s + h < s_hi) {
+          uint32_t ws[kMats];
+#pragma unroll
+          for (int m = 0; m < kMats; ++m) ws[m] = kNbM == 4 ? c.s[m] : c.s[m] >> (8 * c0);
+#pragma unroll
+          for (int i = 0; i < kMB; ++i) {
+            const int rb = wm * kMB + i;  // 16-row block: byte rb % 4 of its dword
+            uint32_t xs = cur.s[(h * ((kBM + 63) / 64) + rb / 4) * 64 + lane];
+            if (kMB % 4 != 0) xs >>= 8 * (rb % 4 - i % 4);
+            const u32x4 xf = xfrag(cur, i, 4 * h + kb);
+#pragma unroll
+            for (int m = 0; m < kMats; ++m)
+#pragma unroll
+              for (int j = 0; j < kNbM; ++j)
+                acc[i][m * kNbM + j] = mma_fp4_ab(j, i % 4, c.w[m][j], xf, acc[i][m * kNbM + j], ws[m], xs);
+          }
+        }
+        load_codes(c, s + h + 2);
+        store_part(nxt, h);
+      }
+    }
+  } else {
+    int q = 0;
+    auto stage = [&](Codes& c, int s, int p, int s_next, int p_next) {
+      __syncthreads();
+      const Buffer& cur = lds[q & 1];
+      Buffer& nxt = lds[(q + 1) & 1];
+      ++q;
+      float f[kMats][kNbM];
+#pragma unroll
+      for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int j = 0; j < kNbM; ++j) f[m][j] = scale_byte(j, kNbM == 4 ? c.s[m] : c.s[m] >> (8 * c0));
+#pragma unroll
+      for (int part = 0; part < 4; ++part) {
+        load_part(part, s_next, p_next);
+        bf16x8 w[kNB];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m)
+#pragma unroll
+          for (int j = 0; j < kNbM; ++j) w[m * kNbM + j] = mx_bf16(c.w[m][j][part], f[m][j]);
+#pragma unroll
+        for (int i = 0; i < kMB; ++i) {
+          const bf16x8 xf = __builtin_bit_cast(bf16x8, xfrag(cur, i, 4 * kb + part));
+#pragma unroll
+          for (int j = 0; j < kNB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], xf, acc[i][j], 0, 0, 0);
+        }
+        store_part(nxt, part);
+      }
+    };
+    for (int s = s_lo; s < s_hi; s += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (s + h >= s_hi) break;
+#pragma unroll 1
+        for (int p = 0; p < kPlanes; ++p)
+          stage(ring[h], s + h, p, p + 1 < kPlanes ? s + h : s + h + 1, p + 1 < kPlanes ? p + 1 : 0);
+        load_codes(ring[h], s + h + 2);
+      }
+    }
+  }
+
+  // lane: row 16 i + lr of the wave, columns 4 kb .. + 3 of block j
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) {
+    const int row = r0 + wm * 16 * kMB + 16 * i + lr;
+    const bool row_ok = row < a.M;
+    const size_t rowN = static_cast<size_t>(row) * a.N;
+    if (a.splits > 1) {
+#pragma unroll
+      for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int j = 0; j < kNbM; ++j) {
+          const int n = n0 + 16 * j + 4 * kb;
+          if (row_ok && n < a.N)
+            *reinterpret_cast<f32x4*>(a.planes + (static_cast<size_t>(split) * kMats + m) * a.M * a.N + rowN + n) =
+                acc[i][m * kNbM + j];
+        }
+    } else if constexpr (!kGlu) {
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        const int n = n0 + 16 * j + 4 * kb;
+        if (row_ok && n < a.N) mx_store4(a.y, rowN + n, a.y_bf16, acc[i][j]);
+      }
+    } else {
+      f32x4 h[kNbM];
+#pragma unroll
+      for (int j = 0; j < kNbM; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[j][e] = silu(acc[i][j][e]) * acc[i][kNbM + j][e];
+      if constexpr (kFp4) {
+        static_assert(!kFp4 || kNbM % 2 == 0, "blocks of 32 columns");
+#pragma unroll
+        for (int j = 0; j < kNbM; j += 2) mx_store_h(a.y, a.ys, row, a.N, n0 + 16 * j, kb, row_ok, h[j], h[j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kNbM; ++j) {
+          const int n = n0 + 16 * j + 4 * kb;
+          if (row_ok && n < a.N) mx_store_pieces<kP == 3 ? 3 : 2>(a.y, rowN + n, static_cast<size_t>(a.M) * a.N, h[j]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- splits and planes
+
+// The splits' sums, in split order, to y or to h and its form for the down product.
+template <bool kGlu, int kOut>  // kOut: pieces of h (2, 3), 0: MXFP4 h; -: y
+__global__ __launch_bounds__(256) void mx_planes_kernel(const MxTileArgs a) {
+  const size_t mn = static_cast<size_t>(a.M) * a.N;
+  const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;  // four columns of a row
+  if (i * 4 >= mn) return;
+  f32x4 v[2];
+#pragma unroll
+  for (int m = 0; m < (kGlu ? 2 : 1); ++m) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(a.planes + m * mn) + i;
+    const size_t step = mn / 4 * (kGlu ? 2 : 1);
+    v[m] = p[0];
+    for (int s = 1; s < a.splits; ++s) v[m] += p[s * step];
+  }
+  if constexpr (!kGlu) {
+    mx_store4(a.y, 4 * i, a.y_bf16, v[0]);
+  } else {
+    f32x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = silu(v[0][e]) * v[1][e];
+    if constexpr (kOut == 0) {
+      // eight threads hold a block of 32 columns
+      uint32_t mx = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = max(mx, __float_as_uint(h[e]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), o)));
+      const uint32_t byte = mx_scale_byte(mx);
+      const float inv = mx_scale_inverse(byte);
+      float q[8] = {};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = byte == 255 ? 0.0f : h[e] * inv;
+      static_cast<uint16_t*>(a.y)[i] = static_cast<uint16_t>(mx_codes8(q));
+      if ((i & 7) == 0) a.ys[i >> 3] = static_cast<uint8_t>(byte);
+    } else {
+      mx_store_pieces<kOut>(a.y, 4 * i, mn, h);
+    }
+  }
+}
+
+// float32 rows as three bf16 planes.
+__global__ __launch_bounds__(256) void mx_pieces_kernel(const float* __restrict__ x, size_t n, void* out) {
+  const size_t i = (blockIdx.x * static_cast<size_t>(256) + threadIdx.x) * 4;
+  if (i < n) mx_store_pieces<3>(out, i, n, *reinterpret_cast<const f32x4*>(x + i));
+}
+
+template <int kP, bool kGlu, int kWM, int kWN, int kMB, int kNB>
+hipError_t start(const MxTileArgs& a, hipStream_t stream) {
+  const size_t rows = (static_cast<size_t>(a.M) + 16 * kMB * kWM - 1) / (16 * kMB * kWM);
+  const size_t blocks = rows * a.splits * a.tiles;
+  mx_tile_kernel<kP, kWM, kWN, kMB, kNB, kGlu><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int kP, bool kGlu>
+hipError_t start_rows(int bm, const MxTileArgs& a, hipStream_t stream) {
+  // MXFP4 h takes blocks of 32 columns inside a wave
+  constexpr int kN = kP == 0 && kGlu ? 4 : 2;
+  switch (bm) {
+    case 32: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 1 : 2, kN>(a, stream);
+    case 64: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 2 : 4, kN>(a, stream);
+    case 128: return start<kP, kGlu, 2, 4, 4, 4>(a, stream);
+    default: return start<kP, kGlu, 2, 4, 8, 4>(a, stream);
+  }
+}
+
+template <int kP>
+hipError_t start_glu(bool glu, int bm, const MxTileArgs& a, hipStream_t stream) {
+  return glu ? start_rows<kP, true>(bm, a, stream) : start_rows<kP, false>(bm, a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream) {
+  a.splits = p.splits;
+  a.sps = p.sps;
+  a.tiles = p.tiles;
+  hipError_t e = hipErrorInvalidValue;
+  switch (xk) {
+    case kMxXf32: e = start_glu<3>(glu, p.bm, a, stream); break;
+    case kMxXf32h: e = start_rows<2, false>(p.bm, a, stream); break;
+    case kMxXbf16: e = start_glu<1>(glu, p.bm, a, stream); break;
+    case kMxXfp4: e = start_glu<0>(glu, p.bm, a, stream); break;
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  const size_t n4 = static_cast<size_t>(a.M) * a.N / 4;
+  const unsigned blocks = static_cast<unsigned>((n4 + 255) / 256);
+  if (!glu) mx_planes_kernel<false, 1><<<blocks, 256, 0, stream>>>(a);
+  else if (xk == kMxXfp4) mx_planes_kernel<true, 0><<<blocks, 256, 0, stream>>>(a);
+  else if (xk == kMxXf32) mx_planes_kernel<true, 3><<<blocks, 256, 0, stream>>>(a);
+  else mx_planes_kernel<true, 2><<<blocks, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_pieces(const float* x, size_t n, void* out, hipStream_t stream) {
+  mx_pieces_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(x, n, out);
+  return hipGetLastError();
+}
+
+}  // namespace w4
