@@ -186,10 +186,10 @@ constexpr int kMxStreamRows = 16;
 // h as bf16 planes or MXFP4 rows.
 struct MxTileArgs : MxArgs {
   float* planes;  // splits > 1: [splits][matrices][M][N]
-  int tiles, splits, sps;
+  int tiles, row_tiles, band, splits, sps;
 };
 struct MxTilePlan {
-  int bm = 0, tiles = 0, splits = 1, sps = 0;
+  int bm = 0, cols = 0, tiles = 0, splits = 1, sps = 0;
   size_t plane_bytes = 0;  // all splits'
 };
 MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu);

@@ -10,6 +10,7 @@ namespace {
 MxTilePlan tile_plan(int M, int N, int K, int bm, int cols, bool glu, int want) {
   MxTilePlan p;
   p.bm = bm;
+  p.cols = cols;
   p.tiles = (N + cols - 1) / cols;
   const int S = (K + kMxStep - 1) / kMxStep;
   const int tasks = p.tiles * ((M + bm - 1) / bm);
@@ -200,7 +201,7 @@ MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu) {
   const int cols = glu ? 128 : 256;
   const int bm = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
   const size_t tasks256 = static_cast<size_t>((M + 255) / 256) * ((N + cols - 1) / cols);
-  if (bm == 256 && tasks256 < 256) return tile_plan(M, N, K, 128, cols, glu, 256);
+  if (bm == 256 && (tasks256 < 256 || xk == kMxXf32 || xk == kMxXf32h)) return tile_plan(M, N, K, 128, cols, glu, 256);
   return tile_plan(M, N, K, bm, cols, glu, bm <= 64 ? 512 : 256);
 }
 

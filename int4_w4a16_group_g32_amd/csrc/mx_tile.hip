@@ -15,6 +15,8 @@
 // rows a fragment read touches then lie in distinct bank groups.
 #include "mx.h"
 
+#include <cmath>
+
 namespace w4 {
 namespace {
 
@@ -83,12 +85,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
   __shared__ Buffer lds[2];
 
-  // XCD x = b mod 8 takes a contiguous run of tasks: the tiles of one row tile
-  // (and split), which share its rows
+  // XCD x = b mod 8 takes a contiguous run of tasks.  Tasks go through bands of
+  // `band` row tiles column by column, so a run is a block of row and column
+  // tiles whose rows and codes its L2 reads once (launch_mx_tile picks the band).
   const int T = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
   const int xcd = b % kXcds, tq = T / kXcds, trem = T % kXcds;
   const int task = xcd * tq + min(xcd, trem) + b / kXcds;
-  const int tile = task % a.tiles, split = task / a.tiles % a.splits, r0 = task / a.tiles / a.splits * kBM;
+  const int split = task / (a.row_tiles * a.tiles), u = task % (a.row_tiles * a.tiles);
+  const int band0 = u / (a.band * a.tiles) * a.band, in_band = min(a.band, a.row_tiles - band0);
+  const int v = u - band0 * a.tiles;
+  const int tile = v / in_band, r0 = (band0 + v % in_band) * kBM;
   const int nrows = min(kBM, a.M - r0);
   const int s_lo = split * a.sps, s_hi = min(a.S, s_lo + a.sps);
 
@@ -133,7 +139,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   constexpr int kRowsAt = kThreads / kChunks;  // rows staged by one unit of all threads
   u32x4 held[kUnits];
   uint32_t held_s[kScaleUnits > 0 ? kScaleUnits : 1];
-  // unit i of stage q (steps q kSteps ..): 8 (bf16) or 32 values from k
+  // a thread's chunk of its unit i, from step s
   auto stage_load = [&](int i, int s, int p) {
     const int row = srow + i * kRowsAt;
     const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
@@ -190,12 +196,31 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
 
   Codes ring[2];
-  load_codes(ring[0], s_lo);
-  load_codes(ring[1], s_lo + 1);
+  // Loads are issued in the order of their use, here as in the loops (the
+  // barriers keep the compiler from moving them): its waits then leave all
+  // later ones in flight.
 #pragma unroll
   for (int part = 0; part < kParts; ++part) load_part(part, s_lo, 0);
 #pragma unroll
   for (int part = 0; part < kParts; ++part) store_part(lds[0], part);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (kFp4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load_part(h, s_lo + 2, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      load_codes(ring[h], s_lo + h);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    load_codes(ring[0], s_lo);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) load_part(part, s_lo + 1 / kPlanes, 1 % kPlanes);
+    __builtin_amdgcn_sched_barrier(0);
+    load_codes(ring[1], s_lo + 1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
   if constexpr (kFp4) {
     for (int s = s_lo, q = 0; s < s_hi; s += 2, ++q) {
@@ -204,7 +229,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
       Buffer& nxt = lds[(q + 1) & 1];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        load_part(h, s + 2, 0);
+        store_part(nxt, h);
+        load_part(h, s + 4, 0);
+        __builtin_amdgcn_sched_barrier(0);
         Codes& c = ring[h];
         if (s + h < s_hi) {
           uint32_t ws[kMats];
@@ -224,12 +251,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
           }
         }
         load_codes(c, s + h + 2);
-        store_part(nxt, h);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   } else {
     int q = 0;
-    auto stage = [&](Codes& c, int s, int p, int s_next, int p_next) {
+    // (s_next, p_next): two stages on
+    auto stage = [&](Codes& c, int s_next, int p_next) {
       __syncthreads();
       const Buffer& cur = lds[q & 1];
       Buffer& nxt = lds[(q + 1) & 1];
@@ -241,7 +269,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
         for (int j = 0; j < kNbM; ++j) f[m][j] = scale_byte(j, kNbM == 4 ? c.s[m] : c.s[m] >> (8 * c0));
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
+        store_part(nxt, part);
         load_part(part, s_next, p_next);
+        __builtin_amdgcn_sched_barrier(0);
         bf16x8 w[kNB];
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
@@ -253,7 +283,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
 #pragma unroll
           for (int j = 0; j < kNB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], xf, acc[i][j], 0, 0, 0);
         }
-        store_part(nxt, part);
       }
     };
     for (int s = s_lo; s < s_hi; s += 2) {
@@ -262,8 +291,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
         if (s + h >= s_hi) break;
 #pragma unroll 1
         for (int p = 0; p < kPlanes; ++p)
-          stage(ring[h], s + h, p, p + 1 < kPlanes ? s + h : s + h + 1, p + 1 < kPlanes ? p + 1 : 0);
+          stage(ring[h], p + 2 < kPlanes ? s + h : s + h + (p + 2) / kPlanes, (p + 2) % kPlanes);
         load_codes(ring[h], s + h + 2);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -361,8 +391,7 @@ __global__ __launch_bounds__(256) void mx_pieces_kernel(const float* __restrict_
 
 template <int kP, bool kGlu, int kWM, int kWN, int kMB, int kNB>
 hipError_t start(const MxTileArgs& a, hipStream_t stream) {
-  const size_t rows = (static_cast<size_t>(a.M) + 16 * kMB * kWM - 1) / (16 * kMB * kWM);
-  const size_t blocks = rows * a.splits * a.tiles;
+  const size_t blocks = static_cast<size_t>(a.row_tiles) * a.splits * a.tiles;
   mx_tile_kernel<kP, kWM, kWN, kMB, kNB, kGlu><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
@@ -374,9 +403,13 @@ hipError_t start_rows(int bm, const MxTileArgs& a, hipStream_t stream) {
   switch (bm) {
     case 32: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 1 : 2, kN>(a, stream);
     case 64: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 2 : 4, kN>(a, stream);
-    case 128: return start<kP, kGlu, 2, 4, 4, 4>(a, stream);
-    default: return start<kP, kGlu, 2, 4, 8, 4>(a, stream);
+    case 128:
+      if constexpr (kP == 0 && !kGlu) return start<kP, kGlu, 1, 8, 8, 2>(a, stream);
+      return start<kP, kGlu, 2, 4, 4, 4>(a, stream);
+    default:
+      if constexpr (kP < 2) return start<kP, kGlu, 2, 4, 8, 4>(a, stream);  // (two or three planes: no such plan)
   }
+  return hipErrorInvalidValue;
 }
 
 template <int kP>
@@ -390,6 +423,13 @@ hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, 
   a.splits = p.splits;
   a.sps = p.sps;
   a.tiles = p.tiles;
+  a.row_tiles = (a.M + p.bm - 1) / p.bm;
+  // a run of n tasks as r row tiles of xb bytes by n / r column tiles of wb:
+  // r xb + n / r wb is least at r = sqrt(n wb / xb)
+  const double n = std::max(1.0, static_cast<double>(a.row_tiles) * a.tiles * a.splits / kXcds);
+  const double xb = p.bm * (xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : (xk == kMxXf32h ? 4 : 6)));
+  const double wb = p.cols * 0.53 * (glu ? 2 : 1);
+  a.band = std::min(a.row_tiles, std::max(1, static_cast<int>(std::sqrt(n * wb / xb) + 0.5)));
   hipError_t e = hipErrorInvalidValue;
   switch (xk) {
     case kMxXf32: e = start_glu<3>(glu, p.bm, a, stream); break;
