@@ -18,40 +18,39 @@
 // Bound by the weights' bytes.  A workgroup owns the columns of one tile and
 // all of K: its waves take every kW-th step, so nothing is summed across
 // workgroups and one launch is the whole product; the waves' sums meet in LDS
-// in wave order.  The rows come straight from the L2: few of them are there.
+// in wave order.  A wave keeps kRing steps of codes and rows in flight.  bf16
+// and float32 rows pass through the wave's own part of LDS: each lane splits
+// eight values into their pieces and writes them, and reads back fragments (the
+// 64 lanes split 4 rows at once; splitting in fragment order, 16 rows whether
+// they are there or not, and without LDS, took four decoding rows through the
+// 7168 / 18432 MLP in 86 us).
 #include "mx.h"
 
 namespace w4 {
 namespace {
 
-constexpr int kW = 8;        // waves of a workgroup
-constexpr int kRows = 16;    // rows of x in a launch's row block
-constexpr int kRing = 2;     // steps in flight per wave
+constexpr int kRows = 16;         // rows of x in a launch's row block
 constexpr int kOob = 0x7fffffff;  // an offset past every buffer: the load gives 0
+constexpr int kXcds = 8;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, size_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes), 0x00020000);
 }
+constexpr int kNt = 2;  // nontemporal: codes are read once
+template <int kAux = 0>
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off, int soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, kAux));
+}
 
-template <int kX, int kNB, int kMats>
-struct Step {
-  static constexpr int kXv = kX == kMxXfp4 ? 1 : (kX == kMxXbf16 ? 4 : 8);
-  u32x4 w[kMats][kNB];
-  uint32_t ws[kMats];
-  u32x4 x[kXv];
-  uint32_t xs;
-};
-
-// bf16 piece number p of eight float32 values: 8 significant bits each, cut off
-// (the last of two pieces rounded to nearest); r holds what is left.
-template <int kLeft>
-__device__ __forceinline__ bf16x8 next_piece(float r[8]) {
-  uint32_t w[4];
+// bf16 piece of eight float32 values: 8 significant bits each, cut off, r left
+// with the rest; or with kLast all that is left, rounded to nearest.
+template <bool kLast>
+__device__ __forceinline__ u32x4 next_piece(float r[8]) {
+  u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (kLeft == 0) {
-      const bf16x2 b = __builtin_convertvector(f32x2{r[2 * i], r[2 * i + 1]}, bf16x2);
-      w[i] = __builtin_bit_cast(uint32_t, b);
+    if constexpr (kLast) {
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{r[2 * i], r[2 * i + 1]}, bf16x2));
     } else {
       const uint32_t a = __float_as_uint(r[2 * i]), b = __float_as_uint(r[2 * i + 1]);
       w[i] = __builtin_amdgcn_perm(b, a, 0x07060302);
@@ -59,20 +58,45 @@ __device__ __forceinline__ bf16x8 next_piece(float r[8]) {
       r[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
     }
   }
-  return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+  return w;
 }
 
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
   return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
 }
 
-// One tile: kNB 16-column blocks of each of kMats matrices, one block of 16 rows.
-template <int kX, int kNB, bool kGlu>
+template <int kA>
+__device__ __forceinline__ f32x4 mma_fp4(const u32x4& w, const i32x8& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), x, acc, 4, 4, kA, static_cast<int>(ws), 0,
+                                                          static_cast<int>(xs));
+}
+
+// One tile: kNB 16-column blocks of each matrix, up to 4 kC rows (of a block of
+// 16); kW waves.
+template <int kX, int kC, int kNB, bool kGlu, int kW>
 __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
   constexpr int kMats = kGlu ? 2 : 1;
-  using St = Step<kX, kNB, kMats>;
+  constexpr bool kFp4 = kX == kMxXfp4, kWide = kX == kMxXf32 || kX == kMxXf32h;
+  constexpr int kPieces = kFp4 ? 0 : (kX == kMxXbf16 ? 1 : (kX == kMxXf32h ? 2 : 3));
+  constexpr int kR = 4 * kC;                            // rows in LDS
+  constexpr int kXv = kFp4 ? 1 : kC * (kWide ? 2 : 1);  // 16-byte loads of x a step
+  constexpr int kRing = 2;                              // steps in flight
+  constexpr int kXUnits = kPieces * kR * 16;            // LDS of a wave: pieces of 128 k
+  constexpr int kRedUnits = kMats * kNB * 64;           // its sums
+  struct Step {
+    u32x4 w[kMats][kNB];
+    uint32_t ws[kMats];
+    u32x4 x[kXv];
+    uint32_t xs;
+  };
+  __shared__ u32x4 lds[kW * (kXUnits > kRedUnits ? kXUnits : kRedUnits)];
+
+  // XCD x = b mod 8 takes a contiguous run of tiles: neighbours share lines of scales
+  const int T = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  const int xcd = b % kXcds, tq = T / kXcds, trem = T % kXcds;
+  const int task = xcd * tq + min(xcd, trem) + b / kXcds;
   const int tiles = (a.N + 16 * kNB - 1) / (16 * kNB);
-  const int tile = blockIdx.x % tiles, r0 = blockIdx.x / tiles * kRows;
+  const int tile = task % tiles, r0 = task / tiles * kRows;
   const int nrows = min(kRows, a.M - r0);
   const int wv = wave_id(), lane = lane_id();
   const int lr = lane & 15, kb = lane >> 4;
@@ -85,32 +109,42 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     wr[t] = rsrc(a.wc[t] + static_cast<size_t>(J) * a.S * kMxTileCodes, static_cast<size_t>(a.S) * kMxTileCodes);
     sr[t] = rsrc(a.ws[t] + static_cast<size_t>(J) * a.S * kMxTileScales, static_cast<size_t>(a.S) * kMxTileScales);
   }
-  const size_t xrow = kX == kMxXfp4 ? a.K / 2 : static_cast<size_t>(a.K) * (kX == kMxXbf16 ? 2 : 4);
   // rows past the last one and k past K read as zeros
-  const __amdgpu_buffer_rsrc_t xr = rsrc(static_cast<const char*>(a.x) + r0 * xrow, nrows * xrow);
-  constexpr int kBlockBytes = kX == kMxXfp4 ? 16 : (kX == kMxXbf16 ? 64 : 128);
-  const int xoff = lr < nrows ? lr * static_cast<int>(xrow) + kb * kBlockBytes : kOob;
+  const int xrow = kFp4 ? a.K / 2 : a.K * (kWide ? 4 : 2);
+  const __amdgpu_buffer_rsrc_t xr =
+      rsrc(static_cast<const char*>(a.x) + static_cast<size_t>(r0) * xrow, static_cast<size_t>(nrows) * xrow);
   const int G = a.K / kMxBlock;
-  const __amdgpu_buffer_rsrc_t xsr = rsrc(kX == kMxXfp4 ? a.xs + static_cast<size_t>(r0) * G : nullptr,
-                                          kX == kMxXfp4 ? static_cast<size_t>(nrows) * G : 0);
+  const __amdgpu_buffer_rsrc_t xsr = rsrc(kFp4 ? a.xs + static_cast<size_t>(r0) * G : nullptr,
+                                          kFp4 ? static_cast<size_t>(nrows) * G : 0);
 
-  auto load = [&](St& st, int s) {
-    s = min(s, a.S - 1);  // (past the end: read again, not used)
+  auto load = [&](Step& st, int s) {
+    const int sc = min(s, a.S - 1);  // (past the end: read again, not used)
 #pragma unroll
     for (int t = 0; t < kMats; ++t) {
-      st.ws[t] = __builtin_amdgcn_raw_buffer_load_b32(sr[t], lane * 4, s * kMxTileScales, 0);
 #pragma unroll
-      for (int c = 0; c < kNB; ++c)
-        st.w[t][c] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr[t], lane * 16, s * kMxTileCodes + (c0 + c) * 1024, 0));
+      for (int c = 0; c < kNB; ++c) st.w[t][c] = load16<kNt>(wr[t], lane * 16 + (c0 + c) * 1024, sc * kMxTileCodes);
+      st.ws[t] = __builtin_amdgcn_raw_buffer_load_b32(sr[t], lane * 4, sc * kMxTileScales, 0);
     }
-    const bool on = lr < nrows && 4 * s + kb < G;
-    const int at = on ? xoff + s * 4 * kBlockBytes : kOob;
-#pragma unroll
-    for (int i = 0; i < St::kXv; ++i)
-      st.x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, on ? at + 16 * i : kOob, 0, 0));
-    if constexpr (kX == kMxXfp4)
+    if constexpr (kFp4) {
+      const bool on = lr < nrows && 4 * s + kb < G;
+      st.x[0] = load16(xr, on ? lr * xrow + (4 * s + kb) * 16 : kOob, 0);
       st.xs = __builtin_amdgcn_raw_buffer_load_b8(xsr, on ? lr * G + 4 * s + kb : kOob, 0, 0);
+    } else {
+      // eight values of row (lane + 64 c) / 16
+      const int k8 = 16 * s + lr;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int row = kb + 4 * c;
+        const int at = row < nrows && 8 * k8 < a.K ? row * xrow + k8 * (kWide ? 32 : 16) : kOob;
+        if constexpr (kWide) {
+          st.x[2 * c] = load16(xr, at, 0);
+          st.x[2 * c + 1] = load16(xr, at == kOob ? kOob : at + 16, 0);
+        } else {
+          st.x[c] = load16(xr, at, 0);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // (loads stay in the order of their use)
   };
 
   f32x4 acc[kMats][kNB];
@@ -119,28 +153,41 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
 #pragma unroll
     for (int c = 0; c < kNB; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto multiply = [&](const St& st) {
+  u32x4* xl = lds + wv * kXUnits;
+  const int rr = lr & (kR - 1);  // (columns past the rows compute what nothing reads)
+  auto multiply = [&](const Step& st) {
     uint32_t sc[kMats];
 #pragma unroll
     for (int t = 0; t < kMats; ++t) sc[t] = kNB == 4 ? st.ws[t] : st.ws[t] >> (8 * c0);
-    if constexpr (kX == kMxXfp4) {
+    if constexpr (kFp4) {
       const i32x8 xb = widen(st.x[0]);
 #pragma unroll
       for (int t = 0; t < kMats; ++t) {
         // (the scale's byte is an immediate of the instruction)
-        acc[t][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(st.w[t][0]), xb, acc[t][0], 4, 4, 0,
-                                                                     static_cast<int>(sc[t]), 0, static_cast<int>(st.xs));
-        if constexpr (kNB > 1)
-          acc[t][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(st.w[t][1]), xb, acc[t][1], 4, 4, 1, static_cast<int>(sc[t]), 0, static_cast<int>(st.xs));
+        acc[t][0] = mma_fp4<0>(st.w[t][0], xb, acc[t][0], sc[t], st.xs);
+        if constexpr (kNB > 1) acc[t][1] = mma_fp4<1>(st.w[t][1], xb, acc[t][1], sc[t], st.xs);
         if constexpr (kNB > 2) {
-          acc[t][2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(st.w[t][2]), xb, acc[t][2], 4, 4, 2, static_cast<int>(sc[t]), 0, static_cast<int>(st.xs));
-          acc[t][3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(st.w[t][3]), xb, acc[t][3], 4, 4, 3, static_cast<int>(sc[t]), 0, static_cast<int>(st.xs));
+          acc[t][2] = mma_fp4<2>(st.w[t][2], xb, acc[t][2], sc[t], st.xs);
+          acc[t][3] = mma_fp4<3>(st.w[t][3], xb, acc[t][3], sc[t], st.xs);
         }
       }
     } else {
+      // pieces to LDS; a wave's LDS operations run in order, so this needs no barrier
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int row = kb + 4 * c, at = row * 16 + (lr ^ row);
+        if constexpr (kWide) {
+          float r[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(st.x[2 * c + i / 4][i % 4]);
+          xl[at] = next_piece<false>(r);
+          if constexpr (kPieces == 3) xl[kR * 16 + at] = next_piece<false>(r);
+          xl[(kPieces - 1) * kR * 16 + at] = next_piece<true>(r);
+        } else {
+          xl[at] = st.x[c];
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
       float f[kMats][4];
 #pragma unroll
       for (int t = 0; t < kMats; ++t)
@@ -148,34 +195,29 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
         f[t][3] = mx_scale<3>(sc[t]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        bf16x8 xf[kPieces > 0 ? kPieces : 1];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+          xf[p] = __builtin_bit_cast(bf16x8, xl[(p * kR + rr) * 16 + ((4 * kb + j) ^ rr)]);
         bf16x8 w[kMats][kNB];
 #pragma unroll
         for (int t = 0; t < kMats; ++t)
 #pragma unroll
           for (int c = 0; c < kNB; ++c) w[t][c] = mx_bf16(st.w[t][c][j], f[t][c]);
-        auto mma = [&](const bf16x8& xp) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
 #pragma unroll
           for (int t = 0; t < kMats; ++t)
 #pragma unroll
             for (int c = 0; c < kNB; ++c)
-              acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t][c], xp, acc[t][c], 0, 0, 0);
-        };
-        if constexpr (kX == kMxXbf16) {
-          mma(__builtin_bit_cast(bf16x8, st.x[j]));
-        } else {
-          float r[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(st.x[2 * j + i / 4][i % 4]);
-          mma(next_piece<1>(r));
-          if constexpr (kX == kMxXf32) mma(next_piece<1>(r));
-          mma(next_piece<0>(r));
-        }
+              acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t][c], xf[p], acc[t][c], 0, 0, 0);
       }
+      __builtin_amdgcn_wave_barrier();
     }
   };
 
   const int n = wv < a.S ? (a.S - wv + kW - 1) / kW : 0;  // steps wv, wv + kW, ...
-  St ring[kRing];
+  Step ring[kRing];
 #pragma unroll
   for (int j = 0; j < kRing; ++j) load(ring[j], wv + j * kW);
   for (int i = 0; i < n; i += kRing) {
@@ -186,8 +228,9 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     }
   }
 
-  // the waves' sums, in wave order: item it is lane it % 64 of block it / 64
-  __shared__ f32x4 red[kW][kMats * kNB][64];
+  // the waves' sums, in wave order
+  f32x4(*red)[kMats * kNB][64] = reinterpret_cast<f32x4(*)[kMats * kNB][64]>(lds);
+  __syncthreads();  // (every wave is done with its rows)
 #pragma unroll
   for (int t = 0; t < kMats; ++t)
 #pragma unroll
@@ -200,8 +243,9 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     return v;
   };
   // lane: row r0 + lr, columns 4 kb .. 4 kb + 3 of a block
-  if constexpr (kGlu && kX == kMxXfp4) {
+  if constexpr (kGlu && kFp4) {
     // h to MXFP4: 32 columns are two blocks of the four lanes of one row
+    static_assert(kNB % 2 == 0, "blocks of 32 columns");
     if (wv >= kNB / 2) return;
     const int c = 2 * wv;
     f32x4 h[2];
@@ -213,6 +257,7 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     }
     mx_store_h(a.y, a.ys, r0 + lr, a.N, n0 + 16 * c, kb, lr < nrows, h[0], h[1]);
   } else {
+    static_assert(kNB <= kW, "a wave a block");
     if (wv >= kNB) return;
     const int n = n0 + 16 * wv + 4 * kb;
     f32x4 v = sum(wv);
@@ -226,30 +271,38 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
   }
 }
 
-template <int kX, int kNB, bool kGlu>
+template <int kX, int kC, int kNB, bool kGlu, int kW>
 hipError_t start(const MxArgs& a, hipStream_t stream) {
   const size_t tiles = (static_cast<size_t>(a.N) + 16 * kNB - 1) / (16 * kNB);
   const size_t blocks = tiles * ((static_cast<size_t>(a.M) + kRows - 1) / kRows);
-  mx_stream_kernel<kX, kNB, kGlu><<<static_cast<unsigned>(blocks), kW * 64, 0, stream>>>(a);
+  mx_stream_kernel<kX, kC, kNB, kGlu, kW><<<static_cast<unsigned>(blocks), kW * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <bool kGlu>
-hipError_t start_x(MxX xk, const MxArgs& a, hipStream_t stream) {
-  constexpr int kNB = kGlu ? 2 : 1;
-  switch (xk) {
-    case kMxXf32: return start<kMxXf32, kNB, kGlu>(a, stream);
-    case kMxXf32h: return start<kMxXf32h, kNB, kGlu>(a, stream);
-    case kMxXbf16: return start<kMxXbf16, kNB, kGlu>(a, stream);
-    case kMxXfp4: return start<kMxXfp4, kNB, kGlu>(a, stream);
-  }
-  return hipErrorInvalidValue;
+template <int kX, int kNB, bool kGlu, int kW>
+hipError_t start_rows(const MxArgs& a, hipStream_t stream) {
+  if (kX == kMxXfp4 || a.M <= 4) return start<kX, 1, kNB, kGlu, kW>(a, stream);
+  if (a.M <= 8) return start<kX, 2, kNB, kGlu, kW>(a, stream);
+  return start<kX, 4, kNB, kGlu, kW < 8 ? kW : 8>(a, stream);  // (LDS: 12 KiB a wave)
+}
+
+template <int kX, bool kGlu>
+hipError_t start_shape(const MxArgs& a, hipStream_t stream) {
+  if constexpr (kGlu) return start_rows<kX, 2, true, 4>(a, stream);
+  if (a.N >= 32 * 192) return start_rows<kX, 2, false, 16>(a, stream);
+  return start_rows<kX, 1, false, 8>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mx_stream(MxX xk, bool glu, const MxArgs& a, hipStream_t stream) {
-  return glu ? start_x<true>(xk, a, stream) : start_x<false>(xk, a, stream);
+  switch (xk) {
+    case kMxXf32: return glu ? start_shape<kMxXf32, true>(a, stream) : start_shape<kMxXf32, false>(a, stream);
+    case kMxXf32h: return start_shape<kMxXf32h, false>(a, stream);  // (h is never a gate's input)
+    case kMxXbf16: return glu ? start_shape<kMxXbf16, true>(a, stream) : start_shape<kMxXbf16, false>(a, stream);
+    case kMxXfp4: return glu ? start_shape<kMxXfp4, true>(a, stream) : start_shape<kMxXfp4, false>(a, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace w4
