@@ -90,12 +90,6 @@ __device__ __forceinline__ bf16x8 mx_bf16(uint32_t codes, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Byte c of a dword of scale bytes as the float power of two.
-template <int c>
-__device__ __forceinline__ float mx_scale(uint32_t dword) {
-  return __uint_as_float(c == 3 ? (dword >> 24) << 23 : ((dword >> (8 * c)) & 0xffu) << 23);
-}
-
 // Four adjacent outputs from element `at`.
 __device__ __forceinline__ void mx_store4(void* y, size_t at, int bf16, const f32x4& v) {
   if (bf16) {

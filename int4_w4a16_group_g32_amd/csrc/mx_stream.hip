@@ -65,27 +65,30 @@ __device__ __forceinline__ i32x8 widen(const u32x4& v) {
   return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
 }
 
-template <int kA>
 __device__ __forceinline__ f32x4 mma_fp4(const u32x4& w, const i32x8& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), x, acc, 4, 4, kA, static_cast<int>(ws), 0,
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), x, acc, 4, 4, 0, static_cast<int>(ws), 0,
                                                           static_cast<int>(xs));
 }
 
 // One tile: kNB 16-column blocks of each matrix, up to 4 kC rows (of a block of
-// 16); kW waves.
-template <int kX, int kC, int kNB, bool kGlu, int kW>
+// 16); kW waves, each with kRing steps in flight.
+template <int kX, int kC, int kNB, bool kGlu, int kW, int kRing>
 __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
   constexpr int kMats = kGlu ? 2 : 1;
   constexpr bool kFp4 = kX == kMxXfp4, kWide = kX == kMxXf32 || kX == kMxXf32h;
   constexpr int kPieces = kFp4 ? 0 : (kX == kMxXbf16 ? 1 : (kX == kMxXf32h ? 2 : 3));
   constexpr int kR = 4 * kC;                            // rows in LDS
   constexpr int kXv = kFp4 ? 1 : kC * (kWide ? 2 : 1);  // 16-byte loads of x a step
-  constexpr int kRing = 2;                              // steps in flight
   constexpr int kXUnits = kPieces * kR * 16;            // LDS of a wave: pieces of 128 k
+  // Column v of x's operands is piece v / kR of row v % kR: the pieces of few
+  // rows share an instruction, and the columns of a row are added at the end.
+  constexpr int kGroups = (kPieces * kR + 15) / 16;     // instructions of one k block
+  constexpr int kFolds = kGroups == 1 && kPieces > 1 ? kPieces : (kR < 16 && kPieces > 1 ? 2 : 1);
   constexpr int kRedUnits = kMats * kNB * 64;           // its sums
+  constexpr int kSpan = 4 % kNB == 0 ? 1 : (kNB + 6) / 4;  // 64-column tiles the columns may touch
   struct Step {
     u32x4 w[kMats][kNB];
-    uint32_t ws[kMats];
+    uint32_t ws[kMats][kSpan];
     u32x4 x[kXv];
     uint32_t xs;
   };
@@ -101,13 +104,22 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
   const int wv = wave_id(), lane = lane_id();
   const int lr = lane & 15, kb = lane >> 4;
 
-  // the tile's codes and scales: 64-column tile J, first 16-column block c0
+  // the tile's codes and scales: kNB 16-column blocks from block c0 of 64-column
+  // tile J, which they leave where kNB is no divisor of 4; a block past the last
+  // tile reads the last one's, for nothing
   const int n0 = tile * 16 * kNB, J = n0 / kMxTileRows, c0 = n0 / 16 % 4;
+  const int span = min(kSpan, (a.N + kMxTileRows - 1) / kMxTileRows - J);
   __amdgpu_buffer_rsrc_t wr[kMats], sr[kMats];
 #pragma unroll
   for (int t = 0; t < kMats; ++t) {
-    wr[t] = rsrc(a.wc[t] + static_cast<size_t>(J) * a.S * kMxTileCodes, static_cast<size_t>(a.S) * kMxTileCodes);
-    sr[t] = rsrc(a.ws[t] + static_cast<size_t>(J) * a.S * kMxTileScales, static_cast<size_t>(a.S) * kMxTileScales);
+    wr[t] = rsrc(a.wc[t] + static_cast<size_t>(J) * a.S * kMxTileCodes, static_cast<size_t>(a.S) * kMxTileCodes * span);
+    sr[t] = rsrc(a.ws[t] + static_cast<size_t>(J) * a.S * kMxTileScales, static_cast<size_t>(a.S) * kMxTileScales * span);
+  }
+  int wat[kNB];  // block c's bytes from J's codes, of step 0
+#pragma unroll
+  for (int c = 0; c < kNB; ++c) {
+    const int blk = min(c0 + c, 4 * span - 1);
+    wat[c] = blk / 4 * a.S * kMxTileCodes + blk % 4 * 1024;
   }
   // rows past the last one and k past K read as zeros
   const int xrow = kFp4 ? a.K / 2 : a.K * (kWide ? 4 : 2);
@@ -122,8 +134,10 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
 #pragma unroll
     for (int t = 0; t < kMats; ++t) {
 #pragma unroll
-      for (int c = 0; c < kNB; ++c) st.w[t][c] = load16<kNt>(wr[t], lane * 16 + (c0 + c) * 1024, sc * kMxTileCodes);
-      st.ws[t] = __builtin_amdgcn_raw_buffer_load_b32(sr[t], lane * 4, sc * kMxTileScales, 0);
+      for (int c = 0; c < kNB; ++c) st.w[t][c] = load16<kNt>(wr[t], lane * 16, sc * kMxTileCodes + wat[c]);
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i)
+        st.ws[t][i] = __builtin_amdgcn_raw_buffer_load_b32(sr[t], lane * 4, sc * kMxTileScales + min(i, span - 1) * a.S * kMxTileScales, 0);
     }
     if constexpr (kFp4) {
       const bool on = lr < nrows && 4 * s + kb < G;
@@ -154,23 +168,36 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     for (int c = 0; c < kNB; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   u32x4* xl = lds + wv * kXUnits;
-  const int rr = lr & (kR - 1);  // (columns past the rows compute what nothing reads)
-  auto multiply = [&](const Step& st) {
-    uint32_t sc[kMats];
+  // lane lr's chunk row of group i: columns past the pieces are zeros where a
+  // later group shares the accumulator, and else compute what nothing reads
+  auto frag = [&](int i, int j) {
+    const int v = 16 * i + lr;
+    const bool in = v < kPieces * kR;
+    const int row = in ? v : 0;
+    u32x4 x = xl[row * 16 + ((4 * kb + j) ^ (row & (kR - 1)))];
+    if (kGroups > 1 && kPieces * kR % 16 != 0 && i == kGroups - 1) {
 #pragma unroll
-    for (int t = 0; t < kMats; ++t) sc[t] = kNB == 4 ? st.ws[t] : st.ws[t] >> (8 * c0);
+      for (int e = 0; e < 4; ++e) x[e] = in ? x[e] : 0;
+    }
+    return __builtin_bit_cast(bf16x8, x);
+  };
+  auto multiply = [&](const Step& st) {
+    uint32_t sc[kMats][kNB];  // block c's scale byte
+#pragma unroll
+    for (int t = 0; t < kMats; ++t)
+#pragma unroll
+      for (int c = 0; c < kNB; ++c) {
+        uint32_t d = st.ws[t][0];
+#pragma unroll
+        for (int i = 1; i < kSpan; ++i) d = (c0 + c) / 4 == i ? st.ws[t][i] : d;
+        sc[t][c] = (d >> (8 * ((c0 + c) % 4))) & 0xffu;
+      }
     if constexpr (kFp4) {
       const i32x8 xb = widen(st.x[0]);
 #pragma unroll
-      for (int t = 0; t < kMats; ++t) {
-        // (the scale's byte is an immediate of the instruction)
-        acc[t][0] = mma_fp4<0>(st.w[t][0], xb, acc[t][0], sc[t], st.xs);
-        if constexpr (kNB > 1) acc[t][1] = mma_fp4<1>(st.w[t][1], xb, acc[t][1], sc[t], st.xs);
-        if constexpr (kNB > 2) {
-          acc[t][2] = mma_fp4<2>(st.w[t][2], xb, acc[t][2], sc[t], st.xs);
-          acc[t][3] = mma_fp4<3>(st.w[t][3], xb, acc[t][3], sc[t], st.xs);
-        }
-      }
+      for (int t = 0; t < kMats; ++t)
+#pragma unroll
+        for (int c = 0; c < kNB; ++c) acc[t][c] = mma_fp4(st.w[t][c], xb, acc[t][c], sc[t][c], st.xs);
     } else {
       // pieces to LDS; a wave's LDS operations run in order, so this needs no barrier
 #pragma unroll
@@ -188,24 +215,18 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
         }
       }
       __builtin_amdgcn_wave_barrier();
-      float f[kMats][4];
-#pragma unroll
-      for (int t = 0; t < kMats; ++t)
-        f[t][0] = mx_scale<0>(sc[t]), f[t][1] = mx_scale<1>(sc[t]), f[t][2] = mx_scale<2>(sc[t]),
-        f[t][3] = mx_scale<3>(sc[t]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        bf16x8 xf[kPieces > 0 ? kPieces : 1];
+        bf16x8 xf[kGroups > 0 ? kGroups : 1];
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p)
-          xf[p] = __builtin_bit_cast(bf16x8, xl[(p * kR + rr) * 16 + ((4 * kb + j) ^ rr)]);
+        for (int p = 0; p < kGroups; ++p) xf[p] = frag(p, j);
         bf16x8 w[kMats][kNB];
 #pragma unroll
         for (int t = 0; t < kMats; ++t)
 #pragma unroll
-          for (int c = 0; c < kNB; ++c) w[t][c] = mx_bf16(st.w[t][c][j], f[t][c]);
+          for (int c = 0; c < kNB; ++c) w[t][c] = mx_bf16(st.w[t][c][j], __uint_as_float(sc[t][c] << 23));
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p)
+        for (int p = 0; p < kGroups; ++p)
 #pragma unroll
           for (int t = 0; t < kMats; ++t)
 #pragma unroll
@@ -240,6 +261,14 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
     f32x4 v = red[0][b][lane];
 #pragma unroll
     for (int w = 1; w < kW; ++w) v += red[w][b][lane];
+    // the smaller pieces' columns, lanes kR apart, to the first
+    if constexpr (kFolds > 1) {
+      const f32x4 u = v;
+#pragma unroll
+      for (int f = 1; f < kFolds; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += __shfl(u[e], lane + f * kR);
+    }
     return v;
   };
   // lane: row r0 + lr, columns 4 kb .. 4 kb + 3 of a block
@@ -271,26 +300,50 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
   }
 }
 
-template <int kX, int kC, int kNB, bool kGlu, int kW>
+template <int kX, int kC, int kNB, bool kGlu, int kW, int kRing>
 hipError_t start(const MxArgs& a, hipStream_t stream) {
   const size_t tiles = (static_cast<size_t>(a.N) + 16 * kNB - 1) / (16 * kNB);
   const size_t blocks = tiles * ((static_cast<size_t>(a.M) + kRows - 1) / kRows);
-  mx_stream_kernel<kX, kC, kNB, kGlu, kW><<<static_cast<unsigned>(blocks), kW * 64, 0, stream>>>(a);
+  mx_stream_kernel<kX, kC, kNB, kGlu, kW, kRing><<<static_cast<unsigned>(blocks), kW * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int kX, int kNB, bool kGlu, int kW>
+template <int kX, int kNB, bool kGlu, int kW, int kRing>
 hipError_t start_rows(const MxArgs& a, hipStream_t stream) {
-  if (kX == kMxXfp4 || a.M <= 4) return start<kX, 1, kNB, kGlu, kW>(a, stream);
-  if (a.M <= 8) return start<kX, 2, kNB, kGlu, kW>(a, stream);
-  return start<kX, 4, kNB, kGlu, kW < 8 ? kW : 8>(a, stream);  // (LDS: 12 KiB a wave)
+  if (kX == kMxXfp4 || a.M <= 4) return start<kX, 1, kNB, kGlu, kW, kRing>(a, stream);
+  if constexpr (kX != kMxXfp4) {
+    if (a.M <= 8) return start<kX, 2, kNB, kGlu, kW, kRing>(a, stream);
+    return start<kX, 4, kNB, kGlu, kW, kRing>(a, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
+constexpr int kCus = 256;
+
+// The blocks that the busiest compute unit gets with nb of them a workgroup.
+int most_blocks(int N, int nb) { return ((N + 16 * nb - 1) / (16 * nb) + kCus - 1) / kCus * nb; }
+
+// Columns of a workgroup: what loads the compute units most evenly, and of
+// equals the most (fewer workgroups read x), e.g. for N = 18432 one round of 231
+// workgroups of 80 columns, for 7168 one of 224 of 32.  Gate and up, four
+// float32 rows, 7168 -> 18432: 80 columns 27.3 us, 48 columns (384 workgroups)
+// 32.1, 32 (576) 29.8, 16 (1152) 32.1.  Bytes in flight count too: the
+// L2 of an XCD holds the lines that 32 compute units wait for, and beyond
+// about 80 KiB each it slows down (80 columns with two steps a wave in flight
+// 30.1 us, 32 columns with two, three, four 29.8, 33.6, 38.4).
 template <int kX, bool kGlu>
 hipError_t start_shape(const MxArgs& a, hipStream_t stream) {
-  if constexpr (kGlu) return start_rows<kX, 2, true, 4>(a, stream);
-  if (a.N >= 32 * 192) return start_rows<kX, 2, false, 16>(a, stream);
-  return start_rows<kX, 1, false, 8>(a, stream);
+  if constexpr (kGlu && kX == kMxXfp4) {  // (h's blocks of 32 columns stay in a workgroup)
+    const int m2 = most_blocks(a.N, 2), m4 = most_blocks(a.N, 4), m6 = most_blocks(a.N, 6);
+    if (m6 <= m4 && m6 <= m2) return start_rows<kX, 6, true, 8, 1>(a, stream);
+    if (m4 <= m2) return start_rows<kX, 4, true, 8, 1>(a, stream);
+    return start_rows<kX, 2, true, 4, 2>(a, stream);
+  } else {
+    const int m1 = most_blocks(a.N, 1), m2 = most_blocks(a.N, 2), m5 = most_blocks(a.N, 5);
+    if (m5 <= m2 && m5 <= m1) return start_rows<kX, 5, kGlu, 8, kGlu ? 1 : 2>(a, stream);
+    if (m2 <= m1) return start_rows<kX, 2, kGlu, kGlu ? 4 : 8, 2>(a, stream);
+    return start_rows<kX, 1, kGlu, 8, kGlu ? 2 : 4>(a, stream);
+  }
 }
 
 }  // namespace

@@ -105,6 +105,34 @@ def test_gemm(M, K, N, kind, yt):
     assert torch.equal(y, again)
 
 
+# widths at which a workgroup of a few rows takes one, two, four to six blocks of columns
+WIDE = [(1, 160, 4112), (4, 96, 18448), (7, 288, 8208), (8, 160, 16400), (13, 96, 20400), (16, 416, 4112)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("M,K,N", WIDE)
+def test_gemm_of_few_rows_and_many_columns(M, K, N, kind):
+    rng = np.random.default_rng(M + N)
+    w, wv = weight(rng, N, K)
+    x, xv = rows(rng, M, K, kind)
+    y = torch.full((M + 1, N), 7.0, device="cuda")
+    L.mx_gemm(x, w, y[:M], L.new_workspace(L.mx_gemm_workspace_bytes(M, code_of(kind), w)))
+    check(y[:M], xv @ wv.T, out_bound(xv @ wv.T, gemm_bound(xv, wv, kind), torch.float32), f"{M}x{K}x{N} {kind}")
+    assert y[M].eq(7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("M,H,I", [(3, 96, 18464), (6, 160, 4128), (16, 96, 18464), (2, 64, 10272), (11, 32, 24608)])
+def test_swiglu_mlp_of_few_rows_and_a_wide_intermediate(M, H, I, kind):
+    rng = np.random.default_rng(M + H + I)
+    (g, gv), (u, uv), (d, dv) = weight(rng, I, H, 0.2), weight(rng, I, H, 0.2), weight(rng, H, I, 0.06)
+    x, xv = rows(rng, M, H, kind)
+    y = torch.empty((M, H), device="cuda")
+    L.mx_swiglu_mlp(x, g, u, d, y, L.new_workspace(L.mx_swiglu_mlp_workspace_bytes(M, code_of(kind), g, u, d)))
+    ref, b = mlp_reference(xv, gv, uv, dv, kind)
+    check(y, ref, out_bound(ref, b, torch.float32), f"{M}x{H}x{I} {kind}")
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
 @pytest.mark.parametrize("M", [3, 40, 300])
 def test_gemm_scales_over_the_whole_range(M, kind):
