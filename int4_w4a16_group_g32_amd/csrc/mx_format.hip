@@ -102,43 +102,57 @@ __global__ __launch_bounds__(256) void mx_prepack_kernel(const uint4* __restrict
   dst_scales[tiled_scale(r, g, S)] = in ? scales[r * G + g] : 127;
 }
 
-__device__ __forceinline__ float mx_value(uint32_t code, float scale) {
-  // E2M1's fields as a float's: 0.5 (code 1) is its only subnormal
-  const uint32_t e = (code >> 1) & 3, m = code & 1;
-  const float mag = e == 0 ? 0.5f * m : __uint_as_float(((e + 126) << 23) | (m << 22));
-  return (code & 8 ? -mag : mag) * scale;
-}
-
-// One thread per eight values.
-template <typename T>
+// One thread per kE times eight values, a block's threads side by side: wave
+// stores of 1 KiB (bf16) or 2 KiB.
+constexpr int kE = 4;
+template <typename T, bool kTiled>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, size_t n8, int G,
-                                                            int S, int tiled, T* __restrict__ out) {
-  const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;
-  if (i >= n8) return;
-  size_t word = i, sc = i >> 2;
-  if (tiled) {
-    const size_t r = (i >> 2) / G;
-    const int g = static_cast<int>((i >> 2) % G);
-    word = tiled_unit(r, g, S) * 4 + (i & 3);
-    sc = tiled_scale(r, g, S);
+                                                            int S, T* __restrict__ out) {
+  const size_t i0 = blockIdx.x * static_cast<size_t>(256 * kE) + threadIdx.x;
+  uint32_t c[kE], byte[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    const size_t i = i0 + 256 * e;
+    if (i >= n8) break;
+    size_t word = i, sc = i >> 2;
+    if constexpr (kTiled) {
+      const size_t r = (i >> 2) / G;
+      const int g = static_cast<int>((i >> 2) % G);
+      word = tiled_unit(r, g, S) * 4 + (i & 3);
+      sc = tiled_scale(r, g, S);
+    }
+    c[e] = codes[word];
+    byte[e] = scales[sc];
   }
-  const uint32_t c = codes[word], byte = scales[sc];
-  // 2^-127 is a subnormal float; 255 is NaN
-  const float s = byte == 255 ? __uint_as_float(0x7fc00000u)
-                              : (byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23));
-  float v[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = mx_value((c >> (4 * j)) & 15u, s);
-  if constexpr (sizeof(T) == 4) {
-    float4* o = reinterpret_cast<float4*>(out + 8 * i);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t b[4];
+  for (int e = 0; e < kE; ++e) {
+    const size_t i = i0 + 256 * e;
+    if (i >= n8) break;
+    // (byte 0 is 2^-127, a subnormal float; 255 is NaN)
+    const float s = __uint_as_float(byte[e] == 255 ? 0x7fc00000u : (byte[e] == 0 ? 0x00400000u : byte[e] << 23));
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = f32_to_bf16(v[2 * j]) | static_cast<uint32_t>(f32_to_bf16(v[2 * j + 1])) << 16;
-    *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(b[0], b[1], b[2], b[3]);
+    for (int j = 0; j < 4; ++j) {
+      // exact: a code has two significant bits
+      const f32x2 p = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[e], 1.0f, 0)
+                      : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[e], 1.0f, 1)
+                      : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[e], 1.0f, 2)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[e], 1.0f, 3);
+      v[2 * j] = p[0] * s;
+      v[2 * j + 1] = p[1] * s;
+    }
+    if constexpr (sizeof(T) == 4) {
+      float4* o = reinterpret_cast<float4*>(out + 8 * i);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        b[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
+      *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
   }
 }
 
@@ -246,12 +260,16 @@ extern "C" w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4
   if (out_bytes < n * dtype_bytes(ot)) return W4A16_ERR_INVALID_ARG;
   if (n == 0) return W4A16_OK;
   const uint32_t* c = reinterpret_cast<const uint32_t*>(m->codes);
-  const int G = m->K / kMxBlock, S = (m->K + kMxStep - 1) / kMxStep, tiled = m->layout == W4A16_MX_TILED;
-  if (ot == W4A16_F32)
-    mx_dequantize_kernel<<<blocks_for(n / 8), 256, 0, stream>>>(c, m->scales, n / 8, G, S, tiled,
-                                                                static_cast<float*>(out));
-  else
-    mx_dequantize_kernel<<<blocks_for(n / 8), 256, 0, stream>>>(c, m->scales, n / 8, G, S, tiled,
-                                                                static_cast<uint16_t*>(out));
+  const int G = m->K / kMxBlock, S = (m->K + kMxStep - 1) / kMxStep;
+  const bool tiled = m->layout == W4A16_MX_TILED;
+  const unsigned blocks = blocks_for((n / 8 + kE - 1) / kE);
+  auto run = [&](auto kernel, auto* o) { kernel<<<blocks, 256, 0, stream>>>(c, m->scales, n / 8, G, S, o); };
+  if (ot == W4A16_F32) {
+    float* o = static_cast<float*>(out);
+    tiled ? run(mx_dequantize_kernel<float, true>, o) : run(mx_dequantize_kernel<float, false>, o);
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out);
+    tiled ? run(mx_dequantize_kernel<uint16_t, true>, o) : run(mx_dequantize_kernel<uint16_t, false>, o);
+  }
   return launch_status();
 }

@@ -21,31 +21,50 @@ struct NormArgs {
   const void *y, *r, *post_w, *gate, *pre_w;
   void *r_out, *n;
   uint8_t* n_scales;
-  int H, gate_rows;
+  int M, H, gate_rows;
   int y_bf16, r_bf16, w_bf16, n_bf16;
   double alpha, eps;
 };
 
-// Eight values from element 8 i.
-__device__ __forceinline__ void get8(const void* p, size_t i, int bf16, float v[8]) {
-  if (bf16) {
-    const uint4 a = static_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight values from element 8 i, as they are stored; kB: bf16 for certain.
+template <bool kB>
+struct Raw8 {
+  uint4 v[kB ? 1 : 2];
+};
+template <bool kB>
+__device__ __forceinline__ Raw8<kB> get8(const void* p, size_t i, int bf16) {
+  Raw8<kB> r;
+  if constexpr (kB) {
+    r.v[0] = static_cast<const uint4*>(p)[i];
+  } else if (bf16) {
+    r.v[0] = static_cast<const uint4*>(p)[i];
+  } else {
+    r.v[0] = static_cast<const uint4*>(p)[2 * i];
+    r.v[1] = static_cast<const uint4*>(p)[2 * i + 1];
+  }
+  return r;
+}
+template <bool kB>
+__device__ __forceinline__ void values8(const Raw8<kB>& r, int bf16, float v[8]) {
+  constexpr int l = kB ? 0 : 1;
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[l].x, r.v[l].y, r.v[l].z, r.v[l].w};
+  if (kB || bf16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(w[j] << 16);
       v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
   } else {
-    const float4 a = static_cast<const float4*>(p)[2 * i], b = static_cast<const float4*>(p)[2 * i + 1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
   }
 }
 __device__ __forceinline__ void put8(void* p, size_t i, int bf16, const float v[8]) {
   if (bf16) {
     uint32_t b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = f32_to_bf16(v[2 * j]) | static_cast<uint32_t>(f32_to_bf16(v[2 * j + 1])) << 16;
+    for (int j = 0; j < 4; ++j)
+      b[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
     static_cast<uint4*>(p)[i] = make_uint4(b[0], b[1], b[2], b[3]);
   } else {
     static_cast<float4*>(p)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
@@ -63,12 +82,12 @@ __device__ __forceinline__ float rounded_to_odd(double v) {
   return b == a || (u & 1) || !(b <= 3.4028234663852886e38) ? f : __uint_as_float(b > a ? u - 1 : u + 1);
 }
 
+// Sum over the workgroup, the same bits in every thread.
 template <typename F>
 __device__ __forceinline__ F row_sum(F v, F* lds) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   const int waves = static_cast<int>(blockDim.x) >> 6;
-  __syncthreads();  // (the previous sum is read)
   if (lane_id() == 0) lds[wave_id()] = v;
   __syncthreads();
   F t = lds[0];
@@ -76,115 +95,197 @@ __device__ __forceinline__ F row_sum(F v, F* lds) {
   return t;
 }
 
+// A block's 32 values lie in four threads.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 1)));
+  return max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 2)));
+}
+
+// Codes and scale byte of n = s * w * pre, eight values of a block of 32, as
+// float64 gives them.  The products are first taken in float32, off by at most
+// four half-steps; borders between codes, and powers of two, have at most two
+// mantissa bits, so a value whose lower 21 are 16 steps or more from all zeros
+// is on the same side in float64.  Where some value of the wave is nearer (1 in
+// 2^17), the wave goes by float64.
+__device__ __forceinline__ uint32_t codes_of(const float s[8], const float w[8], double pre, uint32_t& byte) {
+  const float p = static_cast<float>(pre);
+  float v[8];
+  uint32_t m = 0, low = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = s[j] * w[j] * p;
+    const uint32_t u = __float_as_uint(v[j]);
+    m = max(m, u & 0x7fffffffu);
+    low = min(low, (u + 16) & 0x1fffffu);
+  }
+  m = quad_max(m);
+  // (beside a largest of 2^-90 what float32 flushed is code 0 either way)
+  const bool near = low < 32 || m < (127u - 90u) << 23 || m >= 255u << 23 || !(p > 0x1p-100f && p < 0x1p100f);
+  float o[8];
+  if (!__any(near)) {
+    byte = mx_scale_byte(m);
+    const float inv = mx_scale_inverse(byte);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = v[j] * inv;
+    return mx_codes8(o);
+  }
+  double d[8];
+  m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    d[j] = static_cast<double>(s[j]) * pre * w[j];
+    // (the upper half orders magnitudes by their exponents, which is all a scale needs)
+    m = max(m, static_cast<uint32_t>(__double_as_longlong(d[j]) >> 32) & 0x7fffffffu);
+  }
+  m = quad_max(m);
+  const bool bad = m >= (1023u + 128u) << 20;  // no float: beyond its range, an infinity or NaN
+  byte = bad ? 255u : static_cast<uint32_t>(max(static_cast<int>(m >> 20) - 1023 - 2 + 127, 0));
+  // 2^(127 - byte), exact in float64
+  const double inv = __longlong_as_double(static_cast<long long>(1023 + 127 - static_cast<int>(byte)) << 52);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = bad ? 0.0f : rounded_to_odd(d[j] * inv);
+  return mx_codes8(o);
+}
+
 // kC chunks of eight values a thread; chunk c of thread t is t + c * blockDim.x.
-template <int kC, bool kMx>
-__global__ __launch_bounds__(1024) void block_norm_kernel(const NormArgs a) {
+// kB: y, r, the weights and gate are bf16; then a workgroup takes rows
+// blockIdx.x, + gridDim.x, ..., and asks for the next row's values as soon as it
+// holds s of its own (else one row: the values of two would not fit).
+template <int kC, bool kMx, bool kB>
+__global__ __launch_bounds__(kB && kC > 1 ? 512 : 1024) void block_norm_kernel(const NormArgs a) {
   using F = std::conditional_t<kMx, double, float>;
-  __shared__ F lds[16];
+  constexpr bool kEarly = kB || kC == 1;  // (else too many registers)
+  __shared__ F lds[2][2][16];
   const int t = static_cast<int>(threadIdx.x), T = static_cast<int>(blockDim.x);
   const int n8 = a.H / 8;
-  const size_t row = blockIdx.x, base = row * n8;
-  float in[8];
-  F s[kC][8];
+  // products of three bf16 values are exact in float32
+  const bool exact = kB || (a.y_bf16 && a.w_bf16);
+  Raw8<kB> y[kC], r[kC], g[kC], pw[kC], nw[kC];
+  auto load = [&](int row) {
+    const size_t base = static_cast<size_t>(row) * n8;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    const int i = t + c * T;
+    for (int c = 0; c < kC; ++c) {
+      const int i = t + c * T;
+      if (i >= n8) continue;
+      y[c] = get8<kB>(a.y, base + i, a.y_bf16);
+      if (kEarly && a.r != nullptr) r[c] = get8<kB>(a.r, base + i, a.r_bf16);
+      if (kEarly && a.gate != nullptr) g[c] = get8<kB>(a.gate, (a.gate_rows == 1 ? 0 : base) + i, a.w_bf16);
+      if (kC == 1 && a.post_w != nullptr) pw[c] = get8<kB>(a.post_w, i, a.w_bf16);
+    }
+  };
+  load(blockIdx.x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) in[j] = 0.0f;
-    if (i < n8) get8(a.y, base + i, a.y_bf16, in);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[c][j] = in[j];
-  }
-  F post = 1;
-  if (a.post_w != nullptr) {
-    F q = 0;
-#pragma unroll
-    for (int c = 0; c < kC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q += s[c][j] * s[c][j];
-    post = 1 / sqrt(row_sum(q, lds) / a.H + static_cast<F>(a.eps));
-  }
-  F q = 0;
-#pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    const int i = t + c * T;
-    if (i >= n8) continue;
-    float w[8];
+  for (int c = 0; c < kC; ++c)
+    if (kC == 1 && a.n != nullptr && t < n8) nw[c] = get8<kB>(a.pre_w, t, a.w_bf16);
+  int turn = 0;
+  for (int row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+    const size_t base = static_cast<size_t>(row) * n8;
+    F scale = static_cast<F>(a.alpha);
     if (a.post_w != nullptr) {
-      get8(a.post_w, i, a.w_bf16, w);
+      F q = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[c][j] = s[c][j] * post * w[j];
-    }
-    if (a.gate != nullptr) {
-      get8(a.gate, (a.gate_rows == 1 ? 0 : base) + i, a.w_bf16, w);
+      for (int c = 0; c < kC; ++c) {
+        if (t + c * T >= n8) continue;
+        float v[8];
+        values8(y[c], a.y_bf16, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[c][j] *= w[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[c][j] *= static_cast<F>(a.alpha);
-    if (a.r != nullptr) {
-      get8(a.r, base + i, a.r_bf16, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[c][j] += w[j];
-    }
-    // s as it is stored
-    float o[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      o[j] = static_cast<float>(s[c][j]);
-      if (a.r_bf16) o[j] = bf16_to_f32(f32_to_bf16(o[j]));
-      s[c][j] = o[j];
-      q += s[c][j] * s[c][j];
-    }
-    if (a.r_out != nullptr) put8(a.r_out, base + i, a.r_bf16, o);
-  }
-  if (a.n == nullptr) return;
-  const F pre = 1 / sqrt(row_sum(q, lds) / a.H + static_cast<F>(a.eps));
-#pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    const int i = t + c * T;
-    if (i >= n8) continue;  // (four threads of a block of 32 go together)
-    float w[8];
-    get8(a.pre_w, i, a.w_bf16, w);
-    if constexpr (!kMx) {
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = s[c][j] * pre * w[j];
-      put8(a.n, base + i, a.n_bf16, o);
-    } else {
-      double v[8], m = 0;
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = s[c][j] * pre * w[j];
-        bad |= !(fabs(v[j]) <= 3.4028234663852886e38);
-        m = fmax(m, fabs(v[j]));
+        for (int j = 0; j < 8; ++j) q += static_cast<F>(v[j]) * static_cast<F>(v[j]);
       }
-      m = fmax(m, __shfl_xor(m, 1));
-      m = fmax(m, __shfl_xor(m, 2));
-      int b = bad;
-      b |= __shfl_xor(b, 1);
-      b |= __shfl_xor(b, 2);
-      // floor(log2 m) - 2, at least -127 (0 and float64 subnormals have exponent field 0)
-      const int e = static_cast<int>(__double_as_longlong(m) >> 52) - 1023;
-      const uint32_t byte = b ? 255u : static_cast<uint32_t>(max(e - 2 + 127, 0));
-      // 2^(127 - byte), exact in float64
-      const double inv = __longlong_as_double(static_cast<long long>(1023 + 127 - static_cast<int>(byte)) << 52);
-      float o[8];
+      scale *= 1 / sqrt(row_sum(q, lds[turn][0]) / a.H + static_cast<F>(a.eps));
+    }
+    F q = 0;
+    float s[kC][8];  // s as it is stored
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = b ? 0.0f : rounded_to_odd(v[j] * inv);
-      static_cast<uint32_t*>(a.n)[base + i] = mx_codes8(o);
-      if ((i & 3) == 0) a.n_scales[(base + i) >> 2] = static_cast<uint8_t>(byte);
+    for (int c = 0; c < kC; ++c) {
+      const int i = t + c * T;
+      if (i >= n8) continue;
+      float v[8], w[8];
+      F p[8];
+      if (!kEarly && a.r != nullptr) r[c] = get8<kB>(a.r, base + i, a.r_bf16);
+      if (!kEarly && a.gate != nullptr) g[c] = get8<kB>(a.gate, (a.gate_rows == 1 ? 0 : base) + i, a.w_bf16);
+      if (kC > 1 && a.post_w != nullptr) pw[c] = get8<kB>(a.post_w, i, a.w_bf16);
+      values8(y[c], a.y_bf16, v);
+      if (!kMx || exact) {
+        if (a.post_w != nullptr) {
+          values8(pw[c], a.w_bf16, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+        }
+        if (a.gate != nullptr) {
+          values8(g[c], a.w_bf16, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = v[j];
+        if (a.post_w != nullptr) {
+          values8(pw[c], a.w_bf16, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] *= w[j];
+        }
+        if (a.gate != nullptr) {
+          values8(g[c], a.w_bf16, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] *= w[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+      if (a.r != nullptr) values8(r[c], a.r_bf16, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[c][j] = static_cast<float>(p[j] * scale + static_cast<F>(w[j]));
+      if (kB || a.r_bf16) {
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          b[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{s[c][2 * j], s[c][2 * j + 1]}, bf16x2));
+          s[c][2 * j] = __uint_as_float(b[j] << 16);
+          s[c][2 * j + 1] = __uint_as_float(b[j] & 0xffff0000u);
+        }
+        if (a.r_out != nullptr) static_cast<uint4*>(a.r_out)[base + i] = make_uint4(b[0], b[1], b[2], b[3]);
+      } else if (a.r_out != nullptr) {
+        put8(a.r_out, base + i, 0, s[c]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q += static_cast<F>(s[c][j]) * static_cast<F>(s[c][j]);
+    }
+    if (kB && row + static_cast<int>(gridDim.x) < a.M) load(row + gridDim.x);
+    if (a.n == nullptr) continue;
+    const F pre = 1 / sqrt(row_sum(q, lds[turn][1]) / a.H + static_cast<F>(a.eps));
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int i = t + c * T;
+      if (i >= n8) continue;  // (four threads of a block of 32 go together)
+      if (kC > 1) nw[c] = get8<kB>(a.pre_w, i, a.w_bf16);
+      float w[8];
+      values8(nw[c], a.w_bf16, w);
+      if constexpr (!kMx) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = s[c][j] * pre * w[j];
+        put8(a.n, base + i, a.n_bf16, o);
+      } else {
+        uint32_t byte;
+        static_cast<uint32_t*>(a.n)[base + i] = codes_of(s[c], w, pre, byte);
+        if ((i & 3) == 0) a.n_scales[(base + i) >> 2] = static_cast<uint8_t>(byte);
+      }
     }
   }
 }
 
-template <int kC>
-void start(const NormArgs& a, bool mx, int M, int T, hipStream_t stream) {
+constexpr int kCus = 256;
+
+template <int kC, bool kB>
+void start(const NormArgs& a, bool mx, int T, hipStream_t stream) {
+  // (a compute unit holds four workgroups of 256 threads with their next rows)
+  const int blocks = kB ? std::min(a.M, kCus * std::max(1, 1024 / T)) : a.M;
   if (mx)
-    block_norm_kernel<kC, true><<<M, T, 0, stream>>>(a);
+    block_norm_kernel<kC, true, kB><<<blocks, T, 0, stream>>>(a);
   else
-    block_norm_kernel<kC, false><<<M, T, 0, stream>>>(a);
+    block_norm_kernel<kC, false, kB><<<blocks, T, 0, stream>>>(a);
 }
 
 bool good_type(w4a16_dtype_t t) { return t == W4A16_F32 || t == W4A16_BF16; }
@@ -236,15 +337,19 @@ extern "C" w4a16_status_t w4a16_block_norm(const w4a16_norm_t* p, int32_t M, int
   NormArgs a{};
   a.y = p->y, a.r = p->r, a.post_w = p->post_w, a.gate = p->gate, a.pre_w = p->pre_w;
   a.r_out = p->r_out, a.n = mx ? p->n_codes : p->n, a.n_scales = p->n_scales;
-  a.H = H, a.gate_rows = p->gate_rows;
+  a.M = M, a.H = H, a.gate_rows = p->gate_rows;
   a.y_bf16 = p->y_type == W4A16_BF16, a.r_bf16 = p->r_type == W4A16_BF16;
   a.w_bf16 = p->w_type == W4A16_BF16, a.n_bf16 = p->n_type == W4A16_BF16;
   a.alpha = p->alpha, a.eps = p->eps;
+  // a thread's chunks: one where there are few rows (a row's latency counts),
+  // else as few as leave several rows to a compute unit (2048 bf16 rows of 7168
+  // to MXFP4: one chunk 57 us, two 36, four 44)
   const int n8 = H / 8;
-  const int C = n8 <= 1024 ? 1 : (n8 <= 2048 ? 2 : 4);
+  const int C = n8 <= 256 || (M <= kCus && n8 <= 1024) ? 1 : (n8 <= 1024 ? 2 : 4);
   const int T = ((n8 + C - 1) / C + 63) / 64 * 64;
-  if (C == 1) start<1>(a, mx, M, T, stream);
-  else if (C == 2) start<2>(a, mx, M, T, stream);
-  else start<4>(a, mx, M, T, stream);
+  const bool b = a.y_bf16 && a.w_bf16 && (a.r == nullptr || a.r_bf16) && a.r_bf16 && (C == 1 || T <= 512);
+  if (C == 1) b ? start<1, true>(a, mx, T, stream) : start<1, false>(a, mx, T, stream);
+  else if (C == 2) b ? start<2, true>(a, mx, T, stream) : start<2, false>(a, mx, T, stream);
+  else b ? start<4, true>(a, mx, T, stream) : start<4, false>(a, mx, T, stream);
   return launch_status();
 }

@@ -31,6 +31,10 @@ CASES = [
     (130, 256, "bf16", "bf16", "f32", True, "channel"), (33, 8200, "f32", "f32", "bf16", True, "row"),
     (5, 16392, "bf16", "bf16", "bf16", True, "channel"), (2, 32768, "f32", "f32", "f32", False, "none"),
     (1000, 96, "bf16", "f32", "bf16", False, "channel"),
+    # more rows than workgroups: each takes several
+    (600, 7168, "bf16", "bf16", "bf16", True, "row"), (1400, 2304, "bf16", "bf16", "bf16", False, "channel"),
+    (530, 16384, "bf16", "bf16", "bf16", True, "none"), (4100, 64, "bf16", "bf16", "bf16", True, "channel"),
+    (300, 7168, "f32", "f32", "f32", True, "row"),
 ]
 
 
