@@ -179,12 +179,13 @@ constexpr int kMxStreamRows = 16;
 // rows as bf16 planes [pieces][M][K], or MXFP4 rows; y as in MxArgs, or with glu
 // h as bf16 planes or MXFP4 rows.
 struct MxTileArgs : MxArgs {
-  float* planes;  // splits > 1: [splits][matrices][M][N]
-  int tiles, row_tiles, band, splits, sps;
+  float* planes;  // sums of shared tiles: [workgroup of a tile][matrices][M][N]
+  int tiles, row_tiles, band, bm, cols;
+  int unit_steps, per, quota;  // steps of a unit of K; units of a tile, and of a workgroup
 };
 struct MxTilePlan {
-  int bm = 0, cols = 0, tiles = 0, splits = 1, sps = 0;
-  size_t plane_bytes = 0;  // all splits'
+  int bm = 0, cols = 0, tiles = 0, unit_steps = 0, per = 0, quota = 0;
+  size_t plane_bytes = 0;  // 0: every tile is one workgroup's
 };
 MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu);
 hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream);

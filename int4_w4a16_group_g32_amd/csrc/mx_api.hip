@@ -5,23 +5,6 @@
 namespace w4 {
 namespace {
 
-// Tiles of `cols` columns, `bm` rows; K is split where the tiles alone leave
-// compute units idle.
-MxTilePlan tile_plan(int M, int N, int K, int bm, int cols, bool glu, int want) {
-  MxTilePlan p;
-  p.bm = bm;
-  p.cols = cols;
-  p.tiles = (N + cols - 1) / cols;
-  const int S = (K + kMxStep - 1) / kMxStep;
-  const int tasks = p.tiles * ((M + bm - 1) / bm);
-  const int most = std::max(1, S / 4);
-  p.splits = std::min(most, std::max(1, want / tasks));
-  p.sps = ((S + p.splits - 1) / p.splits + 1) / 2 * 2;  // (pairs of steps)
-  p.splits = (S + p.sps - 1) / p.sps;
-  if (p.splits > 1) p.plane_bytes = static_cast<size_t>(p.splits) * (glu ? 2 : 1) * M * N * 4;
-  return p;
-}
-
 w4a16_status_t check_mx_weight(const w4a16_mx_t* w) {
   const w4a16_status_t st = check_mx(w);
   if (st != W4A16_OK) return st;
@@ -197,12 +180,40 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
 
 }  // namespace
 
+// Row tiles of the height that the rows fill.  Where the tiles are fewer than
+// the compute units, their units of K (pairs of steps) are dealt out evenly to
+// one workgroup each, wherever that cuts a tile, if what this saves is more than
+// the shared tiles' sums cost: a float32 plane for each workgroup of a tile,
+// written and read at about 4 TB/s, and a launch of about 4 us.
 MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu) {
-  const int cols = glu ? 128 : 256;
-  const int bm = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
-  const size_t tasks256 = static_cast<size_t>((M + 255) / 256) * ((N + cols - 1) / cols);
-  if (bm == 256 && (tasks256 < 256 || xk == kMxXf32 || xk == kMxXf32h)) return tile_plan(M, N, K, 128, cols, glu, 256);
-  return tile_plan(M, N, K, bm, cols, glu, bm <= 64 ? 512 : 256);
+  constexpr int kCus = 256;
+  MxTilePlan p;
+  p.cols = glu ? 128 : 256;
+  p.tiles = (N + p.cols - 1) / p.cols;
+  const int S = (K + kMxStep - 1) / kMxStep;
+  p.bm = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
+  const bool wide = xk == kMxXf32 || xk == kMxXf32h;
+  if (p.bm == 256 && (wide || static_cast<size_t>((M + 255) / 256) * p.tiles < kCus)) p.bm = 128;
+  const size_t tiles = static_cast<size_t>((M + p.bm - 1) / p.bm) * p.tiles;
+  if (tiles < kCus && S > 2) {
+    p.unit_steps = 2;
+    p.per = (S + 1) / 2;
+    p.quota = std::max(2, static_cast<int>((tiles * p.per + kCus - 1) / kCus));
+    const int most = (p.per + p.quota - 2) / p.quota + 1;  // workgroups of a tile
+    // a unit: 256 k, at 5 (bf16 planes) or 12 TFLOP/s of a compute unit, and at
+    // least its 35 KB of codes and scales at its share of 6 TB/s
+    const double planes = xk == kMxXf32 ? 3 : (xk == kMxXf32h ? 2 : 1);
+    const double unit_us = std::max(2.0 * p.bm * 256 * 256 * planes / (xk == kMxXfp4 ? 12e6 : 5e6), 35e3 / 23e3);
+    const double bytes = 4.0 * M * N * (glu ? 2 : 1);
+    const double shared = std::min<double>(most, 1 + static_cast<double>(p.per) / p.quota);
+    if (p.quota < p.per && (p.per - p.quota) * unit_us > 4 + 2 * shared * bytes / 4e6) {
+      p.plane_bytes = static_cast<size_t>(most) * (glu ? 2 : 1) * M * N * 4;
+      return p;
+    }
+  }
+  p.unit_steps = S;
+  p.per = p.quota = 1;
+  return p;
 }
 
 }  // namespace w4

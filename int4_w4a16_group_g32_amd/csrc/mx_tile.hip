@@ -4,8 +4,8 @@
 // mx_stream.hip: the weights are the matrix cores' first operand, the rows of x
 // the second, and a lane ends with four adjacent columns of one row.
 //
-// A workgroup has eight waves, kWM along the rows and kWN along the columns, a
-// wave kMB x kNB blocks of 16 x 16.  The rows of one stage of K (128 of bf16,
+// A workgroup has eight waves, kWM along the rows, kWN along the columns and
+// kWK along K, a wave kMB x kNB blocks of 16 x 16.  The rows of one stage of K (128 of bf16,
 // 256 of MXFP4) are staged in LDS, double-buffered, one barrier a stage; each
 // wave streams its own columns' codes into registers two steps ahead and, for
 // 16-bit rows, expands them there.  float32 rows come as bf16 planes (pieces
@@ -65,17 +65,18 @@ __device__ __forceinline__ float scale_byte(int c, uint32_t d) {
 }
 
 // kP: bf16 planes of x (1 .. 3), or 0 for MXFP4 rows.
-template <int kP, int kWM, int kWN, int kMB, int kNB, bool kGlu>
+template <int kP, int kWM, int kWN, int kWK, int kMB, int kNB, bool kGlu>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void mx_tile_kernel(const MxTileArgs a) {
-  static_assert(kWM * kWN * 64 == kThreads, "eight waves");
+  static_assert(kWM * kWN * kWK * 64 == kThreads, "eight waves");
   constexpr bool kFp4 = kP == 0;
+  static_assert(!kFp4 || kWK == 1, "MXFP4 rows: no waves along K");
   constexpr int kPlanes = kFp4 ? 1 : kP;
   constexpr int kMats = kGlu ? 2 : 1;
   constexpr int kNbM = kNB / kMats;                       // blocks of each matrix
   constexpr int kBM = 16 * kMB * kWM, kCols = 16 * kNbM;  // rows of the tile; columns of a wave
   constexpr int kBN = kCols * kWN;
-  constexpr int kChunks = kFp4 ? 8 : 16;                  // 16-byte chunks of a row and stage
-  constexpr int kSteps = kFp4 ? 2 : 1;                    // steps of 128 k in a stage
+  constexpr int kSteps = kFp4 ? 2 : kWK;                  // steps of 128 k in a stage
+  constexpr int kChunks = kFp4 ? 8 : 16 * kWK;            // 16-byte chunks of a row and stage
   constexpr int kUnits = (kBM * kChunks + kThreads - 1) / kThreads;  // chunks staged by a thread
   constexpr int kParts = kFp4 ? 2 : 4;                    // of a stage's compute, between which they are staged
   constexpr int kScaleUnits = kFp4 ? (kBM * 8 + kThreads - 1) / kThreads : 0;  // scale bytes staged by a thread
@@ -85,39 +86,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
   __shared__ Buffer lds[2];
 
-  // XCD x = b mod 8 takes a contiguous run of tasks.  Tasks go through bands of
-  // `band` row tiles column by column, so a run is a block of row and column
-  // tiles whose rows and codes its L2 reads once (launch_mx_tile picks the band).
+  // XCD x = b mod 8 takes a contiguous run of workgroups
   const int T = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
   const int xcd = b % kXcds, tq = T / kXcds, trem = T % kXcds;
   const int task = xcd * tq + min(xcd, trem) + b / kXcds;
-  const int split = task / (a.row_tiles * a.tiles), u = task % (a.row_tiles * a.tiles);
-  const int band0 = u / (a.band * a.tiles) * a.band, in_band = min(a.band, a.row_tiles - band0);
-  const int v = u - band0 * a.tiles;
-  const int tile = v / in_band, r0 = (band0 + v % in_band) * kBM;
-  const int nrows = min(kBM, a.M - r0);
-  const int s_lo = split * a.sps, s_hi = min(a.S, s_lo + a.sps);
-
   const int t = static_cast<int>(threadIdx.x), wv = wave_id(), lane = lane_id();
   const int lr = lane & 15, kb = lane >> 4;
-  const int wm = wv / kWN, wn = wv % kWN;
-  const int n0 = tile * kBN + wn * kCols;  // the wave's first column
-  const int J = n0 / kMxTileRows, c0 = n0 / 16 % 4;
+  const int wk = wv / (kWM * kWN), wm = wv / kWN % kWM, wn = wv % kWN;
   const int tiles64 = (a.N + kMxTileRows - 1) / kMxTileRows;
   const size_t cb = static_cast<size_t>(a.S) * kMxTileCodes, sb = static_cast<size_t>(a.S) * kMxTileScales;
 
-  // (a wave past the last column streams tile 0 and stores nothing)
-  const size_t Jr = J < tiles64 ? J : 0;
-  __amdgpu_buffer_rsrc_t wr[kMats], sr[kMats];
-#pragma unroll
-  for (int m = 0; m < kMats; ++m) {
-    wr[m] = rsrc(a.wc[m] + Jr * cb, cb);
-    sr[m] = rsrc(a.ws[m] + Jr * sb, sb);
-  }
   struct Codes {
     u32x4 w[kMats][kNbM];
     uint32_t s[kMats];
   };
+  __amdgpu_buffer_rsrc_t wr[kMats], sr[kMats];
+  int r0, nrows, n0, c0, s_lo, s_hi;  // the segment's rows, the wave's columns, K steps
   auto load_codes = [&](Codes& c, int s) {
     s = min(s, a.S - 1);  // (past the end: read again, not used)
 #pragma unroll
@@ -131,10 +115,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   // staging: rows past the last one and k past K read as zeros
   const size_t xrow = kFp4 ? a.K / 2 : static_cast<size_t>(a.K) * 2;
   const size_t plane = static_cast<size_t>(a.M) * xrow;
-  const char* xbase = static_cast<const char*>(a.x) + r0 * xrow;
+  const char* xbase;
   const int G = a.K / kMxBlock;
-  const __amdgpu_buffer_rsrc_t xsr =
-      rsrc(kFp4 ? a.xs + static_cast<size_t>(r0) * G : nullptr, kFp4 ? static_cast<size_t>(nrows) * G : 0);
+  __amdgpu_buffer_rsrc_t xsr;
   const int chunk = t % kChunks, srow = t / kChunks;
   constexpr int kRowsAt = kThreads / kChunks;  // rows staged by one unit of all threads
   u32x4 held[kUnits];
@@ -143,7 +126,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   auto stage_load = [&](int i, int s, int p) {
     const int row = srow + i * kRowsAt;
     const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
-    const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s < s_hi;
+    const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s + (kFp4 ? 0 : chunk / 16) < s_hi;
     held[i] = load16(rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
   };
   auto stage_store = [&](Buffer& buf, int i) {
@@ -163,11 +146,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
 
   f32x4 acc[kMB][kNB];
-#pragma unroll
-  for (int i = 0; i < kMB; ++i)
-#pragma unroll
-    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
   // unit i is staged in part i * kParts / kUnits of the compute
   auto part_of = [](int i) { return i * kParts / kUnits; };
   auto load_part = [&](int part, int s, int p) {
@@ -196,6 +174,43 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
 
   Codes ring[2];
+  // Units of K (stages of all tiles in a row, a.per of them) are dealt out in
+  // runs of a.quota to workgroups; a run may cross tiles.
+  int unit = task * a.quota;
+  const int unit_end = min(unit + a.quota, a.per * a.tiles * a.row_tiles);
+  for (bool again = false; unit < unit_end; again = true) {
+  // Tiles go through bands of `band` row tiles column by column, so the
+  // workgroups of an XCD share a block of row and column tiles whose rows and
+  // codes its L2 reads once (launch_mx_tile picks the band).
+  const int u = unit / a.per, at = unit - u * a.per, run = min(a.per - at, unit_end - unit);
+  const int band0 = u / (a.band * a.tiles) * a.band, in_band = min(a.band, a.row_tiles - band0);
+  const int tile = (u - band0 * a.tiles) / in_band;
+  r0 = (band0 + (u - band0 * a.tiles) % in_band) * kBM;
+  nrows = min(kBM, a.M - r0);
+  s_lo = at * a.unit_steps;
+  s_hi = min(a.S, (at + run) * a.unit_steps);
+  const bool whole = run == a.per;
+  const int slot = task - u * a.per / a.quota;  // among the workgroups of this tile
+  unit += run;
+  n0 = tile * kBN + wn * kCols;
+  c0 = n0 / 16 % 4;
+  {
+    // (a wave past the last column streams tile 0 and stores nothing)
+    const size_t J = n0 / kMxTileRows < tiles64 ? n0 / kMxTileRows : 0;
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) {
+      wr[m] = rsrc(a.wc[m] + J * cb, cb);
+      sr[m] = rsrc(a.ws[m] + J * sb, sb);
+    }
+  }
+  xbase = static_cast<const char*>(a.x) + r0 * xrow;
+  if constexpr (kFp4) xsr = rsrc(a.xs + static_cast<size_t>(r0) * G, static_cast<size_t>(nrows) * G);
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (again) __syncthreads();  // (the last segment's LDS is read)
+
   // Loads are issued in the order of their use, here as in the loops (the
   // barriers keep the compiler from moving them): its waits then leave all
   // later ones in flight.
@@ -213,12 +228,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
       __builtin_amdgcn_sched_barrier(0);
     }
   } else {
-    load_codes(ring[0], s_lo);
+    load_codes(ring[0], s_lo + wk);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int part = 0; part < kParts; ++part) load_part(part, s_lo + 1 / kPlanes, 1 % kPlanes);
+    for (int part = 0; part < kParts; ++part) load_part(part, s_lo + 1 / kPlanes * kWK, 1 % kPlanes);
     __builtin_amdgcn_sched_barrier(0);
-    load_codes(ring[1], s_lo + 1);
+    load_codes(ring[1], s_lo + kWK + wk);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -257,7 +272,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   } else {
     int q = 0;
     // (s_next, p_next): two stages on
-    auto stage = [&](Codes& c, int s_next, int p_next) {
+    auto stage = [&](Codes& c, bool on, int s_next, int p_next) {
       __syncthreads();
       const Buffer& cur = lds[q & 1];
       Buffer& nxt = lds[(q + 1) & 1];
@@ -272,6 +287,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
         store_part(nxt, part);
         load_part(part, s_next, p_next);
         __builtin_amdgcn_sched_barrier(0);
+        if (kWK > 1 && !on) continue;
         bf16x8 w[kNB];
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
@@ -279,23 +295,48 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
           for (int j = 0; j < kNbM; ++j) w[m * kNbM + j] = mx_bf16(c.w[m][j][part], f[m][j]);
 #pragma unroll
         for (int i = 0; i < kMB; ++i) {
-          const bf16x8 xf = __builtin_bit_cast(bf16x8, xfrag(cur, i, 4 * kb + part));
+          const bf16x8 xf = __builtin_bit_cast(bf16x8, xfrag(cur, i, 16 * wk + 4 * kb + part));
 #pragma unroll
           for (int j = 0; j < kNB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], xf, acc[i][j], 0, 0, 0);
         }
       }
     };
-    for (int s = s_lo; s < s_hi; s += 2) {
+    for (int s = s_lo; s < s_hi; s += 2 * kWK) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (s + h >= s_hi) break;
+        const int sh = s + h * kWK;
+        if (sh >= s_hi) break;
 #pragma unroll 1
         for (int p = 0; p < kPlanes; ++p)
-          stage(ring[h], p + 2 < kPlanes ? s + h : s + h + (p + 2) / kPlanes, (p + 2) % kPlanes);
-        load_codes(ring[h], s + h + 2);
+          stage(ring[h], sh + wk < s_hi, p + 2 < kPlanes ? sh : sh + (p + 2) / kPlanes * kWK, (p + 2) % kPlanes);
+        load_codes(ring[h], sh + 2 * kWK + wk);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+  }
+
+  // the waves along K meet in LDS, in their order
+  if constexpr (kWK > 1) {
+    static_assert(sizeof(lds) >= kWM * kWN * kMB * kNB * 64 * sizeof(f32x4), "room for a wave group's sums");
+    f32x4(*red)[kMB][kNB][64] = reinterpret_cast<f32x4(*)[kMB][kNB][64]>(&lds[0]);
+    const int wg = wv % (kWM * kWN);
+    for (int k = 1; k < kWK; ++k) {
+      __syncthreads();
+      if (wk == k) {
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+          for (int j = 0; j < kNB; ++j) red[wg][i][j][lane] = acc[i][j];
+      }
+      __syncthreads();
+      if (wk == 0) {
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+          for (int j = 0; j < kNB; ++j) acc[i][j] += red[wg][i][j][lane];
+      }
+    }
+    if (wk != 0) continue;
   }
 
   // lane: row 16 i + lr of the wave, columns 4 kb .. + 3 of block j
@@ -304,14 +345,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     const int row = r0 + wm * 16 * kMB + 16 * i + lr;
     const bool row_ok = row < a.M;
     const size_t rowN = static_cast<size_t>(row) * a.N;
-    if (a.splits > 1) {
+    if (!whole) {
 #pragma unroll
       for (int m = 0; m < kMats; ++m)
 #pragma unroll
         for (int j = 0; j < kNbM; ++j) {
           const int n = n0 + 16 * j + 4 * kb;
           if (row_ok && n < a.N)
-            *reinterpret_cast<f32x4*>(a.planes + (static_cast<size_t>(split) * kMats + m) * a.M * a.N + rowN + n) =
+            *reinterpret_cast<f32x4*>(a.planes + (static_cast<size_t>(slot) * kMats + m) * a.M * a.N + rowN + n) =
                 acc[i][m * kNbM + j];
         }
     } else if constexpr (!kGlu) {
@@ -339,24 +380,30 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
       }
     }
   }
+  }
 }
 
-// ---------------------------------------------------------------- splits and planes
+// ---------------------------------------------------------------- shared tiles and planes
 
-// The splits' sums, in split order, to y or to h and its form for the down product.
+// The sums of tiles that several workgroups share, in their order along K, to y
+// or to h and its form for the down product.
 template <bool kGlu, int kOut>  // kOut: pieces of h (2, 3), 0: MXFP4 h; -: y
 __global__ __launch_bounds__(256) void mx_planes_kernel(const MxTileArgs a) {
   const size_t mn = static_cast<size_t>(a.M) * a.N;
   const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;  // four columns of a row
   if (i * 4 >= mn) return;
+  // (shared tiles are one band)
+  const int u = static_cast<int>(4 * i % a.N) / a.cols * a.row_tiles + static_cast<int>(4 * i / a.N) / a.bm;
+  const int n = ((u + 1) * a.per - 1) / a.quota - u * a.per / a.quota + 1;  // workgroups of this tile
+  if (n == 1) return;  // (stored whole)
   f32x4 v[2];
+  constexpr int kM = kGlu ? 2 : 1;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.planes) + i;
 #pragma unroll
-  for (int m = 0; m < (kGlu ? 2 : 1); ++m) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(a.planes + m * mn) + i;
-    const size_t step = mn / 4 * (kGlu ? 2 : 1);
-    v[m] = p[0];
-    for (int s = 1; s < a.splits; ++s) v[m] += p[s * step];
-  }
+  for (int m = 0; m < kM; ++m) v[m] = p[m * (mn / 4)];
+  for (int s = 1; s < n; ++s)
+#pragma unroll
+    for (int m = 0; m < kM; ++m) v[m] += p[(static_cast<size_t>(s) * kM + m) * (mn / 4)];
   if constexpr (!kGlu) {
     mx_store4(a.y, 4 * i, a.y_bf16, v[0]);
   } else {
@@ -389,25 +436,34 @@ __global__ __launch_bounds__(256) void mx_pieces_kernel(const float* __restrict_
   if (i < n) mx_store_pieces<3>(out, i, n, *reinterpret_cast<const f32x4*>(x + i));
 }
 
-template <int kP, bool kGlu, int kWM, int kWN, int kMB, int kNB>
+template <int kP, bool kGlu, int kWM, int kWN, int kWK, int kMB, int kNB>
 hipError_t start(const MxTileArgs& a, hipStream_t stream) {
-  const size_t blocks = static_cast<size_t>(a.row_tiles) * a.splits * a.tiles;
-  mx_tile_kernel<kP, kWM, kWN, kMB, kNB, kGlu><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+  const size_t blocks = (static_cast<size_t>(a.row_tiles) * a.tiles * a.per + a.quota - 1) / a.quota;
+  mx_tile_kernel<kP, kWM, kWN, kWK, kMB, kNB, kGlu><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <int kP, bool kGlu>
 hipError_t start_rows(int bm, const MxTileArgs& a, hipStream_t stream) {
-  // MXFP4 h takes blocks of 32 columns inside a wave
-  constexpr int kN = kP == 0 && kGlu ? 4 : 2;
-  switch (bm) {
-    case 32: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 1 : 2, kN>(a, stream);
-    case 64: return start<kP, kGlu, kN == 4 ? 2 : 1, kN == 4 ? 4 : 8, kN == 4 ? 2 : 4, kN>(a, stream);
-    case 128:
-      if constexpr (kP == 0 && !kGlu) return start<kP, kGlu, 1, 8, 8, 2>(a, stream);
-      return start<kP, kGlu, 2, 4, 4, 4>(a, stream);
-    default:
-      if constexpr (kP < 2) return start<kP, kGlu, 2, 4, 8, 4>(a, stream);  // (two or three planes: no such plan)
+  if constexpr (kP == 0) {
+    // MXFP4 h takes blocks of 32 columns inside a wave
+    constexpr int kM = kGlu ? 2 : 1, kN = kGlu ? 4 : 2;
+    switch (bm) {
+      case 32: return start<0, kGlu, kM, 8 / kM, 1, 2 / kM, kN>(a, stream);
+      case 64: return start<0, kGlu, kM, 8 / kM, 1, 4 / kM, kN>(a, stream);
+      case 128:
+        if constexpr (!kGlu) return start<0, false, 1, 8, 1, 8, 2>(a, stream);
+        return start<0, kGlu, 2, 4, 1, 4, 4>(a, stream);
+      default: return start<0, kGlu, 2, 4, 1, 8, 4>(a, stream);
+    }
+  } else {
+    switch (bm) {
+      case 32: return start<kP, kGlu, 1, 4, 2, 2, 4>(a, stream);
+      case 64: return start<kP, kGlu, 1, 4, 2, 4, 4>(a, stream);
+      case 128: return start<kP, kGlu, 2, 4, 1, 4, 4>(a, stream);
+      default:
+        if constexpr (kP == 1) return start<kP, kGlu, 2, 4, 1, 8, 4>(a, stream);  // (no plan with more planes)
+    }
   }
   return hipErrorInvalidValue;
 }
@@ -420,16 +476,19 @@ hipError_t start_glu(bool glu, int bm, const MxTileArgs& a, hipStream_t stream) 
 }  // namespace
 
 hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream) {
-  a.splits = p.splits;
-  a.sps = p.sps;
   a.tiles = p.tiles;
+  a.bm = p.bm;
+  a.cols = p.cols;
+  a.unit_steps = p.unit_steps;
+  a.per = p.per;
+  a.quota = p.quota;
   a.row_tiles = (a.M + p.bm - 1) / p.bm;
   // a run of n tasks as r row tiles of xb bytes by n / r column tiles of wb:
   // r xb + n / r wb is least at r = sqrt(n wb / xb)
-  const double n = std::max(1.0, static_cast<double>(a.row_tiles) * a.tiles * a.splits / kXcds);
+  const double n = std::max(1.0, static_cast<double>(a.row_tiles) * a.tiles / kXcds);
   const double xb = p.bm * (xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : (xk == kMxXf32h ? 4 : 6)));
   const double wb = p.cols * 0.53 * (glu ? 2 : 1);
-  a.band = std::min(a.row_tiles, std::max(1, static_cast<int>(std::sqrt(n * wb / xb) + 0.5)));
+  a.band = p.plane_bytes != 0 ? a.row_tiles : std::min(a.row_tiles, std::max(1, static_cast<int>(std::sqrt(n * wb / xb) + 0.5)));
   hipError_t e = hipErrorInvalidValue;
   switch (xk) {
     case kMxXf32: e = start_glu<3>(glu, p.bm, a, stream); break;
@@ -437,7 +496,7 @@ hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, 
     case kMxXbf16: e = start_glu<1>(glu, p.bm, a, stream); break;
     case kMxXfp4: e = start_glu<0>(glu, p.bm, a, stream); break;
   }
-  if (e != hipSuccess || p.splits == 1) return e;
+  if (e != hipSuccess || p.plane_bytes == 0) return e;
   const size_t n4 = static_cast<size_t>(a.M) * a.N / 4;
   const unsigned blocks = static_cast<unsigned>((n4 + 255) / 256);
   if (!glu) mx_planes_kernel<false, 1><<<blocks, 256, 0, stream>>>(a);
