@@ -150,6 +150,13 @@ __device__ __forceinline__ void mx_store_pieces(void* planes, size_t at, size_t 
   }
 }
 
+// h as the down product takes it: float32, or two or three bf16 planes.
+__device__ __forceinline__ void mx_store_hidden(void* h, size_t at, size_t plane, int pieces, const f32x4& v) {
+  if (pieces == 0) mx_store4(h, at, 0, v);
+  else if (pieces == 2) mx_store_pieces<2>(h, at, plane, v);
+  else mx_store_pieces<3>(h, at, plane, v);
+}
+
 // ---------------------------------------------------------------- products
 
 // What the activations of a product are.
@@ -169,11 +176,14 @@ struct MxArgs {
   void* y;                // [M][N], or the codes of h
   uint8_t* ys;            // MXFP4 h: its scales
   int y_bf16;
+  int h_pieces;           // other h: 0 float32, else bf16 planes of M * N
 };
 
 // Rows in blocks of 16, the whole K inside a workgroup (mx_stream.hip).
 hipError_t launch_mx_stream(MxX xk, bool glu, const MxArgs& a, hipStream_t stream);
 constexpr int kMxStreamRows = 16;
+// 16-column blocks of a workgroup (of each matrix)
+int mx_stream_blocks(MxX xk, bool glu, int N);
 
 // More rows, tiles of them in LDS (mx_tile.hip).  x: [M][K] bf16, or float32
 // rows as bf16 planes [pieces][M][K], or MXFP4 rows; y as in MxArgs, or with glu
@@ -187,7 +197,8 @@ struct MxTilePlan {
   int bm = 0, cols = 0, tiles = 0, unit_steps = 0, per = 0, quota = 0;
   size_t plane_bytes = 0;  // 0: every tile is one workgroup's
 };
-MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu);
+// (bm 0: the streamed form)
+MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu);
 hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream);
 // float32 values as three bf16 planes of n values
 hipError_t launch_mx_pieces(const float* x, size_t n, void* out, hipStream_t stream);

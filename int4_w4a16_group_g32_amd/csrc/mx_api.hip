@@ -2,6 +2,8 @@
 // launches.
 #include "mx.h"
 
+#include <cmath>
+
 namespace w4 {
 namespace {
 
@@ -78,16 +80,14 @@ MxArgs mx_args(const MxRows& r, int M, const w4a16_mx_t* w0, const w4a16_mx_t* w
 size_t pieces_bytes(MxX kind, size_t n) { return kind == kMxXf32 ? 6 * n : (kind == kMxXf32h ? 4 * n : 0); }
 
 struct MxGemmPlan {
-  bool tile = false;
   MxTilePlan t;
   size_t x_off = 0, planes_off = 0, bytes = 0;
 };
 MxGemmPlan plan_mx_gemm(int M, const w4a16_mx_t* w, MxX kind) {
   MxGemmPlan p;
   Carve c;
-  p.tile = M > kMxStreamRows;
-  if (p.tile) {
-    p.t = plan_mx_tile(M, w->rows, w->K, kind, false);
+  p.t = plan_mx_product(M, w->rows, w->K, kind, false);
+  if (p.t.bm != 0) {
     c.take(p.x_off, pieces_bytes(kind, static_cast<size_t>(M) * w->K));
     c.take(p.planes_off, p.t.plane_bytes);
   }
@@ -96,7 +96,6 @@ MxGemmPlan plan_mx_gemm(int M, const w4a16_mx_t* w, MxX kind) {
 }
 
 struct MxMlpPlan {
-  bool tile = false;
   MxX hkind = kMxXf32;
   MxTilePlan gu, dn;
   size_t x_off = 0, h_off = 0, hs_off = 0, planes_off = 0, bytes = 0;
@@ -105,29 +104,26 @@ MxMlpPlan plan_mx_mlp(int M, const w4a16_mx_t* gate, MxX kind) {
   MxMlpPlan p;
   Carve c;
   const size_t n = static_cast<size_t>(M) * gate->rows;
-  p.tile = M > kMxStreamRows;
   // h of bf16 rows keeps 16 bits, well under the rounding of its own operands
   p.hkind = kind == kMxXbf16 ? kMxXf32h : kind;
+  p.gu = plan_mx_product(M, gate->rows, gate->K, kind, true);
+  p.dn = plan_mx_product(M, gate->K, gate->rows, p.hkind, false);
   if (kind == kMxXfp4) {
     c.take(p.h_off, n / 2);
     c.take(p.hs_off, n / kMxBlock);
   } else {
-    c.take(p.h_off, p.tile ? pieces_bytes(p.hkind, n) : n * 4);
+    c.take(p.h_off, p.dn.bm != 0 ? pieces_bytes(p.hkind, n) : n * 4);
   }
-  if (p.tile) {
-    p.gu = plan_mx_tile(M, gate->rows, gate->K, kind, true);
-    p.dn = plan_mx_tile(M, gate->K, gate->rows, p.hkind, false);
-    c.take(p.x_off, pieces_bytes(kind, static_cast<size_t>(M) * gate->K));
-    c.take(p.planes_off, std::max(p.gu.plane_bytes, p.dn.plane_bytes));
-  }
+  c.take(p.x_off, p.gu.bm != 0 ? pieces_bytes(kind, static_cast<size_t>(M) * gate->K) : 0);
+  c.take(p.planes_off, std::max(p.gu.plane_bytes, p.dn.plane_bytes));
   p.bytes = std::max<size_t>(c.cursor, 256);
   return p;
 }
 
 // One product, streamed or in tiles; pieces: where float32 rows go as planes.
-w4a16_status_t mx_product(MxX kind, bool glu, bool tile, const MxTilePlan& t, MxArgs a, void* pieces, void* planes,
+w4a16_status_t mx_product(MxX kind, bool glu, const MxTilePlan& t, MxArgs a, void* pieces, void* planes,
                           hipStream_t stream) {
-  if (!tile) return launch_mx_stream(kind, glu, a, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
+  if (t.bm == 0) return launch_mx_stream(kind, glu, a, stream) == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
   MxTileArgs ta{};
   static_cast<MxArgs&>(ta) = a;
   ta.planes = static_cast<float*>(planes);
@@ -151,7 +147,7 @@ w4a16_status_t mx_gemm(const MxRows& r, int M, const w4a16_mx_t* w, void* y, w4a
   MxArgs a = mx_args(r, M, w, nullptr, y);
   a.y_bf16 = yt == W4A16_BF16;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
-  return mx_product(r.kind, false, p.tile, p.t, a, wsb + p.x_off, wsb + p.planes_off, stream);
+  return mx_product(r.kind, false, p.t, a, wsb + p.x_off, wsb + p.planes_off, stream);
 }
 
 w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, const w4a16_mx_t* up,
@@ -171,48 +167,76 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
   h.kind = p.hkind;
   MxArgs gu = mx_args(r, M, gate, up, wsb + p.h_off);
   gu.ys = wsb + p.hs_off;
-  st = mx_product(r.kind, true, p.tile, p.gu, gu, wsb + p.x_off, wsb + p.planes_off, stream);
+  gu.h_pieces = p.dn.bm == 0 ? 0 : (p.hkind == kMxXf32 ? 3 : 2);
+  st = mx_product(r.kind, true, p.gu, gu, wsb + p.x_off, wsb + p.planes_off, stream);
   if (st != W4A16_OK) return st;
   MxArgs dn = mx_args(h, M, down, nullptr, y);
   dn.y_bf16 = yt == W4A16_BF16;
-  return mx_product(h.kind, false, p.tile, p.dn, dn, nullptr, wsb + p.planes_off, stream);
+  return mx_product(h.kind, false, p.dn, dn, nullptr, wsb + p.planes_off, stream);
 }
 
 }  // namespace
 
-// Row tiles of the height that the rows fill.  Where the tiles are fewer than
-// the compute units, their units of K (pairs of steps) are dealt out evenly to
-// one workgroup each, wherever that cuts a tile, if what this saves is more than
-// the shared tiles' sums cost: a float32 plane for each workgroup of a tile,
-// written and read at about 4 TB/s, and a launch of about 4 us.
-MxTilePlan plan_mx_tile(int M, int N, int K, MxX xk, bool glu) {
+// Streamed or in tiles, and which.  Row tiles have the height that the rows
+// fill.  Where the tiles are fewer than the compute units, their units of K
+// (pairs of steps) are dealt out evenly to one workgroup each, wherever that
+// cuts a tile, if what this saves is more than the shared tiles' sums cost: a
+// float32 plane for each workgroup of a tile, written and read at about 4 TB/s,
+// and a launch of about 4 us.
+//
+// Up to 16 rows stream.  More rows stream in blocks of 16, each reading the
+// weights (from the L2, mostly) and all of x once a workgroup, while that is
+// shorter than the tiles' longer way: 37 float32 rows, 2304 -> 7168, 19.6 us
+// streamed and 24.8 in tiles, 7168 -> 4096 44 and 27; 64 bf16 rows, 2304 -> 7168,
+// 15.0 and 18.5, 7168 -> 4096 29 and 19.  The times below are fitted to such
+// measurements (17 to 128 rows, K 1056 to 7168, N 1040 to 18432), in us.
+MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu) {
   constexpr int kCus = 256;
   MxTilePlan p;
-  p.cols = glu ? 128 : 256;
+  if (M <= kMxStreamRows) return p;
+  const int mats = glu ? 2 : 1;
+  const double planes = xk == kMxXf32 ? 3 : (xk == kMxXf32h ? 2 : 1);
+  const bool wide = xk == kMxXf32 || xk == kMxXf32h;
+  p.cols = 256 / mats;
   p.tiles = (N + p.cols - 1) / p.cols;
   const int S = (K + kMxStep - 1) / kMxStep;
   p.bm = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
-  const bool wide = xk == kMxXf32 || xk == kMxXf32h;
   if (p.bm == 256 && (wide || static_cast<size_t>((M + 255) / 256) * p.tiles < kCus)) p.bm = 128;
   const size_t tiles = static_cast<size_t>((M + p.bm - 1) / p.bm) * p.tiles;
-  if (tiles < kCus && S > 2) {
-    p.unit_steps = 2;
-    p.per = (S + 1) / 2;
-    p.quota = std::max(2, static_cast<int>((tiles * p.per + kCus - 1) / kCus));
-    const int most = (p.per + p.quota - 2) / p.quota + 1;  // workgroups of a tile
-    // a unit: 256 k, at 5 (bf16 planes) or 12 TFLOP/s of a compute unit, and at
-    // least its 35 KB of codes and scales at its share of 6 TB/s
-    const double planes = xk == kMxXf32 ? 3 : (xk == kMxXf32h ? 2 : 1);
-    const double unit_us = std::max(2.0 * p.bm * 256 * 256 * planes / (xk == kMxXfp4 ? 12e6 : 5e6), 35e3 / 23e3);
-    const double bytes = 4.0 * M * N * (glu ? 2 : 1);
-    const double shared = std::min<double>(most, 1 + static_cast<double>(p.per) / p.quota);
-    if (p.quota < p.per && (p.per - p.quota) * unit_us > 4 + 2 * shared * bytes / 4e6) {
-      p.plane_bytes = static_cast<size_t>(most) * (glu ? 2 : 1) * M * N * 4;
-      return p;
-    }
-  }
   p.unit_steps = S;
   p.per = p.quota = 1;
+  int units = (S + 1) / 2 * static_cast<int>((tiles + kCus - 1) / kCus);  // of the busiest workgroup
+  double sums_us = 0;
+  if (tiles < kCus && S > 2) {
+    const int per = (S + 1) / 2, quota = std::max(2, static_cast<int>((tiles * per + kCus - 1) / kCus));
+    const int most = (per + quota - 2) / quota + 1;  // workgroups of a tile
+    // a unit: 256 k, at 5 (bf16 planes) or 12 TFLOP/s of a compute unit, and at
+    // least its 35 KB of codes and scales at its share of 6 TB/s
+    const double unit_us = std::max(2.0 * p.bm * 256 * 256 * planes / (xk == kMxXfp4 ? 12e6 : 5e6), 35e3 / 23e3);
+    const double bytes = 4.0 * M * N * mats;
+    const double us = 2 * std::min<double>(most, 1 + static_cast<double>(per) / quota) * bytes / 4e6;
+    if (quota < per && (per - quota) * unit_us > 4 + us) {
+      p.unit_steps = 2;
+      p.per = per;
+      p.quota = units = quota;
+      p.plane_bytes = static_cast<size_t>(most) * mats * M * N * 4;
+      sums_us = us;
+    }
+  }
+  if (M <= 128) {
+    const int nb = mx_stream_blocks(xk, glu, N), blocks = (M + 15) / 16;
+    const double wgs = std::ceil(N / (16.0 * nb)), xbytes = xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : 4);
+    const double slots = std::ceil(wgs * blocks / kCus), steps = std::ceil(S / 8.0);
+    const double traffic =
+        (wgs * 16 * K * xbytes / 11e6 + 0.53 * mats * N * K / 6e6) * (wide ? 1.4 : 1) + 0.8;
+    const bool fp4 = xk == kMxXfp4;
+    const double slot = 0.7 + steps * (fp4 ? 0.55 + 0.1 * nb * mats : 0.3 + 0.25 * nb * mats);
+    const double stream_us = 2.5 + std::max(slots * slot, blocks * traffic);
+    const int h = p.bm == 32 ? 0 : (p.bm == 64 ? 1 : 2);
+    constexpr double kBase[2][3] = {{8.5, 10.3, 12}, {6.8, 7.8, 7}}, kStage[2][3] = {{0.8, 1.5, 2.5}, {0.7, 0.8, 1}};
+    const double tile_us = kBase[fp4][h] + (xk == kMxXf32 ? 2.3 : 0) + units * planes * kStage[fp4][h] + sums_us;
+    if (stream_us < tile_us) return MxTilePlan();
+  }
   return p;
 }
 

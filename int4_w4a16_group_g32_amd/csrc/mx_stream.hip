@@ -296,7 +296,9 @@ __global__ __launch_bounds__(kW * 64) void mx_stream_kernel(const MxArgs a) {
       for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
     }
     if (lr >= nrows || n >= a.N) return;
-    mx_store4(a.y, static_cast<size_t>(r0 + lr) * a.N + n, a.y_bf16, v);
+    const size_t to = static_cast<size_t>(r0 + lr) * a.N + n;
+    if constexpr (kGlu) mx_store_hidden(a.y, to, static_cast<size_t>(a.M) * a.N, a.h_pieces, v);
+    else mx_store4(a.y, to, a.y_bf16, v);
   }
 }
 
@@ -331,22 +333,32 @@ int most_blocks(int N, int nb) { return ((N + 16 * nb - 1) / (16 * nb) + kCus - 
 // L2 of an XCD holds the lines that 32 compute units wait for, and beyond
 // about 80 KiB each it slows down (80 columns with two steps a wave in flight
 // 30.1 us, 32 columns with two, three, four 29.8, 33.6, 38.4).
+int blocks_of(MxX xk, bool glu, int N) {
+  if (glu && xk == kMxXfp4) {  // (h's blocks of 32 columns stay in a workgroup)
+    const int m2 = most_blocks(N, 2), m4 = most_blocks(N, 4), m6 = most_blocks(N, 6);
+    return m6 <= m4 && m6 <= m2 ? 6 : (m4 <= m2 ? 4 : 2);
+  }
+  const int m1 = most_blocks(N, 1), m2 = most_blocks(N, 2), m5 = most_blocks(N, 5);
+  return m5 <= m2 && m5 <= m1 ? 5 : (m2 <= m1 ? 2 : 1);
+}
+
 template <int kX, bool kGlu>
 hipError_t start_shape(const MxArgs& a, hipStream_t stream) {
-  if constexpr (kGlu && kX == kMxXfp4) {  // (h's blocks of 32 columns stay in a workgroup)
-    const int m2 = most_blocks(a.N, 2), m4 = most_blocks(a.N, 4), m6 = most_blocks(a.N, 6);
-    if (m6 <= m4 && m6 <= m2) return start_rows<kX, 6, true, 8, 1>(a, stream);
-    if (m4 <= m2) return start_rows<kX, 4, true, 8, 1>(a, stream);
+  const int nb = blocks_of(static_cast<MxX>(kX), kGlu, a.N);
+  if constexpr (kGlu && kX == kMxXfp4) {
+    if (nb == 6) return start_rows<kX, 6, true, 8, 1>(a, stream);
+    if (nb == 4) return start_rows<kX, 4, true, 8, 1>(a, stream);
     return start_rows<kX, 2, true, 4, 2>(a, stream);
   } else {
-    const int m1 = most_blocks(a.N, 1), m2 = most_blocks(a.N, 2), m5 = most_blocks(a.N, 5);
-    if (m5 <= m2 && m5 <= m1) return start_rows<kX, 5, kGlu, 8, kGlu ? 1 : 2>(a, stream);
-    if (m2 <= m1) return start_rows<kX, 2, kGlu, kGlu ? 4 : 8, 2>(a, stream);
+    if (nb == 5) return start_rows<kX, 5, kGlu, 8, kGlu ? 1 : 2>(a, stream);
+    if (nb == 2) return start_rows<kX, 2, kGlu, kGlu ? 4 : 8, 2>(a, stream);
     return start_rows<kX, 1, kGlu, 8, kGlu ? 2 : 4>(a, stream);
   }
 }
 
 }  // namespace
+
+int mx_stream_blocks(MxX xk, bool glu, int N) { return blocks_of(xk, glu, N); }
 
 hipError_t launch_mx_stream(MxX xk, bool glu, const MxArgs& a, hipStream_t stream) {
   switch (xk) {

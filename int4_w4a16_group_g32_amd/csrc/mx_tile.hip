@@ -34,6 +34,9 @@ __device__ __forceinline__ i32x8 widen(const u32x4& v) {
   return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
 }
 
+// The compiler moves no vector memory access across this.
+__device__ __forceinline__ void keep_loads() { __builtin_amdgcn_sched_barrier(0x38f); }
+
 // acc += W x, both MXFP4; kA and kB: the scales' bytes.
 template <int kA, int kB>
 __device__ __forceinline__ f32x4 mma_fp4(const u32x4& w, const u32x4& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
@@ -78,6 +81,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   constexpr int kSteps = kFp4 ? 2 : kWK;                  // steps of 128 k in a stage
   constexpr int kChunks = kFp4 ? 8 : 16 * kWK;            // 16-byte chunks of a row and stage
   constexpr int kUnits = (kBM * kChunks + kThreads - 1) / kThreads;  // chunks staged by a thread
+  constexpr bool kAhead = kMB < 8;                        // operands a part ahead
   constexpr int kParts = kFp4 ? 2 : 4;                    // of a stage's compute, between which they are staged
   constexpr int kScaleUnits = kFp4 ? (kBM * 8 + kThreads - 1) / kThreads : 0;  // scale bytes staged by a thread
   struct Buffer {
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   const size_t plane = static_cast<size_t>(a.M) * xrow;
   const char* xbase;
   const int G = a.K / kMxBlock;
-  __amdgpu_buffer_rsrc_t xsr;
+  __amdgpu_buffer_rsrc_t xr, xsr;
   const int chunk = t % kChunks, srow = t / kChunks;
   constexpr int kRowsAt = kThreads / kChunks;  // rows staged by one unit of all threads
   u32x4 held[kUnits];
@@ -127,7 +131,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     const int row = srow + i * kRowsAt;
     const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
     const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s + (kFp4 ? 0 : chunk / 16) < s_hi;
-    held[i] = load16(rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
+    held[i] = load16(kPlanes == 1 ? xr : rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
   };
   auto stage_store = [&](Buffer& buf, int i) {
     const int row = srow + i * kRowsAt;
@@ -204,6 +208,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     }
   }
   xbase = static_cast<const char*>(a.x) + r0 * xrow;
+  xr = rsrc(xbase, nrows * xrow);
   if constexpr (kFp4) xsr = rsrc(a.xs + static_cast<size_t>(r0) * G, static_cast<size_t>(nrows) * G);
 #pragma unroll
   for (int i = 0; i < kMB; ++i)
@@ -216,25 +221,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   // later ones in flight.
 #pragma unroll
   for (int part = 0; part < kParts; ++part) load_part(part, s_lo, 0);
+  keep_loads();
+  load_codes(ring[0], s_lo + wk);
+  keep_loads();
+  load_codes(ring[1], s_lo + kWK + wk);
+  keep_loads();
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) store_part(lds[0], part);
-  __builtin_amdgcn_sched_barrier(0);
-  if constexpr (kFp4) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load_part(h, s_lo + 2, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      load_codes(ring[h], s_lo + h);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  } else {
-    load_codes(ring[0], s_lo + wk);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) load_part(part, s_lo + 1 / kPlanes * kWK, 1 % kPlanes);
-    __builtin_amdgcn_sched_barrier(0);
-    load_codes(ring[1], s_lo + kWK + wk);
-    __builtin_amdgcn_sched_barrier(0);
+  for (int part = 0; part < kParts; ++part) {
+    store_part(lds[0], part);
+    load_part(part, s_lo + (kFp4 ? 2 : 1 / kPlanes * kWK), 1 % kPlanes);
+    keep_loads();
   }
 
   if constexpr (kFp4) {
@@ -271,36 +267,51 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     }
   } else {
     int q = 0;
-    // (s_next, p_next): two stages on
-    auto stage = [&](Codes& c, bool on, int s_next, int p_next) {
+    // Part j takes codes 8 j .. 8 j + 7 of every lane.  While its products run,
+    // the codes of the next part, or of the next stage's first, are expanded and
+    // its rows read: w and xf hold one part more than is in use (but in the
+    // tallest tile, whose registers are full).
+    bf16x8 w[kAhead ? 2 : 1][kNB], xf[kAhead ? 2 : 1][kMB];
+    auto expand = [&](const Codes& c, int part, bf16x8 o[kNB]) {
+#pragma unroll
+      for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int j = 0; j < kNbM; ++j)
+          o[m * kNbM + j] = mx_bf16(c.w[m][j][part], scale_byte(j, kNbM == 4 ? c.s[m] : c.s[m] >> (8 * c0)));
+    };
+    // c: this stage's codes, cn: the next one's; (s_next, p_next): two stages on
+    auto stage = [&](const Codes& c, const Codes& cn, int s_next, int p_next) {
       __syncthreads();
       const Buffer& cur = lds[q & 1];
       Buffer& nxt = lds[(q + 1) & 1];
       ++q;
-      float f[kMats][kNbM];
+      auto frags = [&](int part) {
 #pragma unroll
-      for (int m = 0; m < kMats; ++m)
-#pragma unroll
-        for (int j = 0; j < kNbM; ++j) f[m][j] = scale_byte(j, kNbM == 4 ? c.s[m] : c.s[m] >> (8 * c0));
+        for (int i = 0; i < kMB; ++i)
+          xf[kAhead ? part & 1 : 0][i] = __builtin_bit_cast(bf16x8, xfrag(cur, i, 16 * wk + 4 * kb + part));
+      };
+      if (kAhead) frags(0);
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
         store_part(nxt, part);
         load_part(part, s_next, p_next);
-        __builtin_amdgcn_sched_barrier(0);
-        if (kWK > 1 && !on) continue;
-        bf16x8 w[kNB];
-#pragma unroll
-        for (int m = 0; m < kMats; ++m)
-#pragma unroll
-          for (int j = 0; j < kNbM; ++j) w[m * kNbM + j] = mx_bf16(c.w[m][j][part], f[m][j]);
-#pragma unroll
-        for (int i = 0; i < kMB; ++i) {
-          const bf16x8 xf = __builtin_bit_cast(bf16x8, xfrag(cur, i, 16 * wk + 4 * kb + part));
-#pragma unroll
-          for (int j = 0; j < kNB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], xf, acc[i][j], 0, 0, 0);
+        keep_loads();
+        if constexpr (kAhead) {
+          if (part < 3) frags(part + 1);
+          expand(part < 3 ? c : cn, (part + 1) & 3, w[(part + 1) & 1]);
+        } else {
+          frags(part);
+          expand(c, part, w[0]);
         }
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+          for (int j = 0; j < kNB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[kAhead ? part & 1 : 0][j], xf[kAhead ? part & 1 : 0][i],
+                                                              acc[i][j], 0, 0, 0);
       }
     };
+    if (kAhead) expand(ring[0], 0, w[0]);
     for (int s = s_lo; s < s_hi; s += 2 * kWK) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -308,9 +319,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
         if (sh >= s_hi) break;
 #pragma unroll 1
         for (int p = 0; p < kPlanes; ++p)
-          stage(ring[h], sh + wk < s_hi, p + 2 < kPlanes ? sh : sh + (p + 2) / kPlanes * kWK, (p + 2) % kPlanes);
+          stage(ring[h], p + 1 < kPlanes ? ring[h] : ring[1 - h],
+                p + 2 < kPlanes ? sh : sh + (p + 2) / kPlanes * kWK, (p + 2) % kPlanes);
         load_codes(ring[h], sh + 2 * kWK + wk);
-        __builtin_amdgcn_sched_barrier(0);
+        keep_loads();
       }
     }
   }
@@ -375,7 +387,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
 #pragma unroll
         for (int j = 0; j < kNbM; ++j) {
           const int n = n0 + 16 * j + 4 * kb;
-          if (row_ok && n < a.N) mx_store_pieces<kP == 3 ? 3 : 2>(a.y, rowN + n, static_cast<size_t>(a.M) * a.N, h[j]);
+          if (row_ok && n < a.N) mx_store_hidden(a.y, rowN + n, static_cast<size_t>(a.M) * a.N, a.h_pieces, h[j]);
         }
       }
     }
@@ -387,7 +399,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
 
 // The sums of tiles that several workgroups share, in their order along K, to y
 // or to h and its form for the down product.
-template <bool kGlu, int kOut>  // kOut: pieces of h (2, 3), 0: MXFP4 h; -: y
+template <bool kGlu, bool kFp4>  // kFp4: h as MXFP4
 __global__ __launch_bounds__(256) void mx_planes_kernel(const MxTileArgs a) {
   const size_t mn = static_cast<size_t>(a.M) * a.N;
   const size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x;  // four columns of a row
@@ -410,7 +422,7 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(const MxTileArgs a) {
     f32x4 h;
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = silu(v[0][e]) * v[1][e];
-    if constexpr (kOut == 0) {
+    if constexpr (kFp4) {
       // eight threads hold a block of 32 columns
       uint32_t mx = 0;
 #pragma unroll
@@ -425,7 +437,7 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(const MxTileArgs a) {
       static_cast<uint16_t*>(a.y)[i] = static_cast<uint16_t>(mx_codes8(q));
       if ((i & 7) == 0) a.ys[i >> 3] = static_cast<uint8_t>(byte);
     } else {
-      mx_store_pieces<kOut>(a.y, 4 * i, mn, h);
+      mx_store_hidden(a.y, 4 * i, mn, a.h_pieces, h);
     }
   }
 }
@@ -499,10 +511,9 @@ hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, 
   if (e != hipSuccess || p.plane_bytes == 0) return e;
   const size_t n4 = static_cast<size_t>(a.M) * a.N / 4;
   const unsigned blocks = static_cast<unsigned>((n4 + 255) / 256);
-  if (!glu) mx_planes_kernel<false, 1><<<blocks, 256, 0, stream>>>(a);
-  else if (xk == kMxXfp4) mx_planes_kernel<true, 0><<<blocks, 256, 0, stream>>>(a);
-  else if (xk == kMxXf32) mx_planes_kernel<true, 3><<<blocks, 256, 0, stream>>>(a);
-  else mx_planes_kernel<true, 2><<<blocks, 256, 0, stream>>>(a);
+  if (!glu) mx_planes_kernel<false, false><<<blocks, 256, 0, stream>>>(a);
+  else if (xk == kMxXfp4) mx_planes_kernel<true, true><<<blocks, 256, 0, stream>>>(a);
+  else mx_planes_kernel<true, false><<<blocks, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
