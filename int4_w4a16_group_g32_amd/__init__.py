@@ -266,14 +266,30 @@ def _on_device(**tensors):
                 raise ValueError(f"{name} is on device {d}, the current device is {dev}")
 
 
-def _ready(t, name: str, dtype, shape):
-    """`_need` and `_on_device` of one tensor: the common case in one line (0.4 us for 1.1), the rest to report."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous():
-        d = t.get_device()
-        if d >= 0 and d == _current_device():
-            return
-    _need(t, name, dtype, shape)
-    _on_device(**{name: t})
+# The MXFP4 calls and block_norm ask of each tensor what `_need` and `_on_device` ask, in one expression
+# (0.3 us for 1.1: a few-row call is bound by the host); those two then say what is wrong.
+_F32, _BF16, _U8 = torch.float32, torch.bfloat16, torch.uint8
+
+
+def _fits(t, dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
+def _ready(t, name: str, dtype, shape, dev: int):
+    """Refuses a tensor of another type, shape, layout or device than the current one, `dev`."""
+    if not (isinstance(t, torch.Tensor) and _fits(t, dtype, shape, dev)):
+        _need(t, name, dtype, shape)
+        _on_device(**{name: t})
+
+
+def _device_of(t) -> int:
+    """The current device, of which `t` must be."""
+    d = t.get_device()
+    return d if d >= 0 and d == _current_device() else -2  # (no tensor is of device -2)
+
+
+def _stream_of(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _need_x(x: torch.Tensor, K: int):
@@ -313,17 +329,18 @@ class MxMatrix:
 
     def check(self, name: str):
         """The tensors' dtypes, sizes and devices for the shape."""
+        self._ready(name, _device_of(self.codes) if isinstance(self.codes, torch.Tensor) else -2)
+
+    def _ready(self, name: str, dev: int):
         c, s, rows, K = self.codes, self.scales, self.rows, self.K
         if self.layout == MX_TILED:
             tiles = -(-rows // 64) * -(-K // 128)
             nc, ns = tiles * 4096, tiles * 256
         else:
             nc, ns = rows * (K // 2), rows * (K // 32)
-        if (c.dtype == torch.uint8 == s.dtype and c.numel() == nc and s.numel() == ns and c.is_contiguous()
-                and s.is_contiguous()):
-            d = c.get_device()
-            if 0 <= d == s.get_device() and d == _current_device():
-                return
+        if (c.dtype is _U8 and s.dtype is _U8 and c.numel() == nc and s.numel() == ns and c.is_contiguous()
+                and s.is_contiguous() and c.get_device() == dev and s.get_device() == dev):
+            return
         _need(c, f"{name}.codes", torch.uint8)
         _need(s, f"{name}.scales", torch.uint8)
         if (c.numel(), s.numel()) != (nc, ns):
@@ -619,9 +636,9 @@ def mx_empty(rows: int, K: int, layout: int = MX_ROWS, device="cuda") -> MxMatri
     return MxMatrix(codes, scales, rows, K, layout)
 
 
-def _need_mx_out(out: MxMatrix, name: str, rows: int, K: int):
-    out.check(name)
-    if (out.rows, out.K, out.layout) != (rows, K, MX_ROWS):
+def _need_mx_out(out: MxMatrix, name: str, rows: int, K: int, dev: int):
+    out._ready(name, dev)
+    if out.rows != rows or out.K != K or out.layout != MX_ROWS:
         raise ValueError(f"{name} must be {rows} rows of {K} in ROWS, got {out.rows} of {out.K} in layout {out.layout}")
 
 
@@ -630,12 +647,15 @@ def mx_quantize(x: torch.Tensor, out: MxMatrix, stream=None):
     xt = _dtype_code(x)
     if x.dim() != 2:
         raise ValueError(f"x must be [rows][K], got {tuple(x.shape)}")
-    rows, K = x.shape
-    _ready(x, "x", x.dtype, (rows, K))
-    _need_mx_out(out, "out", rows, K)
-    _check(load_library().w4a16_mx_quantize(x.data_ptr(), xt, rows, K, out.codes.data_ptr(), out.codes.numel(),
-                                            out.scales.data_ptr(), out.scales.numel(), _stream(stream)),
-           "w4a16_mx_quantize")
+    rows, K = shape = x.shape
+    dev = _device_of(x)
+    _ready(x, "x", x.dtype, shape, dev)
+    _need_mx_out(out, "out", rows, K, dev)
+    c, s = out.codes, out.scales
+    st = load_library().w4a16_mx_quantize(x.data_ptr(), xt, rows, K, c.data_ptr(), c.numel(), s.data_ptr(), s.numel(),
+                                          _stream_of(stream, dev))
+    if st != OK:
+        raise W4A16Error(st, "w4a16_mx_quantize")
 
 
 def mx_quantize_weight(w: torch.Tensor, out: MxMatrix, stream=None):
@@ -643,9 +663,9 @@ def mx_quantize_weight(w: torch.Tensor, out: MxMatrix, stream=None):
     wt = _dtype_code(w)
     if w.dim() != 2:
         raise ValueError(f"w must be [K][N], got {tuple(w.shape)}")
-    _need(w, "w", w.dtype)
-    _need_mx_out(out, "out", w.shape[1], w.shape[0])
-    _on_device(w=w)
+    dev = _device_of(w)
+    _ready(w, "w", w.dtype, w.shape, dev)
+    _need_mx_out(out, "out", w.shape[1], w.shape[0], dev)
     _check(load_library().w4a16_mx_quantize_weight(_ptr(w), wt, w.shape[0], w.shape[1], _ptr(out.codes),
                                                    _nbytes(out.codes), _ptr(out.scales), _nbytes(out.scales),
                                                    _stream(stream)), "w4a16_mx_quantize_weight")
@@ -666,11 +686,14 @@ def mx_prepack(src: MxMatrix, dst: MxMatrix, stream=None) -> MxMatrix:
 
 def mx_dequantize(m: MxMatrix, out: torch.Tensor, stream=None):
     """The values of m [rows][K], either layout, as float32 or bfloat16."""
-    m.check("m")
     ot = _dtype_code(out)
-    _ready(out, "out", out.dtype, (m.rows, m.K))
-    _check(load_library().w4a16_mx_dequantize(ctypes.byref(m.desc()), out.data_ptr(), ot, _nbytes(out),
-                                              _stream(stream)), "w4a16_mx_dequantize")
+    dev = _device_of(out)
+    m._ready("m", dev)
+    _ready(out, "out", out.dtype, (m.rows, m.K), dev)
+    st = load_library().w4a16_mx_dequantize(ctypes.byref(m.desc()), out.data_ptr(), ot, _nbytes(out),
+                                            _stream_of(stream, dev))
+    if st != OK:
+        raise W4A16Error(st, "w4a16_mx_dequantize")
 
 
 def mx_quantize_to_weight(w: torch.Tensor, stream=None) -> MxMatrix:
@@ -689,38 +712,40 @@ def mx_gemm_workspace_bytes(M: int, xt: int, w: MxMatrix) -> int:
     return lib.w4a16_mx_gemm_workspace_bytes(M, xt, ctypes.byref(w.desc()))
 
 
-def _mx_x(x, K: int):
+def _mx_x(x, K: int, dev: int):
     """The type code and rows of activations [M][K]."""
     xt = _dtype_code(x)
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"activations must be [M][{K}], got {tuple(x.shape)}")
-    _ready(x, "x", x.dtype, x.shape)
+    _ready(x, "x", x.dtype, x.shape, dev)
     return xt, x.shape[0]
 
 
-def _mx_io(y, shape, ws) -> int:
-    """y float32 or bfloat16 of this shape, ws bytes; returns y's type code."""
+def _mx_io(y, M: int, N: int, ws, dev: int) -> int:
+    """y float32 or bfloat16 [M][N], ws bytes; returns y's type code."""
     yt = _dtype_code(y)
-    _ready(y, "y", y.dtype, shape)
-    _ready(ws, "ws", torch.uint8, ws.shape)
+    _ready(y, "y", y.dtype, (M, N), dev)
+    _ready(ws, "ws", _U8, ws.shape, dev)
     return yt
 
 
 def mx_gemm(x, w: MxMatrix, y: torch.Tensor, ws: torch.Tensor, stream=None):
     """y = x W^T over a TILED MXFP4 weight; x a float32 or bfloat16 tensor [M][K], or an MxMatrix (ROWS)."""
-    w.check("w")
+    dev = _device_of(y)
+    w._ready("w", dev)
     lib, d = load_library(), ctypes.byref(w.desc())
     if isinstance(x, MxMatrix):
-        x.check("x")
-        M = x.rows
-        yt = _mx_io(y, (M, w.rows), ws)
-        _check(lib.w4a16_mx_gemm_a4(ctypes.byref(x.desc()), d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
-                                    _stream(stream)), "w4a16_mx_gemm_a4")
+        x._ready("x", dev)
+        yt = _mx_io(y, x.rows, w.rows, ws, dev)
+        st = lib.w4a16_mx_gemm_a4(ctypes.byref(x.desc()), d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
+                                  _stream_of(stream, dev))
     else:
-        xt, M = _mx_x(x, w.K)
-        yt = _mx_io(y, (M, w.rows), ws)
-        _check(lib.w4a16_mx_gemm(x.data_ptr(), xt, M, d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(), _stream(stream)),
-               "w4a16_mx_gemm")
+        xt, M = _mx_x(x, w.K, dev)
+        yt = _mx_io(y, M, w.rows, ws, dev)
+        st = lib.w4a16_mx_gemm(x.data_ptr(), xt, M, d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
+                               _stream_of(stream, dev))
+    if st != OK:
+        raise W4A16Error(st, "w4a16_mx_gemm")
 
 
 def mx_swiglu_mlp_workspace_bytes(M: int, xt: int, gate: MxMatrix, up: MxMatrix, down: MxMatrix) -> int:
@@ -733,18 +758,21 @@ def mx_swiglu_mlp_workspace_bytes(M: int, xt: int, gate: MxMatrix, up: MxMatrix,
 
 def mx_swiglu_mlp(x, gate: MxMatrix, up: MxMatrix, down: MxMatrix, y: torch.Tensor, ws: torch.Tensor, stream=None):
     """The SwiGLU MLP over TILED MXFP4 weights; x as in mx_gemm (with an MxMatrix, h is MXFP4 too)."""
-    gate.check("gate"), up.check("up"), down.check("down")
+    dev = _device_of(y)
+    gate._ready("gate", dev), up._ready("up", dev), down._ready("down", dev)
     lib, d = load_library(), [ctypes.byref(w.desc()) for w in (gate, up, down)]
     if isinstance(x, MxMatrix):
-        x.check("x")
-        yt = _mx_io(y, (x.rows, down.rows), ws)
-        _check(lib.w4a16_mx_swiglu_mlp_a4(ctypes.byref(x.desc()), *d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
-                                          _stream(stream)), "w4a16_mx_swiglu_mlp_a4")
+        x._ready("x", dev)
+        yt = _mx_io(y, x.rows, down.rows, ws, dev)
+        st = lib.w4a16_mx_swiglu_mlp_a4(ctypes.byref(x.desc()), *d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
+                                        _stream_of(stream, dev))
     else:
-        xt, M = _mx_x(x, gate.K)
-        yt = _mx_io(y, (M, down.rows), ws)
-        _check(lib.w4a16_mx_swiglu_mlp(x.data_ptr(), xt, M, *d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
-                                       _stream(stream)), "w4a16_mx_swiglu_mlp")
+        xt, M = _mx_x(x, gate.K, dev)
+        yt = _mx_io(y, M, down.rows, ws, dev)
+        st = lib.w4a16_mx_swiglu_mlp(x.data_ptr(), xt, M, *d, y.data_ptr(), yt, ws.data_ptr(), ws.numel(),
+                                     _stream_of(stream, dev))
+    if st != OK:
+        raise W4A16Error(st, "w4a16_mx_swiglu_mlp")
 
 
 # ---------------------------------------------------------------- norms
@@ -759,37 +787,45 @@ def block_norm(y: torch.Tensor, r: torch.Tensor | None = None, r_out: torch.Tens
     if y.dim() != 2:
         raise ValueError(f"y must be [M][H], got {tuple(y.shape)}")
     M, H = shape = y.shape
-    _ready(y, "y", y.dtype, shape)
+    dev = _device_of(y)
+    _ready(y, "y", y.dtype, shape, dev)
     residual = r if r is not None else r_out
-    rt, rd = yt, y.dtype
+    rt, rp, op = yt, None, None
     if residual is not None:
         rt, rd = _dtype_code(residual), residual.dtype
         if r is not None:
-            _ready(r, "r", rd, shape)
+            _ready(r, "r", rd, shape, dev)
+            rp = r.data_ptr()
         if r_out is not None:
-            _ready(r_out, "r_out", rd, shape)
-    wt = wd = None
-    gate_rows = 1
-    for t, name in ((pre_w, "pre_w"), (post_w, "post_w"), (gate, "gate")):
-        if t is None:
-            continue
-        if wt is None:
-            wt, wd = _dtype_code(t), t.dtype
-        if t is gate and t.dim() == 2:
-            gate_rows = M
-            _ready(t, name, wd, shape)
-        else:
-            _ready(t, name, wd, (H,))
-    nt, n_ptr, codes, scales = F32, None, None, None
+            _ready(r_out, "r_out", rd, shape, dev)
+            op = r_out.data_ptr()
+    first = pre_w if pre_w is not None else post_w if post_w is not None else gate
+    wt, pre, post, gp, gate_rows, row = yt, None, None, None, 1, (H,)
+    if first is not None:
+        wt, wd = _dtype_code(first), first.dtype
+        if pre_w is not None:
+            _ready(pre_w, "pre_w", wd, row, dev)
+            pre = pre_w.data_ptr()
+        if post_w is not None:
+            _ready(post_w, "post_w", wd, row, dev)
+            post = post_w.data_ptr()
+        if gate is not None:
+            if gate.dim() == 2:
+                gate_rows = M
+            _ready(gate, "gate", wd, shape if gate.dim() == 2 else row, dev)
+            gp = gate.data_ptr()
+    nt, np, codes, scales = F32, None, None, None
     if isinstance(n, MxMatrix):
-        _need_mx_out(n, "n", M, H)
+        _need_mx_out(n, "n", M, H, dev)
         codes, scales = n.codes.data_ptr(), n.scales.data_ptr()
     elif n is not None:
-        nt, n_ptr = _dtype_code(n), n.data_ptr()
-        _ready(n, "n", n.dtype, shape)
-    d = NormDesc(y.data_ptr(), _ptr(r), _ptr(r_out), _ptr(post_w), _ptr(pre_w), _ptr(gate), gate_rows, n_ptr, codes,
-                 scales, yt, rt, yt if wt is None else wt, nt, alpha, eps)
-    _check(load_library().w4a16_block_norm(ctypes.byref(d), M, H, _stream(stream)), "w4a16_block_norm")
+        nt = _dtype_code(n)
+        _ready(n, "n", n.dtype, shape, dev)
+        np = n.data_ptr()
+    d = NormDesc(y.data_ptr(), rp, op, post, pre, gp, gate_rows, np, codes, scales, yt, rt, wt, nt, alpha, eps)
+    st = load_library().w4a16_block_norm(ctypes.byref(d), M, H, _stream_of(stream, dev))
+    if st != OK:
+        raise W4A16Error(st, "w4a16_block_norm")
 
 
 # ---------------------------------------------------------------- helpers

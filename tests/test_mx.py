@@ -203,6 +203,7 @@ def _dev(t, cls=_OnDevice):
 def no_calls(monkeypatch):
     """The current device is 0, and no entry point may be reached."""
     monkeypatch.setattr(L, "_current_device", lambda: 0)
+    monkeypatch.setattr(L, "_stream_of", lambda *a: pytest.fail("the library was reached"))
     monkeypatch.setattr(L, "_stream", lambda s: pytest.fail("the library was reached"))
 
 
