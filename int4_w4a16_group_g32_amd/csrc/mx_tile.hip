@@ -78,15 +78,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   constexpr int kNbM = kNB / kMats;                       // blocks of each matrix
   constexpr int kBM = 16 * kMB * kWM, kCols = 16 * kNbM;  // rows of the tile; columns of a wave
   constexpr int kBN = kCols * kWN;
-  constexpr int kSteps = kFp4 ? 2 : kWK;                  // steps of 128 k in a stage
-  constexpr int kChunks = kFp4 ? 8 : 16 * kWK;            // 16-byte chunks of a row and stage
+  constexpr int kSteps = kFp4 ? 4 : kWK;                  // steps of 128 k in a stage
+  constexpr int kChunks = (kFp4 ? 4 : 16) * kSteps;       // 16-byte chunks of a row and stage
   constexpr int kUnits = (kBM * kChunks + kThreads - 1) / kThreads;  // chunks staged by a thread
-  constexpr bool kAhead = kMB < 8;                        // operands a part ahead
-  constexpr int kParts = kFp4 ? 2 : 4;                    // of a stage's compute, between which they are staged
-  constexpr int kScaleUnits = kFp4 ? (kBM * 8 + kThreads - 1) / kThreads : 0;  // scale bytes staged by a thread
+  constexpr int kParts = kFp4 ? kSteps : 4;                    // of a stage's compute, between which they are staged
+  constexpr int kQuads = (kBM + 63) / 64;                 // groups of four 16-row blocks
   struct Buffer {
     u32x4 x[kBM * kChunks];
-    uint32_t s[kFp4 ? 2 * ((kBM + 63) / 64) * 64 : 1];  // per step: scales of four 16-row blocks
+    uint32_t s[kFp4 ? kSteps * kQuads * 64 : 1];  // per step: scales of four 16-row blocks
   };
   __shared__ Buffer lds[2];
 
@@ -124,52 +123,73 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   __amdgpu_buffer_rsrc_t xr, xsr;
   const int chunk = t % kChunks, srow = t / kChunks;
   constexpr int kRowsAt = kThreads / kChunks;  // rows staged by one unit of all threads
-  u32x4 held[kUnits];
-  uint32_t held_s[kScaleUnits > 0 ? kScaleUnits : 1];
+  struct Held {
+    u32x4 x[kUnits];
+    uint32_t s[4];  // (MXFP4: scales of one step of rows 16 apart)
+  };
   // a thread's chunk of its unit i, from step s
-  auto stage_load = [&](int i, int s, int p) {
+  auto stage_load = [&](Held& h, int i, int s, int p) {
     const int row = srow + i * kRowsAt;
     const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
     const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s + (kFp4 ? 0 : chunk / 16) < s_hi;
-    held[i] = load16(kPlanes == 1 ? xr : rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
+    h.x[i] = load16(kPlanes == 1 ? xr : rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
   };
-  auto stage_store = [&](Buffer& buf, int i) {
+  auto stage_store = [&](Buffer& buf, const Held& h, int i) {
     const int row = srow + i * kRowsAt;
-    if (kUnits * kThreads == kBM * kChunks || row < kBM) buf.x[row * kChunks + (chunk ^ (row % kChunks))] = held[i];
+    if (kUnits * kThreads == kBM * kChunks || row < kBM) buf.x[row * kChunks + (chunk ^ (row % kChunks))] = h.x[i];
   };
-  // scale bytes: byte g of row r, eight of a row (two steps)
-  auto scale_load = [&](int i, int s) {
-    const int u = t + i * kThreads, row = u / 8, g = 4 * s + u % 8;
-    held_s[i] = __builtin_amdgcn_raw_buffer_load_b8(xsr, row < nrows && g < G ? row * G + g : kOob, 0, 0);
+  // Scales: thread t < 16 kSteps kQuads takes one step (t / (16 kQuads)) of the rows
+  // 64 g + t % 16 + 16 q, q = 0 .. 3, four bytes each, and leaves dword l of
+  // group g with what lane l needs: its k block's byte of each of the four.
+  const int sg = t / 16 % kQuads, ss = t / (16 * kQuads);
+  const bool stages_scales = kFp4 && t < 16 * kSteps * kQuads;
+  auto scale_load = [&](Held& h, int s) {
+    if (!stages_scales) return;
+    const int g = 4 * (s + ss);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 64 * sg + t % 16 + 16 * q, at = row * G + g;
+      const bool on = row < nrows;
+      if (G % 4 == 0) {
+        h.s[q] = __builtin_amdgcn_raw_buffer_load_b32(xsr, on && g < G ? at : kOob, 0, 0);
+      } else {
+        h.s[q] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h.s[q] |= static_cast<uint32_t>(static_cast<uint8_t>(
+                        __builtin_amdgcn_raw_buffer_load_b8(xsr, on && g + e < G ? at + e : kOob, 0, 0)))
+                    << (8 * e);
+      }
+    }
   };
-  auto scale_store = [&](Buffer& buf, int i) {
-    const int u = t + i * kThreads, row = u / 8, g = u % 8;
-    if (row < kBM)
-      reinterpret_cast<uint8_t*>(buf.s)[((g / 4 * ((kBM + 63) / 64) + row / 64) * 64 + 16 * (g % 4) + row % 16) * 4 +
-                                        row / 16 % 4] = static_cast<uint8_t>(held_s[i]);
+  auto scale_store = [&](Buffer& buf, const Held& h) {
+    if (!stages_scales) return;
+    const uint32_t a01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x05010400), b01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x07030602);
+    const uint32_t a23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x05010400), b23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x07030602);
+    uint32_t* o = buf.s + (ss * kQuads + sg) * 64 + t % 16;
+    o[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100);
+    o[16] = __builtin_amdgcn_perm(a23, a01, 0x07060302);
+    o[32] = __builtin_amdgcn_perm(b23, b01, 0x05040100);
+    o[48] = __builtin_amdgcn_perm(b23, b01, 0x07060302);
   };
 
   f32x4 acc[kMB][kNB];
   // unit i is staged in part i * kParts / kUnits of the compute
   auto part_of = [](int i) { return i * kParts / kUnits; };
-  auto load_part = [&](int part, int s, int p) {
+  auto load_part = [&](Held& h, int part, int s, int p) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-      if (part_of(i) == part) stage_load(i, s, p);
+      if (part_of(i) == part) stage_load(h, i, s, p);
     if constexpr (kFp4) {
-      if (part == 0)
-#pragma unroll
-        for (int i = 0; i < kScaleUnits; ++i) scale_load(i, s);
+      if (part == 0) scale_load(h, s);
     }
   };
-  auto store_part = [&](Buffer& buf, int part) {
+  auto store_part = [&](Buffer& buf, const Held& h, int part) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-      if (part_of(i) == part) stage_store(buf, i);
+      if (part_of(i) == part) stage_store(buf, h, i);
     if constexpr (kFp4) {
-      if (part == 0)
-#pragma unroll
-        for (int i = 0; i < kScaleUnits; ++i) scale_store(buf, i);
+      if (part == 0) scale_store(buf, h);
     }
   };
   auto xfrag = [&](const Buffer& buf, int i, int c) {
@@ -217,33 +237,43 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   if (again) __syncthreads();  // (the last segment's LDS is read)
 
   // Loads are issued in the order of their use, here as in the loops (the
-  // barriers keep the compiler from moving them): its waits then leave all
-  // later ones in flight.
+  // barriers keep the compiler from moving them): its waits, which have to hold
+  // for the first stage as for the others, then leave all later ones in flight.
+  Held held, first;
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) load_part(part, s_lo, 0);
-  keep_loads();
-  load_codes(ring[0], s_lo + wk);
-  keep_loads();
-  load_codes(ring[1], s_lo + kWK + wk);
-  keep_loads();
+  for (int part = 0; part < kParts; ++part) load_part(first, part, s_lo, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (kFp4) {
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) {
-    store_part(lds[0], part);
-    load_part(part, s_lo + (kFp4 ? 2 : 1 / kPlanes * kWK), 1 % kPlanes);
-    keep_loads();
+    for (int h = 0; h < kSteps; ++h) {
+      load_part(held, h, s_lo + kSteps, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (h >= kSteps - 2) load_codes(ring[h & 1], s_lo + h - (kSteps - 2));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    load_codes(ring[0], s_lo + wk);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) load_part(held, part, s_lo + 1 / kPlanes * kWK, 1 % kPlanes);
+    __builtin_amdgcn_sched_barrier(0);
+    load_codes(ring[1], s_lo + kWK + wk);
+    __builtin_amdgcn_sched_barrier(0);
   }
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) store_part(lds[0], first, part);
 
   if constexpr (kFp4) {
-    for (int s = s_lo, q = 0; s < s_hi; s += 2, ++q) {
+    for (int s = s_lo, q = 0; s < s_hi; s += kSteps, ++q) {
       __syncthreads();
       const Buffer& cur = lds[q & 1];
       Buffer& nxt = lds[(q + 1) & 1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        store_part(nxt, h);
-        load_part(h, s + 4, 0);
+      for (int h = 0; h < kSteps; ++h) {
+        store_part(nxt, held, h);
+        load_part(held, h, s + 2 * kSteps, 0);
         __builtin_amdgcn_sched_barrier(0);
-        Codes& c = ring[h];
+        Codes& c = ring[h & 1];
         if (s + h < s_hi) {
           uint32_t ws[kMats];
 #pragma unroll
@@ -251,7 +281,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
 #pragma unroll
           for (int i = 0; i < kMB; ++i) {
             const int rb = wm * kMB + i;  // 16-row block: byte rb % 4 of its dword
-            uint32_t xs = cur.s[(h * ((kBM + 63) / 64) + rb / 4) * 64 + lane];
+            uint32_t xs = cur.s[(h * kQuads + rb / 4) * 64 + lane];
             if (kMB % 4 != 0) xs >>= 8 * (rb % 4 - i % 4);
             const u32x4 xf = xfrag(cur, i, 4 * h + kb);
 #pragma unroll
@@ -269,9 +299,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     int q = 0;
     // Part j takes codes 8 j .. 8 j + 7 of every lane.  While its products run,
     // the codes of the next part, or of the next stage's first, are expanded and
-    // its rows read: w and xf hold one part more than is in use (but in the
-    // tallest tile, whose registers are full).
-    bf16x8 w[kAhead ? 2 : 1][kNB], xf[kAhead ? 2 : 1][kMB];
+    // its rows read: w and xf hold one part more than is in use.
+    bf16x8 w[2][kNB], xf[2][kMB];
     auto expand = [&](const Codes& c, int part, bf16x8 o[kNB]) {
 #pragma unroll
       for (int m = 0; m < kMats; ++m)
@@ -288,30 +317,24 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
       auto frags = [&](int part) {
 #pragma unroll
         for (int i = 0; i < kMB; ++i)
-          xf[kAhead ? part & 1 : 0][i] = __builtin_bit_cast(bf16x8, xfrag(cur, i, 16 * wk + 4 * kb + part));
+          xf[part & 1][i] = __builtin_bit_cast(bf16x8, xfrag(cur, i, 16 * wk + 4 * kb + part));
       };
-      if (kAhead) frags(0);
+      frags(0);
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        store_part(nxt, part);
-        load_part(part, s_next, p_next);
+        store_part(nxt, held, part);
+        load_part(held, part, s_next, p_next);
         keep_loads();
-        if constexpr (kAhead) {
-          if (part < 3) frags(part + 1);
-          expand(part < 3 ? c : cn, (part + 1) & 3, w[(part + 1) & 1]);
-        } else {
-          frags(part);
-          expand(c, part, w[0]);
-        }
+        if (part < 3) frags(part + 1);
+        expand(part < 3 ? c : cn, (part + 1) & 3, w[(part + 1) & 1]);
 #pragma unroll
         for (int i = 0; i < kMB; ++i)
 #pragma unroll
           for (int j = 0; j < kNB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[kAhead ? part & 1 : 0][j], xf[kAhead ? part & 1 : 0][i],
-                                                              acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[part & 1][j], xf[part & 1][i], acc[i][j], 0, 0, 0);
       }
     };
-    if (kAhead) expand(ring[0], 0, w[0]);
+    expand(ring[0], 0, w[0]);
     for (int s = s_lo; s < s_hi; s += 2 * kWK) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -463,21 +486,18 @@ hipError_t start_rows(int bm, const MxTileArgs& a, hipStream_t stream) {
     switch (bm) {
       case 32: return start<0, kGlu, kM, 8 / kM, 1, 2 / kM, kN>(a, stream);
       case 64: return start<0, kGlu, kM, 8 / kM, 1, 4 / kM, kN>(a, stream);
-      case 128:
+      default:  // 128
+        if (a.cols == (kGlu ? 256 : 512)) return start<0, kGlu, 1, 8, 1, 8, 4>(a, stream);
         if constexpr (!kGlu) return start<0, false, 1, 8, 1, 8, 2>(a, stream);
         return start<0, kGlu, 2, 4, 1, 4, 4>(a, stream);
-      default: return start<0, kGlu, 2, 4, 1, 8, 4>(a, stream);
     }
   } else {
     switch (bm) {
       case 32: return start<kP, kGlu, 1, 4, 2, 2, 4>(a, stream);
       case 64: return start<kP, kGlu, 1, 4, 2, 4, 4>(a, stream);
-      case 128: return start<kP, kGlu, 2, 4, 1, 4, 4>(a, stream);
-      default:
-        if constexpr (kP == 1) return start<kP, kGlu, 2, 4, 1, 8, 4>(a, stream);  // (no plan with more planes)
+      default: return start<kP, kGlu, 2, 4, 1, 4, 4>(a, stream);  // 128
     }
   }
-  return hipErrorInvalidValue;
 }
 
 template <int kP>

@@ -33,6 +33,15 @@ def weight(rng, N, K, std=0.02):
     return upload(q, s), O.mx_values64(O.mx_pack(q), s)
 
 
+def big_weight(rng, N, K, std=0.02):
+    """As weight, of uniform codes and scales in three binades (no float64 copies of a large matrix on the way)."""
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    e = int(np.floor(np.log2(std / 3)))
+    s = rng.integers(126 + e, 129 + e, (N, K // 32)).astype(np.uint8)
+    rows_ = L.MxMatrix(torch.as_tensor(codes).cuda(), torch.as_tensor(s).cuda(), N, K)
+    return L.mx_prepack(rows_, L.mx_empty(N, K, L.MX_TILED)), O.mx_values64(codes, s)
+
+
 def upload(q, s):
     c = torch.as_tensor(O.mx_pack(q)).cuda()
     rows = L.MxMatrix(c, torch.as_tensor(s).cuda(), q.shape[0], q.shape[1])

@@ -6,7 +6,7 @@ import torch
 
 import int4_w4a16_group_g32_amd as L
 import oracle as O
-from mx_bounds import (TORCH, check, code_of, gemm_bound, mlp_reference, out_bound, rows, upload, weight)
+from mx_bounds import (TORCH, big_weight, check, code_of, gemm_bound, mlp_reference, out_bound, rows, upload, weight)
 
 pytestmark = pytest.mark.gpu
 
@@ -131,6 +131,65 @@ def test_swiglu_mlp_of_few_rows_and_a_wide_intermediate(M, H, I, kind):
     L.mx_swiglu_mlp(x, g, u, d, y, L.new_workspace(L.mx_swiglu_mlp_workspace_bytes(M, code_of(kind), g, u, d)))
     ref, b = mlp_reference(xv, gv, uv, dv, kind)
     check(y, ref, out_bound(ref, b, torch.float32), f"{M}x{H}x{I} {kind}")
+
+
+# shapes whose tiles share their columns' K among workgroups (the workspace holds their sums), in
+# tiles of 32, 64 and 128 rows, one row tile and several, K that ends inside a stage and a unit
+SHARED = [(20, 7168, 2576), (17, 4256, 4112), (50, 7168, 2576), (64, 4000, 4112), (64, 7136, 4112), (100, 4096, 2064),
+          (150, 2336, 784)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("M,K,N", SHARED)
+def test_gemm_of_shared_tiles(M, K, N, kind):
+    rng = np.random.default_rng(M + K + N)
+    w, wv = big_weight(rng, N, K)
+    x, xv = rows(rng, M, K, kind)
+    size = L.mx_gemm_workspace_bytes(M, code_of(kind), w)
+    # at least two workgroups' sums (64 rows of 4000 are streamed instead, unless float32)
+    assert size >= 2 * M * N * 4 or ((M, K) == (64, 4000) and kind != "f32")
+    y = torch.full((M + 1, N), 7.0, device="cuda")
+    ws = L.new_workspace(size)
+    L.mx_gemm(x, w, y[:M], ws)
+    ref = xv @ wv.T
+    check(y[:M], ref, out_bound(ref, gemm_bound(xv, wv, kind), torch.float32), f"{M}x{K}x{N} {kind}")
+    assert y[M].eq(7.0).all()
+    again = torch.empty((M, N), device="cuda")
+    L.mx_gemm(x, w, again, ws)
+    assert torch.equal(y[:M], again)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("M,H,I", [(20, 2048, 4128), (50, 2048, 4128), (100, 1024, 4128), (30, 4128, 2080)])
+def test_swiglu_mlp_of_shared_tiles(M, H, I, kind):
+    """One product in tiles or both, h handed on in either's form."""
+    rng = np.random.default_rng(M + H + I)
+    (g, gv), (u, uv), (d, dv) = big_weight(rng, I, H), big_weight(rng, I, H), big_weight(rng, H, I)
+    x, xv = rows(rng, M, H, kind)
+    y = torch.empty((M, H), device="cuda")
+    size = L.mx_swiglu_mlp_workspace_bytes(M, code_of(kind), g, u, d)
+    L.mx_swiglu_mlp(x, g, u, d, y, L.new_workspace(size))
+    ref, b = mlp_reference(xv, gv, uv, dv, kind)
+    check(y, ref, out_bound(ref, b, torch.float32), f"{M}x{H}x{I} {kind}")
+
+
+def test_tiles_of_twice_the_columns():
+    """Many MXFP4 rows and columns: 128 x 512 tiles, and 128 x 256 of h; ragged on both sides."""
+    rng = np.random.default_rng(5)
+    M, K, N = 1030, 160, 9232
+    w, wv = big_weight(rng, N, K)
+    x, xv = rows(rng, M, K, "mx")
+    y = torch.full((M + 1, N), 7.0, device="cuda")
+    L.mx_gemm(x, w, y[:M], L.new_workspace(L.mx_gemm_workspace_bytes(M, L.MXFP4, w)))
+    check(y[:M], xv @ wv.T, out_bound(xv @ wv.T, gemm_bound(xv, wv, "mx"), torch.float32), "gemm")
+    assert y[M].eq(7.0).all()
+    M, H, I = 1030, 96, 9248
+    (g, gv), (u, uv), (d, dv) = big_weight(rng, I, H, 0.2), big_weight(rng, I, H, 0.2), big_weight(rng, H, I)
+    x, xv = rows(rng, M, H, "mx")
+    y = torch.empty((M, H), device="cuda")
+    L.mx_swiglu_mlp(x, g, u, d, y, L.new_workspace(L.mx_swiglu_mlp_workspace_bytes(M, L.MXFP4, g, u, d)))
+    ref, b = mlp_reference(xv, gv, uv, dv, "mx")
+    check(y, ref, out_bound(ref, b, torch.float32), "mlp")
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
