@@ -532,8 +532,9 @@ W4A16_API size_t w4a16_mx_scales_bytes(int32_t rows, int32_t K, w4a16_mx_layout_
  * x / scale rounded to nearest, ties to the even code, at most 6, with x's sign.
  * A block of zeros has byte 0, one with an infinity or NaN byte 255 and codes 0.
  * Errors: INVALID_ARG (null/misaligned pointers, rows or K < 0, unknown type,
- * an output smaller than w4a16_mx_codes_bytes / w4a16_mx_scales_bytes),
- * UNSUPPORTED (the limits above); nothing is enqueued then.
+ * an output smaller than w4a16_mx_codes_bytes / w4a16_mx_scales_bytes, outputs
+ * that overlap each other or the input), UNSUPPORTED (the limits above); nothing
+ * is enqueued then.
  */
 W4A16_API w4a16_status_t w4a16_mx_quantize(const void* x, w4a16_dtype_t xt, int32_t rows, int32_t K, uint8_t* codes,
                                            size_t codes_bytes, uint8_t* scales, size_t scales_bytes,
@@ -558,9 +559,10 @@ W4A16_API w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_co
                                           hipStream_t stream);
 
 /*
- * out[rows][K] = the values, as float32 (exact) or bf16 (exact too, but for
- * magnitudes above bf16's largest), from either layout.  Errors as
- * w4a16_dequantize.
+ * out[rows][K] = the values, as float32 or bf16, from either layout: exact, and
+ * an infinity where a value is above the type's largest.  Errors: INVALID_ARG
+ * (null/misaligned, unknown type, out_bytes too small, out overlapping m),
+ * UNSUPPORTED (layout, the limits above).
  */
 W4A16_API w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4a16_dtype_t ot, size_t out_bytes,
                                              hipStream_t stream);
@@ -573,11 +575,12 @@ W4A16_API size_t w4a16_mx_gemm_workspace_bytes(int32_t M, w4a16_dtype_t xt, cons
  * float32, or bf16 rounded once, to nearest even.  Weights and rows enter the
  * matrix cores as exact bf16 values (a float32 value as three whose sum it is),
  * sums are float32.  Rows do not affect one another: an infinity or NaN in x[m]
- * reaches y[m] only (an infinity among float32 values as NaN).  Deterministic:
- * the same inputs give bitwise the same y.
- * Errors: INVALID_ARG (null/misaligned, M < 0, unknown type, y aliasing x),
- * UNSUPPORTED (layout, rows % 16, the limits above, M * N above 2^33),
- * WORKSPACE, HIP.
+ * reaches y[m] only (an infinity among float32 values as NaN); a weight above
+ * bf16's largest reaches its column as an infinity or NaN.  Deterministic: the
+ * same inputs give bitwise the same y.  With K = 0, y is zeros.
+ * Errors: INVALID_ARG (null/misaligned, M < 0, unknown type, y or ws overlapping
+ * x, the weights or each other), UNSUPPORTED (layout, rows % 16, the limits above,
+ * M * N above 2^33), WORKSPACE, HIP.
  */
 W4A16_API w4a16_status_t w4a16_mx_gemm(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_mx_t* w, void* y,
                                        w4a16_dtype_t yt, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -3,6 +3,7 @@
 #include "mx.h"
 
 #include <cmath>
+#include <initializer_list>
 
 namespace w4 {
 namespace {
@@ -52,13 +53,26 @@ w4a16_status_t rows_of(const w4a16_mx_t* x, int32_t K, MxRows& r) {
   return W4A16_OK;
 }
 
-// Pointers and overlaps shared by the products.
-w4a16_status_t check_io(const MxRows& r, const void* y, size_t ybytes, const void* ws) {
+// Pointers shared by the products, and that y and the workspace are apart from
+// each other and from all that is read.
+w4a16_status_t check_io(const MxRows& r, std::initializer_list<const w4a16_mx_t*> weights, const void* y,
+                        size_t ybytes, const void* ws, size_t ws_bytes) {
   if (r.x == nullptr || y == nullptr || ws == nullptr) return W4A16_ERR_INVALID_ARG;
   if (!aligned16(r.x) || !aligned16(y) || !aligned16(ws)) return W4A16_ERR_INVALID_ARG;
-  if (ranges_overlap(r.x, r.bytes, y, ybytes) || ranges_overlap(r.xs, r.sbytes, y, ybytes))
-    return W4A16_ERR_INVALID_ARG;
+  const auto hit = [&](const void* p, size_t n) {
+    return ranges_overlap(p, n, y, ybytes) || ranges_overlap(p, n, ws, ws_bytes);
+  };
+  if (hit(r.x, r.bytes) || hit(r.xs, r.sbytes) || ranges_overlap(y, ybytes, ws, ws_bytes)) return W4A16_ERR_INVALID_ARG;
+  for (const w4a16_mx_t* w : weights)
+    if (hit(w->codes, mx_codes_bytes(w->rows, w->K, true)) || hit(w->scales, mx_scales_bytes(w->rows, w->K, true)))
+      return W4A16_ERR_INVALID_ARG;
   return W4A16_OK;
+}
+
+// y of an empty sum
+w4a16_status_t zeros(void* y, size_t ybytes, hipStream_t stream) {
+  if (ybytes != 0 && (y == nullptr || !aligned16(y))) return W4A16_ERR_INVALID_ARG;
+  return w4a16_workspace_init(y, ybytes, stream);
 }
 
 MxArgs mx_args(const MxRows& r, int M, const w4a16_mx_t* w0, const w4a16_mx_t* w1, void* y) {
@@ -138,11 +152,12 @@ w4a16_status_t mx_product(MxX kind, bool glu, const MxTilePlan& t, MxArgs a, voi
 w4a16_status_t mx_gemm(const MxRows& r, int M, const w4a16_mx_t* w, void* y, w4a16_dtype_t yt, void* ws,
                        size_t ws_bytes, hipStream_t stream) {
   if (yt != W4A16_F32 && yt != W4A16_BF16) return W4A16_ERR_INVALID_ARG;
-  if (M == 0 || w->rows == 0 || w->K == 0) return W4A16_OK;
-  const w4a16_status_t st = check_io(r, y, static_cast<size_t>(M) * w->rows * dtype_bytes(yt), ws);
-  if (st != W4A16_OK) return st;
   if (static_cast<size_t>(M) * w->rows > kMxMaxValues) return W4A16_ERR_UNSUPPORTED;
+  const size_t ybytes = static_cast<size_t>(M) * w->rows * dtype_bytes(yt);
+  if (ybytes == 0 || w->K == 0) return zeros(y, ybytes, stream);
   const MxGemmPlan p = plan_mx_gemm(M, w, r.kind);
+  const w4a16_status_t st = check_io(r, {w}, y, ybytes, ws, std::min(ws_bytes, p.bytes));
+  if (st != W4A16_OK) return st;
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   MxArgs a = mx_args(r, M, w, nullptr, y);
   a.y_bf16 = yt == W4A16_BF16;
@@ -154,11 +169,13 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
                              const w4a16_mx_t* down, void* y, w4a16_dtype_t yt, void* ws, size_t ws_bytes,
                              hipStream_t stream) {
   if (yt != W4A16_F32 && yt != W4A16_BF16) return W4A16_ERR_INVALID_ARG;
-  if (M == 0 || gate->K == 0 || gate->rows == 0) return W4A16_OK;
-  w4a16_status_t st = check_io(r, y, static_cast<size_t>(M) * gate->K * dtype_bytes(yt), ws);
+  w4a16_status_t st = check_mx_shape(M, gate->rows);
   if (st != W4A16_OK) return st;
-  if ((st = check_mx_shape(M, gate->rows)) != W4A16_OK) return st;
+  const size_t ybytes = static_cast<size_t>(M) * gate->K * dtype_bytes(yt);
+  if (ybytes == 0 || gate->rows == 0) return zeros(y, ybytes, stream);
   const MxMlpPlan p = plan_mx_mlp(M, gate, r.kind);
+  st = check_io(r, {gate, up, down}, y, ybytes, ws, std::min(ws_bytes, p.bytes));
+  if (st != W4A16_OK) return st;
   if (ws_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   MxRows h;

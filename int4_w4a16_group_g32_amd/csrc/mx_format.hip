@@ -158,11 +158,15 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 
 inline unsigned blocks_for(size_t n) { return static_cast<unsigned>((n + 255) / 256); }
 
-// Output buffers of the quantisers and the prepack.
+// Output buffers of the quantisers and the prepack, apart from each other and
+// from `in`.
 w4a16_status_t check_out(const void* codes, size_t codes_bytes, const void* scales, size_t scales_bytes, size_t need_c,
-                         size_t need_s) {
+                         size_t need_s, const void* in, size_t in_bytes) {
   if (codes == nullptr || scales == nullptr || !aligned16(codes) || !aligned16(scales)) return W4A16_ERR_INVALID_ARG;
   if (codes_bytes < need_c || scales_bytes < need_s) return W4A16_ERR_INVALID_ARG;
+  if (ranges_overlap(codes, need_c, scales, need_s) || ranges_overlap(in, in_bytes, codes, need_c) ||
+      ranges_overlap(in, in_bytes, scales, need_s))
+    return W4A16_ERR_INVALID_ARG;
   return W4A16_OK;
 }
 
@@ -192,7 +196,7 @@ extern "C" w4a16_status_t w4a16_mx_quantize(const void* x, w4a16_dtype_t xt, int
   const size_t n = static_cast<size_t>(rows) * K;
   if (n == 0) return W4A16_OK;
   if (x == nullptr || !aligned16(x)) return W4A16_ERR_INVALID_ARG;
-  st = check_out(codes, codes_bytes, scales, scales_bytes, n / 2, n / kMxBlock);
+  st = check_out(codes, codes_bytes, scales, scales_bytes, n / 2, n / kMxBlock, x, n * dtype_bytes(xt));
   if (st != W4A16_OK) return st;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (xt == W4A16_F32)
@@ -211,7 +215,7 @@ extern "C" w4a16_status_t w4a16_mx_quantize_weight(const void* w, w4a16_dtype_t 
   const size_t n = static_cast<size_t>(N) * K;
   if (n == 0) return W4A16_OK;
   if (w == nullptr || !aligned16(w)) return W4A16_ERR_INVALID_ARG;
-  st = check_out(codes, codes_bytes, scales, scales_bytes, n / 2, n / kMxBlock);
+  st = check_out(codes, codes_bytes, scales, scales_bytes, n / 2, n / kMxBlock, w, n * dtype_bytes(wt));
   if (st != W4A16_OK) return st;
   uint4* c = reinterpret_cast<uint4*>(codes);
   if (wt == W4A16_F32)
@@ -231,14 +235,14 @@ extern "C" w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_c
   if (out == nullptr) return W4A16_ERR_INVALID_ARG;
   if (src->layout != W4A16_MX_ROWS || src->rows % 16 != 0) return W4A16_ERR_UNSUPPORTED;
   const size_t cb = mx_codes_bytes(src->rows, src->K, true), sb = mx_scales_bytes(src->rows, src->K, true);
-  st = check_out(dst_codes, dst_codes_bytes, dst_scales, dst_scales_bytes, cb, sb);
-  if (st != W4A16_OK) return st;
-  const void* ins[2] = {src->codes, src->scales};
-  const size_t in_bytes[2] = {mx_codes_bytes(src->rows, src->K, false), mx_scales_bytes(src->rows, src->K, false)};
-  for (int i = 0; i < 2; ++i)
-    if (ranges_overlap(ins[i], in_bytes[i], dst_codes, cb) || ranges_overlap(ins[i], in_bytes[i], dst_scales, sb))
+  if (cb != 0) {
+    st = check_out(dst_codes, dst_codes_bytes, dst_scales, dst_scales_bytes, cb, sb, src->codes,
+                   mx_codes_bytes(src->rows, src->K, false));
+    if (st != W4A16_OK) return st;
+    const size_t ib = mx_scales_bytes(src->rows, src->K, false);
+    if (ranges_overlap(src->scales, ib, dst_codes, cb) || ranges_overlap(src->scales, ib, dst_scales, sb))
       return W4A16_ERR_INVALID_ARG;
-  if (ranges_overlap(dst_codes, cb, dst_scales, sb)) return W4A16_ERR_INVALID_ARG;
+  }
   *out = *src;
   out->codes = dst_codes;
   out->scales = dst_scales;
@@ -255,13 +259,15 @@ extern "C" w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4
   const w4a16_status_t st = check_mx(m);
   if (st != W4A16_OK) return st;
   if (ot != W4A16_F32 && ot != W4A16_BF16) return W4A16_ERR_INVALID_ARG;
-  if (out == nullptr || !aligned16(out)) return W4A16_ERR_INVALID_ARG;
-  const size_t n = static_cast<size_t>(m->rows) * m->K;
-  if (out_bytes < n * dtype_bytes(ot)) return W4A16_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(m->rows) * m->K, need = n * dtype_bytes(ot);
   if (n == 0) return W4A16_OK;
+  if (out == nullptr || !aligned16(out) || out_bytes < need) return W4A16_ERR_INVALID_ARG;
   const uint32_t* c = reinterpret_cast<const uint32_t*>(m->codes);
   const int G = m->K / kMxBlock, S = (m->K + kMxStep - 1) / kMxStep;
   const bool tiled = m->layout == W4A16_MX_TILED;
+  if (ranges_overlap(m->codes, mx_codes_bytes(m->rows, m->K, tiled), out, need) ||
+      ranges_overlap(m->scales, mx_scales_bytes(m->rows, m->K, tiled), out, need))
+    return W4A16_ERR_INVALID_ARG;
   const unsigned blocks = blocks_for((n / 8 + kE - 1) / kE);
   auto run = [&](auto kernel, auto* o) { kernel<<<blocks, 256, 0, stream>>>(c, m->scales, n / 8, G, S, o); };
   if (ot == W4A16_F32) {

@@ -268,6 +268,23 @@ def test_zero_rows_do_nothing():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("yt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [1, 40])
+def test_empty_sums_are_zeros(M, yt):
+    """K of 0, and an MLP whose intermediate has no columns."""
+    ws = L.new_workspace(256)
+    w, d = L.mx_empty(48, 0, L.MX_TILED), L.mx_empty(64, 0, L.MX_TILED)
+    g = L.mx_empty(0, 64, L.MX_TILED)
+    for x in (torch.empty((M, 0), device="cuda"), L.mx_empty(M, 0)):
+        y = torch.full((M, 48), 7.0, dtype=yt, device="cuda")
+        L.mx_gemm(x, w, y, ws)
+        assert not y.any()
+    for x in (torch.ones((M, 64), device="cuda"), L.mx_empty(M, 64)):
+        y = torch.full((M, 64), 7.0, dtype=yt, device="cuda")
+        L.mx_swiglu_mlp(x, g, g, d, y, ws)
+        assert not y.any()
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
 @pytest.mark.parametrize("M", [4, 70, 260])
 def test_captured_and_replayed(M, kind):

@@ -243,3 +243,39 @@ def test_binding_refuses_norm_arguments(no_calls):
                dict(n=z(3, 64, t=torch.float16))):
         with pytest.raises(TypeError):
             L.block_norm(y, **{"n": z(3, 64), "pre_w": w, **kw})
+
+
+def test_overlaps_are_refused(lib):
+    """Outputs and workspaces that overlap an input, a weight or each other."""
+    q = lambda x, c, s: lib.w4a16_mx_quantize(_p(x), 0, 4, 64, _p(c), 128, _p(s), 8, None)  # noqa: E731
+    assert q(0x1000, 0x1010, 0x2000) == q(0x1000, 0x2000, 0x13f0) == q(0x1000, 0x2000, 0x2070) == L.ERR_INVALID_ARG
+    qw = lambda w, c, s: lib.w4a16_mx_quantize_weight(_p(w), 1, 64, 4, _p(c), 128, _p(s), 8, None)  # noqa: E731
+    assert qw(0x1000, 0x11f0, 0x2000) == qw(0x1000, 0x2000, 0x1000) == L.ERR_INVALID_ARG
+    for layout in (L.MX_ROWS, L.MX_TILED):
+        m = _mx(64, 256, layout, 0x100000, 0x200000)
+        for out in (0x100000, 0x101ff0, 0x200000, 0x200000 - 64 * 256 * 2 + 16):
+            assert lib.w4a16_mx_dequantize(ctypes.byref(m), _p(out), L.BF16, 1 << 20, None) == L.ERR_INVALID_ARG
+    w, r = _mx(64, 256, codes=0x100000, scales=0x200000), ctypes.byref
+    g, d = _mx(256, 256, codes=0x700000, scales=0x800000), _mx(256, 256, codes=0x900000, scales=0xa00000)
+    n = lib.w4a16_mx_gemm_workspace_bytes(40, L.F32, r(w))
+    for y, ws in ((0x101ff0, 0x500000), (0x2001f0, 0x500000), (0x400000, 0x300000), (0x400000, 0x400000),
+                  (0x400000, 0x100000), (0x400000, 0x200000)):
+        assert lib.w4a16_mx_gemm(_p(0x300000), L.F32, 40, r(w), _p(y), 0, _p(ws), n, None) == L.ERR_INVALID_ARG, (y, ws)
+    n = lib.w4a16_mx_swiglu_mlp_workspace_bytes(4, L.BF16, r(g), r(g), r(d))
+    for y, ws in ((0x900000, 0x500000), (0xa00000, 0x500000), (0x400000, 0x700010), (0x400000, 0x400010)):
+        assert lib.w4a16_mx_swiglu_mlp(_p(0x300000), L.BF16, 4, r(g), r(g), r(d), _p(y), 0, _p(ws), n,
+                                       None) == L.ERR_INVALID_ARG, (y, ws)
+
+
+def test_empty_matrices_need_no_pointers(lib):
+    r, out = ctypes.byref, L.MxDesc()
+    for rows, K in ((0, 64), (16, 0), (0, 0)):
+        m = _mx(rows, K, L.MX_ROWS, 0, 0)
+        assert lib.w4a16_mx_dequantize(r(m), None, 0, 0, None) == L.OK
+        assert lib.w4a16_mx_prepack(r(m), None, 0, None, 0, r(out), None) == L.OK
+        assert (out.rows, out.K, out.layout) == (rows, K, L.MX_TILED)
+        if rows == 0:
+            assert lib.w4a16_mx_gemm(None, 0, 4, r(out), None, 0, None, 0, None) == L.OK
+    w = _mx(16, 0, codes=0, scales=0)  # an empty sum still has its y
+    assert lib.w4a16_mx_gemm(None, 0, 4, r(w), None, 0, None, 0, None) == L.ERR_INVALID_ARG
+    assert lib.w4a16_mx_gemm(None, 0, 4, r(w), _p(0x1008), 0, None, 0, None) == L.ERR_INVALID_ARG
