@@ -182,8 +182,7 @@ struct MxArgs {
 // Rows in blocks of 16, the whole K inside a workgroup (mx_stream.hip).
 hipError_t launch_mx_stream(MxX xk, bool glu, const MxArgs& a, hipStream_t stream);
 constexpr int kMxStreamRows = 16;
-// 16-column blocks of a workgroup (of each matrix)
-int mx_stream_blocks(MxX xk, bool glu, int N);
+constexpr int kMxStreamCols = 32;  // of a workgroup (of each matrix) with more rows
 
 // More rows, tiles of them in LDS (mx_tile.hip).  x: [M][K] bf16, or float32
 // rows as bf16 planes [pieces][M][K], or MXFP4 rows; y as in MxArgs, or with glu

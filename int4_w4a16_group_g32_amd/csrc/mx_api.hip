@@ -203,17 +203,16 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
 //
 // Up to 16 rows stream.  More rows stream in blocks of 16, each reading the
 // weights (from the L2, mostly) and all of x once a workgroup, while that is
-// shorter than the tiles' longer way: 37 float32 rows, 2304 -> 7168, 19.6 us
-// streamed and 24.8 in tiles, 7168 -> 4096 44 and 27; 64 bf16 rows, 2304 -> 7168,
-// 15.0 and 18.5, 7168 -> 4096 29 and 19.  The times below are fitted to such
-// measurements (17 to 128 rows, K 1056 to 7168, N 1040 to 18432), in us.
+// shorter than the tiles' longer way: 37 float32 rows, 2304 -> 7168, 15 us
+// streamed and 25 in tiles, 7168 -> 18432 85 and 56; 64 bf16 rows, 2304 -> 7168,
+// 13.5 and 18.4, 7168 -> 18432 73 and 32.  The times below, in us, are fitted to
+// such measurements (17 to 128 rows, K 1056 to 7168, N 1040 to 18432).
 MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu) {
   constexpr int kCus = 256;
   MxTilePlan p;
   if (M <= kMxStreamRows) return p;
   const int mats = glu ? 2 : 1;
   const double planes = xk == kMxXf32 ? 3 : (xk == kMxXf32h ? 2 : 1);
-  const bool wide = xk == kMxXf32 || xk == kMxXf32h;
   p.cols = 256 / mats;
   p.tiles = (N + p.cols - 1) / p.cols;
   const int S = (K + kMxStep - 1) / kMxStep;
@@ -251,14 +250,13 @@ MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu) {
     }
   }
   if (M <= 128) {
-    const int nb = mx_stream_blocks(xk, glu, N), blocks = (M + 15) / 16;
-    const double wgs = std::ceil(N / (16.0 * nb)), xbytes = xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : 4);
-    const double slots = std::ceil(wgs * blocks / kCus), steps = std::ceil(S / 8.0);
-    const double traffic =
-        (wgs * 16 * K * xbytes / 11e6 + 0.53 * mats * N * K / 6e6) * (wide ? 1.4 : 1) + 0.8;
     const bool fp4 = xk == kMxXfp4;
-    const double slot = 0.7 + steps * (fp4 ? 0.55 + 0.1 * nb * mats : 0.3 + 0.25 * nb * mats);
-    const double stream_us = 2.5 + std::max(slots * slot, blocks * traffic);
+    // a start, and for the workgroups of a compute unit (of the busiest one and on
+    // average) a part of their own and one for each step
+    constexpr double kStart[4] = {3.5, 3.5, 3, 2.7}, kOwn[4] = {0.5, 0.4, 0.2, 0.2};
+    constexpr double kStep[2][4] = {{0.21, 0.20, 0.14, 0.125}, {0.35, 0.35, 0.27, 0.24}};
+    const double wgs = (N + kMxStreamCols - 1) / kMxStreamCols * ((M + 15) / 16) / static_cast<double>(kCus);
+    const double stream_us = kStart[xk] + (std::ceil(wgs) + wgs) / 2 * (kOwn[xk] + S * kStep[glu][xk]);
     const int h = p.bm == 32 ? 0 : (p.bm == 64 ? 1 : 2);
     constexpr double kBase[2][3] = {{8.5, 10.3, 12}, {6.8, 7.8, 7}}, kStage[2][3] = {{0.8, 1.5, 2.5}, {0.7, 0.8, 1}};
     const double tile_us = kBase[fp4][h] + (xk == kMxXf32 ? 2.3 : 0) + units * planes * kStage[fp4][h] + sums_us;

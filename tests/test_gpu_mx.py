@@ -135,19 +135,20 @@ def test_swiglu_mlp_of_few_rows_and_a_wide_intermediate(M, H, I, kind):
 
 # shapes whose tiles share their columns' K among workgroups (the workspace holds their sums), in
 # tiles of 32, 64 and 128 rows, one row tile and several, K that ends inside a stage and a unit
-SHARED = [(20, 7168, 2576), (17, 4256, 4112), (50, 7168, 2576), (64, 4000, 4112), (64, 7136, 4112), (100, 4096, 2064),
-          (150, 2336, 784)]
+SHARED = [(17, 7136, 4112), (32, 7136, 4112), (50, 7168, 4112), (64, 7136, 4112), (100, 6176, 4112), (150, 2336, 784)]
+# several blocks of 16 rows streamed (the first of MXFP4 rows in shared tiles), and unshared tiles of few rows
+OTHERS = [(50, 7168, 2576), (20, 7168, 2576), (17, 4256, 4112), (64, 4000, 4112), (100, 4096, 2064), (17, 288, 65552),
+          (40, 544, 65552)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
-@pytest.mark.parametrize("M,K,N", SHARED)
+@pytest.mark.parametrize("M,K,N", SHARED + OTHERS)
 def test_gemm_of_shared_tiles(M, K, N, kind):
     rng = np.random.default_rng(M + K + N)
     w, wv = big_weight(rng, N, K)
     x, xv = rows(rng, M, K, kind)
     size = L.mx_gemm_workspace_bytes(M, code_of(kind), w)
-    # at least two workgroups' sums (64 rows of 4000 are streamed instead, unless float32)
-    assert size >= 2 * M * N * 4 or ((M, K) == (64, 4000) and kind != "f32")
+    assert size >= 2 * M * N * 4 or (M, K, N) in OTHERS  # at least two workgroups' sums
     y = torch.full((M + 1, N), 7.0, device="cuda")
     ws = L.new_workspace(size)
     L.mx_gemm(x, w, y[:M], ws)
@@ -160,7 +161,8 @@ def test_gemm_of_shared_tiles(M, K, N, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
-@pytest.mark.parametrize("M,H,I", [(20, 2048, 4128), (50, 2048, 4128), (100, 1024, 4128), (30, 4128, 2080)])
+@pytest.mark.parametrize("M,H,I", [(20, 2048, 4128), (50, 2048, 4128), (100, 1024, 4128), (30, 4128, 2080),
+                                   (40, 7168, 4128), (72, 6176, 4128)])
 def test_swiglu_mlp_of_shared_tiles(M, H, I, kind):
     """One product in tiles or both, h handed on in either's form."""
     rng = np.random.default_rng(M + H + I)
