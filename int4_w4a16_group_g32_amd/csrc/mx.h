@@ -189,12 +189,14 @@ constexpr int kMxStreamCols = 32;  // of a workgroup (of each matrix) with more 
 // h as bf16 planes or MXFP4 rows.
 struct MxTileArgs : MxArgs {
   float* planes;  // sums of shared tiles: [workgroup of a tile][matrices][M][N]
-  int tiles, row_tiles, band, bm, cols;
+  int tiles, row_tiles, band, bm, cols, tile0;  // tile0: the first column tile of the launch
   int unit_steps, per, quota;  // steps of a unit of K; units of a tile, and of a workgroup
 };
 struct MxTilePlan {
   int bm = 0, cols = 0, tiles = 0, unit_steps = 0, per = 0, quota = 0;
   size_t plane_bytes = 0;  // 0: every tile is one workgroup's
+  // tiles of other sizes from column rest_from on (0: none)
+  int rest_from = 0, rest_bm = 0, rest_cols = 0;
 };
 // (bm 0: the streamed form)
 MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu);

@@ -249,6 +249,28 @@ MxTilePlan plan_mx_product(int M, int N, int K, MxX xk, bool glu) {
       sums_us = us;
     }
   }
+  // A last round that few workgroups would have: its columns in smaller tiles, if
+  // one round of them is shorter (a round of 64-row tiles takes 0.6 of one of 128
+  // bf16 or float32 rows; of MXFP4 rows 0.72, gate and up 0.8, and from the wide
+  // tiles 0.49 and 0.56, 128-row tiles of half the columns 0.69) by more than a
+  // launch.  1024 MXFP4 rows, 7168 -> 18432 gate and up: 2 rounds and a quarter.
+  if (M > 128 && tiles > kCus && tiles % kCus != 0) {
+    const size_t row_tiles = (M + p.bm - 1) / p.bm;
+    const int full = static_cast<int>(tiles / kCus * kCus / row_tiles) * p.cols;
+    const int narrow = 256 / mats;
+    const bool wide = p.cols != narrow;
+    const double step_us = xk == kMxXfp4 ? (wide ? 0.92 : 0.62) : 1.5 * planes;
+    const auto rounds = [&](int bm) {
+      return std::ceil(std::ceil(static_cast<double>(M) / bm) * ((N - full + narrow - 1) / narrow) / kCus);
+    };
+    const double half = rounds(64) * (xk != kMxXfp4 ? 0.6 : (wide ? (glu ? 0.56 : 0.49) : (glu ? 0.8 : 0.72)));
+    const double other = wide ? rounds(128) * 0.69 : 1;
+    if (full > 0 && (1 - std::min(half, other)) * S * step_us > 4) {
+      p.rest_from = full;
+      p.rest_bm = half < other ? 64 : 128;
+      p.rest_cols = narrow;
+    }
+  }
   if (M <= 128) {
     const bool fp4 = xk == kMxXfp4;
     // a start, and for the workgroups of a compute unit (of the busiest one and on

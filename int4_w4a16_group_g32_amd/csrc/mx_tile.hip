@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   const bool whole = run == a.per;
   const int slot = task - u * a.per / a.quota;  // among the workgroups of this tile
   unit += run;
-  n0 = tile * kBN + wn * kCols;
+  n0 = (a.tile0 + tile) * kBN + wn * kCols;
   c0 = n0 / 16 % 4;
   {
     // (a wave past the last column streams tile 0 and stores nothing)
@@ -508,26 +508,35 @@ hipError_t start_glu(bool glu, int bm, const MxTileArgs& a, hipStream_t stream) 
 }  // namespace
 
 hipError_t launch_mx_tile(MxX xk, bool glu, const MxTilePlan& p, MxTileArgs& a, hipStream_t stream) {
-  a.tiles = p.tiles;
-  a.bm = p.bm;
-  a.cols = p.cols;
   a.unit_steps = p.unit_steps;
   a.per = p.per;
   a.quota = p.quota;
-  a.row_tiles = (a.M + p.bm - 1) / p.bm;
-  // a run of n tasks as r row tiles of xb bytes by n / r column tiles of wb:
-  // r xb + n / r wb is least at r = sqrt(n wb / xb)
-  const double n = std::max(1.0, static_cast<double>(a.row_tiles) * a.tiles / kXcds);
-  const double xb = p.bm * (xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : (xk == kMxXf32h ? 4 : 6)));
-  const double wb = p.cols * 0.53 * (glu ? 2 : 1);
-  a.band = p.plane_bytes != 0 ? a.row_tiles : std::min(a.row_tiles, std::max(1, static_cast<int>(std::sqrt(n * wb / xb) + 0.5)));
-  hipError_t e = hipErrorInvalidValue;
-  switch (xk) {
-    case kMxXf32: e = start_glu<3>(glu, p.bm, a, stream); break;
-    case kMxXf32h: e = start_rows<2, false>(p.bm, a, stream); break;
-    case kMxXbf16: e = start_glu<1>(glu, p.bm, a, stream); break;
-    case kMxXfp4: e = start_glu<0>(glu, p.bm, a, stream); break;
+  const auto columns = [&](int from, int to, int bm, int cols) {
+    a.tile0 = from / cols;
+    a.tiles = (to - from + cols - 1) / cols;
+    a.bm = bm;
+    a.cols = cols;
+    a.row_tiles = (a.M + bm - 1) / bm;
+    // a run of n tasks as r row tiles of xb bytes by n / r column tiles of wb:
+    // r xb + n / r wb is least at r = sqrt(n wb / xb)
+    const double n = std::max(1.0, static_cast<double>(a.row_tiles) * a.tiles / kXcds);
+    const double xb = bm * (xk == kMxXfp4 ? 0.53 : (xk == kMxXbf16 ? 2 : (xk == kMxXf32h ? 4 : 6)));
+    const double wb = cols * 0.53 * (glu ? 2 : 1);
+    a.band = p.plane_bytes != 0 ? a.row_tiles
+                                : std::min(a.row_tiles, std::max(1, static_cast<int>(std::sqrt(n * wb / xb) + 0.5)));
+    switch (xk) {
+      case kMxXf32: return start_glu<3>(glu, bm, a, stream);
+      case kMxXf32h: return start_rows<2, false>(bm, a, stream);
+      case kMxXbf16: return start_glu<1>(glu, bm, a, stream);
+      case kMxXfp4: return start_glu<0>(glu, bm, a, stream);
+    }
+    return hipErrorInvalidValue;
+  };
+  if (p.rest_from != 0) {
+    const hipError_t e = columns(0, p.rest_from, p.bm, p.cols);
+    return e != hipSuccess ? e : columns(p.rest_from, a.N, p.rest_bm, p.rest_cols);
   }
+  const hipError_t e = columns(0, a.N, p.bm, p.cols);
   if (e != hipSuccess || p.plane_bytes == 0) return e;
   const size_t n4 = static_cast<size_t>(a.M) * a.N / 4;
   const unsigned blocks = static_cast<unsigned>((n4 + 255) / 256);

@@ -194,6 +194,32 @@ def test_tiles_of_twice_the_columns():
     check(y, ref, out_bound(ref, b, torch.float32), "mlp")
 
 
+# more tiles than the card has compute units, and not a multiple: the last columns go in smaller tiles
+@pytest.mark.parametrize("kind,M,K,N", [("f32", 2060, 1312, 4112), ("bf16", 2060, 1312, 4112), ("bf16", 260, 928, 23056),
+                                        ("mx", 2060, 4128, 7824), ("mx", 1030, 4128, 16912)])
+def test_gemm_of_a_ragged_last_round(kind, M, K, N):
+    rng = np.random.default_rng(M + K + N)
+    w, wv = big_weight(rng, N, K)
+    x, xv = rows(rng, M, K, kind)
+    y = torch.full((M + 1, N), 7.0, device="cuda")
+    L.mx_gemm(x, w, y[:M], L.new_workspace(L.mx_gemm_workspace_bytes(M, code_of(kind), w)))
+    ref = xv @ wv.T
+    check(y[:M], ref, out_bound(ref, gemm_bound(xv, wv, kind), torch.float32), f"{M}x{K}x{N} {kind}")
+    assert y[M].eq(7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+def test_swiglu_mlp_of_a_ragged_last_round(kind):
+    rng = np.random.default_rng(9)
+    M, H, I = 1030, 1312, 7200
+    (g, gv), (u, uv), (d, dv) = big_weight(rng, I, H), big_weight(rng, I, H), big_weight(rng, H, I)
+    x, xv = rows(rng, M, H, kind)
+    y = torch.empty((M, H), device="cuda")
+    L.mx_swiglu_mlp(x, g, u, d, y, L.new_workspace(L.mx_swiglu_mlp_workspace_bytes(M, code_of(kind), g, u, d)))
+    ref, b = mlp_reference(xv, gv, uv, dv, kind)
+    check(y, ref, out_bound(ref, b, torch.float32), f"{M}x{H}x{I} {kind}")
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
 @pytest.mark.parametrize("M", [3, 40, 300])
 def test_gemm_scales_over_the_whole_range(M, kind):
