@@ -532,9 +532,9 @@ W4A16_API size_t w4a16_mx_scales_bytes(int32_t rows, int32_t K, w4a16_mx_layout_
  * x / scale rounded to nearest, ties to the even code, at most 6, with x's sign.
  * A block of zeros has byte 0, one with an infinity or NaN byte 255 and codes 0.
  * Errors: INVALID_ARG (null/misaligned pointers, rows or K < 0, unknown type,
- * an output smaller than w4a16_mx_codes_bytes / w4a16_mx_scales_bytes, outputs
- * that overlap each other or the input), UNSUPPORTED (the limits above); nothing
- * is enqueued then.
+ * outputs that overlap each other or the input), WORKSPACE (an output smaller
+ * than w4a16_mx_codes_bytes / w4a16_mx_scales_bytes), UNSUPPORTED (the limits
+ * above); nothing is enqueued then.
  */
 W4A16_API w4a16_status_t w4a16_mx_quantize(const void* x, w4a16_dtype_t xt, int32_t rows, int32_t K, uint8_t* codes,
                                            size_t codes_bytes, uint8_t* scales, size_t scales_bytes,
@@ -551,8 +551,8 @@ W4A16_API w4a16_status_t w4a16_mx_quantize_weight(const void* w, w4a16_dtype_t w
 /*
  * ROWS -> TILED, into dst_codes and dst_scales (w4a16_mx_codes_bytes and
  * w4a16_mx_scales_bytes of the TILED layout); `out` receives the descriptor.
- * Errors: INVALID_ARG (null/misaligned, too small, overlapping), UNSUPPORTED
- * (src not ROWS, rows not a multiple of 16, the limits above).
+ * Errors: INVALID_ARG (null/misaligned, overlapping), WORKSPACE (too small),
+ * UNSUPPORTED (src not ROWS, rows not a multiple of 16, the limits above).
  */
 W4A16_API w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_codes, size_t dst_codes_bytes,
                                           uint8_t* dst_scales, size_t dst_scales_bytes, w4a16_mx_t* out,
@@ -561,8 +561,8 @@ W4A16_API w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_co
 /*
  * out[rows][K] = the values, as float32 or bf16, from either layout: exact, and
  * an infinity where a value is above the type's largest.  Errors: INVALID_ARG
- * (null/misaligned, unknown type, out_bytes too small, out overlapping m),
- * UNSUPPORTED (layout, the limits above).
+ * (null/misaligned, unknown type, out overlapping m), WORKSPACE (out_bytes too
+ * small), UNSUPPORTED (layout, the limits above).
  */
 W4A16_API w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4a16_dtype_t ot, size_t out_bytes,
                                              hipStream_t stream);
@@ -652,12 +652,11 @@ typedef struct {
 
 /*
  * Means and products are float32, with MXFP4 rows float64 (their codes then do
- * not depend on the order of a sum).  Rows do not
- * affect one another.  Errors: INVALID_ARG (p or y NULL, pre_w NULL with n,
+ * not depend on the order of a sum).  Rows do not affect one another.  Errors: INVALID_ARG (p or y NULL, pre_w NULL with n,
  * neither r_out nor n, one of n_codes and n_scales alone or both beside n,
  * misaligned, unknown type, gate_rows not 1 or M, an output that overlaps an
- * input, other than r_out == r, or another output), UNSUPPORTED (H not a multiple of 8, with MXFP4 rows 32,
- * or above W4A16_NORM_MAX_H; M above 2^24).
+ * input, other than r_out == r, or another output), UNSUPPORTED (H not a
+ * multiple of 8, with MXFP4 rows 32, or above W4A16_NORM_MAX_H; M above 2^24).
  */
 W4A16_API w4a16_status_t w4a16_block_norm(const w4a16_norm_t* p, int32_t M, int32_t H, hipStream_t stream);
 

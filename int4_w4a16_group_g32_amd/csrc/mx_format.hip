@@ -163,7 +163,7 @@ inline unsigned blocks_for(size_t n) { return static_cast<unsigned>((n + 255) / 
 w4a16_status_t check_out(const void* codes, size_t codes_bytes, const void* scales, size_t scales_bytes, size_t need_c,
                          size_t need_s, const void* in, size_t in_bytes) {
   if (codes == nullptr || scales == nullptr || !aligned16(codes) || !aligned16(scales)) return W4A16_ERR_INVALID_ARG;
-  if (codes_bytes < need_c || scales_bytes < need_s) return W4A16_ERR_INVALID_ARG;
+  if (codes_bytes < need_c || scales_bytes < need_s) return W4A16_ERR_WORKSPACE;
   if (ranges_overlap(codes, need_c, scales, need_s) || ranges_overlap(in, in_bytes, codes, need_c) ||
       ranges_overlap(in, in_bytes, scales, need_s))
     return W4A16_ERR_INVALID_ARG;
@@ -261,7 +261,8 @@ extern "C" w4a16_status_t w4a16_mx_dequantize(const w4a16_mx_t* m, void* out, w4
   if (ot != W4A16_F32 && ot != W4A16_BF16) return W4A16_ERR_INVALID_ARG;
   const size_t n = static_cast<size_t>(m->rows) * m->K, need = n * dtype_bytes(ot);
   if (n == 0) return W4A16_OK;
-  if (out == nullptr || !aligned16(out) || out_bytes < need) return W4A16_ERR_INVALID_ARG;
+  if (out == nullptr || !aligned16(out)) return W4A16_ERR_INVALID_ARG;
+  if (out_bytes < need) return W4A16_ERR_WORKSPACE;
   const uint32_t* c = reinterpret_cast<const uint32_t*>(m->codes);
   const int G = m->K / kMxBlock, S = (m->K + kMxStep - 1) / kMxStep;
   const bool tiled = m->layout == W4A16_MX_TILED;

@@ -4,15 +4,28 @@
 // mx_stream.hip: the weights are the matrix cores' first operand, the rows of x
 // the second, and a lane ends with four adjacent columns of one row.
 //
-// A workgroup has eight waves, kWM along the rows, kWN along the columns and
-// kWK along K, a wave kMB x kNB blocks of 16 x 16.  The rows of one stage of K (128 of bf16,
-// 256 of MXFP4) are staged in LDS, double-buffered, one barrier a stage; each
-// wave streams its own columns' codes into registers two steps ahead and, for
-// 16-bit rows, expands them there.  float32 rows come as bf16 planes (pieces
+// A workgroup has eight waves, kWM along the rows, kWN along the columns and kWK
+// along K, a wave kMB x kNB blocks of 16 x 16: tiles of 128 rows by 256 columns
+// (of gate and up 128 each), fewer rows where there are no more, then with two
+// waves along K instead of along the rows; MXFP4 rows also 128 by 512, which
+// halves the rows' way through L2 and LDS.  The rows of a stage of K (128 k of
+// bf16, 256 with two waves along K, 512 of MXFP4) are staged in LDS, double-
+// buffered, one barrier a stage; each wave streams its own columns' codes into
+// registers two steps ahead and, for 16-bit rows, expands them there, a quarter
+// of a step ahead of their products.  float32 rows come as bf16 planes (pieces
 // whose sum they are), staged one after another against the same codes.
 //
-// LDS rows are 16-byte chunks, chunk c of row r at c ^ (r mod chunks): the 16
-// rows a fragment read touches then lie in distinct bank groups.
+// LDS rows are 16-byte chunks, chunk c of row r at c ^ (r mod chunks), which
+// serves a fragment read of MXFP4 rows in the least time; bf16 reads, four chunks
+// apart, are served twice.  An order without that took the same time.
+//
+// Bound: 2048 bf16 rows, 7168 -> 4096, 90 us (1.34 PFLOP/s, matrix cores 54 %
+// busy with one workgroup a compute unit: the rest is the expansion, the LDS reads
+// and a stage's barrier); MXFP4 rows the same product 37 us (3.3 PFLOP/s, 29 %),
+// where a stage's chain of code loads, staging and LDS reads, at two waves a SIMD,
+// is longer than its 64 products a wave; 1024 MXFP4 rows through the 7168 / 18432
+// MLP 243 us (3.35 PFLOP/s).  64 bf16 rows through it 91 us, 2.3 TB/s of weights:
+// each workgroup's start, the sums' planes (12 us) and the expansion.
 #include "mx.h"
 
 #include <cmath>
@@ -31,7 +44,8 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off, int s
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
 }
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
-  return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
+  return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]),
+               0, 0, 0, 0};
 }
 
 // The compiler moves no vector memory access across this.
@@ -132,7 +146,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
     const int row = srow + i * kRowsAt;
     const int k16 = s * (kFp4 ? 4 : 16) + chunk;  // 16-byte unit of the row
     const bool on = row < nrows && k16 * 16 < static_cast<int>(xrow) && s + (kFp4 ? 0 : chunk / 16) < s_hi;
-    h.x[i] = load16(kPlanes == 1 ? xr : rsrc(xbase + p * plane, nrows * xrow), on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
+    h.x[i] = load16(kPlanes == 1 ? xr : rsrc(xbase + p * plane, nrows * xrow),
+                    on ? row * static_cast<int>(xrow) + k16 * 16 : kOob, 0);
   };
   auto stage_store = [&](Buffer& buf, const Held& h, int i) {
     const int row = srow + i * kRowsAt;
@@ -164,8 +179,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   };
   auto scale_store = [&](Buffer& buf, const Held& h) {
     if (!stages_scales) return;
-    const uint32_t a01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x05010400), b01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x07030602);
-    const uint32_t a23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x05010400), b23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x07030602);
+    const uint32_t a01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x05010400);
+    const uint32_t b01 = __builtin_amdgcn_perm(h.s[1], h.s[0], 0x07030602);
+    const uint32_t a23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x05010400);
+    const uint32_t b23 = __builtin_amdgcn_perm(h.s[3], h.s[2], 0x07030602);
     uint32_t* o = buf.s + (ss * kQuads + sg) * 64 + t % 16;
     o[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100);
     o[16] = __builtin_amdgcn_perm(a23, a01, 0x07060302);

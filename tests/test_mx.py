@@ -71,26 +71,29 @@ def test_quantize_refusals(lib):
     def call(x=0x1000, xt=0, rows=4, K=64, c=0x100000, cb=128, s=0x200000, sb=8, fn=lib.w4a16_mx_quantize):
         return fn(_p(x), xt, rows, K, _p(c), cb, _p(s), sb, None)
     assert call(rows=0, x=0) == L.OK
-    for kw in (dict(x=0), dict(x=0x1008), dict(xt=2), dict(rows=-1), dict(c=0), dict(s=0), dict(cb=127), dict(sb=7),
+    for kw in (dict(x=0), dict(x=0x1008), dict(xt=2), dict(rows=-1), dict(c=0), dict(s=0),
                dict(s=0x200004)):
         assert call(**kw) == L.ERR_INVALID_ARG, kw
+    assert call(cb=127) == call(sb=7) == L.ERR_WORKSPACE
     for kw in (dict(K=48), dict(K=(1 << 20) + 32)):
         assert call(**kw) == L.ERR_UNSUPPORTED, kw
     qw = lambda **kw: lib.w4a16_mx_quantize_weight(_p(kw.get("w", 0x1000)), kw.get("wt", 0), kw.get("K", 64), 4,  # noqa: E731
                                                    _p(0x100000), kw.get("cb", 128), _p(0x200000), 8, None)
-    assert qw(w=0) == qw(wt=5) == qw(cb=100) == qw(K=-32) == L.ERR_INVALID_ARG and qw(K=33) == L.ERR_UNSUPPORTED
+    assert qw(w=0) == qw(wt=5) == qw(K=-32) == L.ERR_INVALID_ARG and qw(K=33) == L.ERR_UNSUPPORTED
+    assert qw(cb=100) == L.ERR_WORKSPACE
 
 
 def test_prepack_and_dequantize_refusals(lib):
     src, out = _mx(64, 256, L.MX_ROWS), L.MxDesc()
     call = lambda s=src, c=0x300000, cb=8192, sc=0x400000, sb=512, o=out: lib.w4a16_mx_prepack(  # noqa: E731
         ctypes.byref(s), _p(c), cb, _p(sc), sb, ctypes.byref(o) if o is not None else None, None)
-    for kw in (dict(c=0), dict(cb=8191), dict(sb=511), dict(o=None), dict(c=0x100800), dict(sc=0x300010),
+    for kw in (dict(c=0), dict(o=None), dict(c=0x100800), dict(sc=0x300010),
                dict(s=_mx(64, 256, L.MX_ROWS, codes=0)), dict(s=_mx(64, 256, L.MX_ROWS, scales=0x200004))):
         assert call(**kw) == L.ERR_INVALID_ARG, kw
+    assert call(cb=8191) == call(sb=511) == L.ERR_WORKSPACE
     assert call(s=_mx()) == call(s=_mx(63, 256, L.MX_ROWS)) == call(s=_mx(64, 40, L.MX_ROWS)) == L.ERR_UNSUPPORTED
     deq = lambda m, o=0x300000, t=0, n=1 << 30: lib.w4a16_mx_dequantize(ctypes.byref(m), _p(o), t, n, None)  # noqa: E731
-    assert deq(src, o=0) == deq(src, t=2) == deq(src, n=64 * 256 * 4 - 1) == L.ERR_INVALID_ARG
+    assert deq(src, o=0) == deq(src, t=2) == L.ERR_INVALID_ARG and deq(src, n=64 * 256 * 4 - 1) == L.ERR_WORKSPACE
     assert deq(_mx(layout=7)) == L.ERR_UNSUPPORTED
     assert lib.w4a16_mx_dequantize(None, _p(0x1000), 0, 64, None) == L.ERR_INVALID_ARG
 
