@@ -699,9 +699,12 @@ def mx_dequantize(m: MxMatrix, out: torch.Tensor, stream=None):
 def mx_quantize_to_weight(w: torch.Tensor, stream=None) -> MxMatrix:
     """Quantize device weights [K][N] and prepack them (TILED)."""
     K, N = w.shape
-    rows = mx_empty(N, K, MX_ROWS, w.device)
-    mx_quantize_weight(w, rows, stream)
-    return mx_prepack(rows, mx_empty(N, K, MX_TILED, w.device), stream)
+    if stream is not None:
+        _stream(stream)  # (of the current device)
+    with torch.cuda.stream(stream):  # the rows, freed on return, are that stream's memory
+        rows = mx_empty(N, K, MX_ROWS, w.device)
+        mx_quantize_weight(w, rows, stream)
+        return mx_prepack(rows, mx_empty(N, K, MX_TILED, w.device), stream)
 
 
 def mx_gemm_workspace_bytes(M: int, xt: int, w: MxMatrix) -> int:

@@ -361,6 +361,19 @@ def test_two_streams_with_their_own_workspaces():
     assert all(torch.equal(a, b) for a, b in zip(ys, want))
 
 
+def test_weights_quantized_on_another_stream():
+    """Their intermediate rows are freed while that stream still works: the current stream's tensors are not put there."""
+    w = torch.randn((4096, 4096), device="cuda")
+    want = L.mx_quantize_to_weight(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [L.mx_quantize_to_weight(w, side) for _ in range(3)]
+    other = [torch.full((4096 * 2048,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g.codes, want.codes) and torch.equal(g.scales, want.scales) for g in got)
+    assert all(o.eq(255).all() for o in other)
+
+
 def test_rows_behind_the_last_stay_as_they_were():
     rng = np.random.default_rng(3)
     w, _ = weight(rng, 272, 160)
