@@ -638,7 +638,7 @@ W4A16_API w4a16_status_t w4a16_mx_swiglu_mlp_a4(const w4a16_mx_t* x, const w4a16
 typedef struct {
   const void* y;         /* device: [M][H] of y_type */
   const void* r;         /* device: [M][H] of r_type, or NULL */
-  void* r_out;           /* device: s, [M][H] of r_type, or NULL; may be r */
+  void* r_out;           /* device: s, [M][H] of r_type, or NULL; may be r (and then y too, if of r_type) */
   const void* post_w;    /* device: [H] of w_type, or NULL */
   const void* pre_w;     /* device: [H] of w_type (unused without n) */
   const void* gate;      /* device: [gate_rows][H] of w_type, or NULL */
@@ -654,8 +654,9 @@ typedef struct {
  * Means and products are float32, with MXFP4 rows float64 (their codes then do
  * not depend on the order of a sum).  Rows do not affect one another.  Errors: INVALID_ARG (p or y NULL, pre_w NULL with n,
  * neither r_out nor n, one of n_codes and n_scales alone or both beside n,
- * misaligned, unknown type, gate_rows not 1 or M, an output that overlaps an
- * input, other than r_out == r, or another output), UNSUPPORTED (H not a
+ * misaligned, unknown type, gate_rows not 1 or M, an output that overlaps
+ * another output or an input, other than r_out == r and with it y == r of one
+ * type), UNSUPPORTED (H not a
  * multiple of 8, with MXFP4 rows 32, or above W4A16_NORM_MAX_H; M above 2^24).
  */
 W4A16_API w4a16_status_t w4a16_block_norm(const w4a16_norm_t* p, int32_t M, int32_t H, hipStream_t stream);

@@ -325,7 +325,11 @@ extern "C" w4a16_status_t w4a16_block_norm(const w4a16_norm_t* p, int32_t M, int
     if (o.p == nullptr) continue;
     if (!aligned16(o.p)) return W4A16_ERR_INVALID_ARG;
     for (const auto& i : ins) {
-      if (i.p == nullptr || (i.p == p->r && o.p == p->r && o.p == p->r_out)) continue;  // (r in place)
+      if (i.p == nullptr) continue;
+      // in place: a thread has read its values of r, and of y where that is r, before it writes them;
+      // a weight or gate there would be read by other rows too
+      const bool in_place = &i == &ins[1] || (&i == &ins[0] && p->y == p->r && p->y_type == p->r_type);
+      if (&o == &outs[0] && p->r_out == p->r && in_place) continue;
       if (ranges_overlap(i.p, i.bytes, o.p, o.bytes)) return W4A16_ERR_INVALID_ARG;
     }
     for (const auto& q : outs)

@@ -1,0 +1,31 @@
+"""CPU checks of refusals of the MXFP4 calls and block_norm: tensors that lie on one another, and sizes
+past the limits (nothing is enqueued: these pointers are not device memory)."""
+import ctypes
+
+import pytest
+
+import int4_w4a16_group_g32_amd as L
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return L.load_library()
+
+
+R = 0x200000  # r and r_out
+
+
+def _norm(lib, M=4, H=64, **kw):
+    a = dict(y=0x100000, r=R, r_out=R, post_w=None, pre_w=0x400000, gate=None, gate_rows=1, n=0x500000, n_codes=None,
+             n_scales=None, y_type=L.F32, r_type=L.F32, w_type=L.F32, n_type=L.F32, alpha=1.0, eps=1e-6)
+    a.update(kw)
+    return lib.w4a16_block_norm(ctypes.byref(L.NormDesc(**a)), M, H, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(gate=R), dict(gate=R, gate_rows=4), dict(gate=R, w_type=L.BF16), dict(gate=R + 256), dict(post_w=R), dict(pre_w=R),
+    dict(pre_w=R + 512), dict(y=R, r_type=L.BF16), dict(y=R, y_type=L.BF16), dict(y=R + 16), dict(y=R, r=None),
+    dict(n=R), dict(y=R, n=R), dict(n=None, n_codes=R, n_scales=0x600000), dict(n=None, n_codes=0x500000, n_scales=R)])
+def test_an_input_in_place_of_the_residual_is_refused(lib, kw):
+    """Only r itself (and y of its type) may be where r_out is: whatever other rows read too may not."""
+    assert _norm(lib, **kw) == L.ERR_INVALID_ARG
