@@ -293,7 +293,9 @@ using namespace w4;
 
 extern "C" size_t w4a16_mx_gemm_workspace_bytes(int32_t M, w4a16_dtype_t xt, const w4a16_mx_t* w) {
   MxRows r;
-  if (M <= 0 || check_mx_weight(w) != W4A16_OK || rows_of(nullptr, xt, M, w->K, r) != W4A16_OK) return 0;
+  if (M <= 0 || check_mx_weight(w) != W4A16_OK || rows_of(nullptr, xt, M, w->K, r) != W4A16_OK ||
+      static_cast<size_t>(M) * w->rows > kMxMaxValues)
+    return 0;
   return plan_mx_gemm(M, w, r.kind).bytes;
 }
 
@@ -306,7 +308,9 @@ extern "C" w4a16_status_t w4a16_mx_gemm(const void* x, w4a16_dtype_t xt, int32_t
 }
 
 extern "C" size_t w4a16_mx_gemm_a4_workspace_bytes(int32_t M, const w4a16_mx_t* w) {
-  if (M <= 0 || check_mx_weight(w) != W4A16_OK || check_mx_shape(M, w->K) != W4A16_OK) return 0;
+  if (M <= 0 || check_mx_weight(w) != W4A16_OK || check_mx_shape(M, w->K) != W4A16_OK ||
+      static_cast<size_t>(M) * w->rows > kMxMaxValues)
+    return 0;
   return plan_mx_gemm(M, w, kMxXfp4).bytes;
 }
 

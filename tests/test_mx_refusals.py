@@ -29,3 +29,17 @@ def _norm(lib, M=4, H=64, **kw):
 def test_an_input_in_place_of_the_residual_is_refused(lib, kw):
     """Only r itself (and y of its type) may be where r_out is: whatever other rows read too may not."""
     assert _norm(lib, **kw) == L.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,rows,K", [(1 << 14, 1 << 20, 8192), (513, 1 << 24, 32), (1 << 24, 528, 32),
+                                      (1 << 24, 1 << 24, 32)])
+def test_products_of_more_values_than_the_limit_have_no_workspace_size(lib, M, rows, K):
+    """M * N above 2^33: the call is refused, and its size is 0."""
+    w = L.MxDesc(0x100000, 0x200000, rows, K, L.MX_TILED)
+    p, r = ctypes.c_void_p, ctypes.byref
+    x = L.MxDesc(0x300000, 0x400000, M, K, L.MX_ROWS)
+    for xt in (L.F32, L.BF16):
+        assert lib.w4a16_mx_gemm_workspace_bytes(M, xt, r(w)) == 0
+        assert lib.w4a16_mx_gemm(p(0x300000), xt, M, r(w), p(0x500000), L.F32, p(0x600000), 1 << 40, None) == L.ERR_UNSUPPORTED
+    assert lib.w4a16_mx_gemm_a4_workspace_bytes(M, r(w)) == 0
+    assert lib.w4a16_mx_gemm_a4(r(x), r(w), p(0x500000), L.F32, p(0x600000), 1 << 40, None) == L.ERR_UNSUPPORTED
