@@ -550,7 +550,8 @@ W4A16_API w4a16_status_t w4a16_mx_quantize_weight(const void* w, w4a16_dtype_t w
 
 /*
  * ROWS -> TILED, into dst_codes and dst_scales (w4a16_mx_codes_bytes and
- * w4a16_mx_scales_bytes of the TILED layout); `out` receives the descriptor.
+ * w4a16_mx_scales_bytes of the TILED layout); `out` receives the descriptor and
+ * may be `src`.
  * Errors: INVALID_ARG (null/misaligned, overlapping), WORKSPACE (too small),
  * UNSUPPORTED (src not ROWS, rows not a multiple of 16, the limits above).
  */

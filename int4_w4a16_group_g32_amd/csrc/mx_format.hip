@@ -243,14 +243,15 @@ extern "C" w4a16_status_t w4a16_mx_prepack(const w4a16_mx_t* src, uint8_t* dst_c
     if (ranges_overlap(src->scales, ib, dst_codes, cb) || ranges_overlap(src->scales, ib, dst_scales, sb))
       return W4A16_ERR_INVALID_ARG;
   }
-  *out = *src;
+  const w4a16_mx_t m = *src;  // (out may be src)
+  *out = m;
   out->codes = dst_codes;
   out->scales = dst_scales;
   out->layout = W4A16_MX_TILED;
   if (cb == 0) return W4A16_OK;
   mx_prepack_kernel<<<blocks_for(sb), 256, 0, stream>>>(
-      reinterpret_cast<const uint4*>(src->codes), src->scales, src->rows, src->K / kMxBlock,
-      (src->K + kMxStep - 1) / kMxStep, sb, reinterpret_cast<uint4*>(dst_codes), dst_scales);
+      reinterpret_cast<const uint4*>(m.codes), m.scales, m.rows, m.K / kMxBlock, (m.K + kMxStep - 1) / kMxStep, sb,
+      reinterpret_cast<uint4*>(dst_codes), dst_scales);
   return launch_status();
 }
 
