@@ -142,7 +142,8 @@ W4A16_API size_t w4a16_prepacked_bytes(const w4a16_weight_t* w);
  * Permute CANONICAL codes into the GROUPED layout the compute kernels stream
  * (one-time load step; the weight and scale maps of page "The Final Wire",
  * section "The Multi-Step Integration Chain").  Scales are not moved: `out`
- * receives a GROUPED descriptor that points at `dst_qw` and at src->scales.
+ * receives a GROUPED descriptor that points at `dst_qw` and at src->scales, and
+ * may be `src`.
  * dst_qw (dst_bytes bytes) must hold w4a16_prepacked_bytes(src) bytes and
  * must not overlap src->qw.  Errors: INVALID_ARG (null/misaligned, out ==
  * NULL, overlap, dst_bytes too small; nothing is enqueued then), UNSUPPORTED

@@ -179,13 +179,13 @@ extern "C" w4a16_status_t w4a16_prepack(const w4a16_weight_t* src, int32_t* dst_
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(src->qw), a1 = a0 + words * 4;
   const uintptr_t b0 = reinterpret_cast<uintptr_t>(dst_qw), b1 = b0 + words * 4;
   if (words != 0 && a0 < b1 && b0 < a1) return W4A16_ERR_INVALID_ARG;
-  *out = *src;
+  const w4a16_weight_t w = *src;  // (out may be src)
+  *out = w;
   out->qw = dst_qw;
   out->layout = W4A16_LAYOUT_GROUPED;
-  const size_t total = static_cast<size_t>(src->num_experts) * (src->K / kGroup) * src->N;
+  const size_t total = static_cast<size_t>(w.num_experts) * (w.K / kGroup) * w.N;
   if (total == 0) return W4A16_OK;
-  prepack_kernel<<<grid_for(total, 256), 256, 0, stream>>>(src->qw, src->K, src->N,
-                                                           src->num_experts, dst_qw);
+  prepack_kernel<<<grid_for(total, 256), 256, 0, stream>>>(w.qw, w.K, w.N, w.num_experts, dst_qw);
   return launch_status();
 }
 
