@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 // four half-steps; borders between codes, and powers of two, have at most two
 // mantissa bits, so a value whose lower 21 are 16 steps or more from all zeros
 // is on the same side in float64.  Where some value of the wave is nearer (1 in
-// 2^17), the wave goes by float64.
+// 2^16, and every zero), the wave goes by float64.
 __device__ __forceinline__ uint32_t codes_of(const float s[8], const float w[8], double pre, uint32_t& byte) {
   const float p = static_cast<float>(pre);
   float v[8];
@@ -119,8 +119,9 @@ __device__ __forceinline__ uint32_t codes_of(const float s[8], const float w[8],
     low = min(low, (u + 16) & 0x1fffffu);
   }
   m = quad_max(m);
-  // (beside a largest of 2^-90 what float32 flushed is code 0 either way)
-  const bool near = low < 32 || m < (127u - 90u) << 23 || m >= 255u << 23 || !(p > 0x1p-100f && p < 0x1p100f);
+  // s * w below 2^-126 has lost bits, but with pre below 2^30 such a value, as one
+  // that is itself below 2^-126, is code 0 either way beside a largest of 2^-90
+  const bool near = low < 32 || m < (127u - 90u) << 23 || m >= 255u << 23 || !(p > 0x1p-100f && p < 0x1p30f);
   float o[8];
   if (!__any(near)) {
     byte = mx_scale_byte(m);

@@ -28,3 +28,26 @@ def test_the_residual_stream_normed_onto_itself(M, H, t, nt):
         assert torch.equal(m.codes, n.codes) and torch.equal(m.scales, n.scales)
     else:
         assert torch.equal(m, n)
+
+
+def _codes_are_float64s(n, nv):
+    q, sc = O.mx_quantize64(nv)
+    wrong = int((n.scales.cpu().numpy() != sc).sum()), int((n.codes.cpu().numpy() != O.mx_pack(q)).sum())
+    assert wrong == (0, 0), f"{wrong} scales and pairs of codes of {sc.size} and {q.size // 2}"
+
+
+def _f(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-40])
+@pytest.mark.parametrize("se,we", [(-75, -68), (-60, -80), (-100, 60), (60, -100), (100, -60), (-20, -20), (-40, -90)])
+@pytest.mark.parametrize("M,H,t", [(3, 4096, "f32"), (600, 2304, "bf16")])
+def test_codes_of_very_small_and_large_rows(M, H, t, se, we, eps):
+    """s and pre_w whose product leaves float32's normal range where s / rms(s) * pre_w does not."""
+    rng = np.random.default_rng(abs(se - 3 * we + M))
+    y = torch.as_tensor(np.ldexp(rng.standard_normal((M, H)), se)).to(TORCH[t])
+    w = torch.as_tensor(np.ldexp(rng.standard_normal(H), we)).to(TORCH[t])
+    n = L.mx_empty(M, H)
+    L.block_norm(y.cuda(), n=n, pre_w=w.cuda(), eps=eps)
+    _codes_are_float64s(n, O.block_norm64(_f(y), eps=eps, pre_w=_f(w))[1])
