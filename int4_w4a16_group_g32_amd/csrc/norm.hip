@@ -82,6 +82,9 @@ __device__ __forceinline__ float rounded_to_odd(double v) {
   return b == a || (u & 1) || !(b <= 3.4028234663852886e38) ? f : __uint_as_float(b > a ? u - 1 : u + 1);
 }
 
+__device__ __forceinline__ bool is_normal(float v) { return __builtin_amdgcn_classf(v, 0x108); }
+__device__ __forceinline__ bool is_normal(double) { return true; }
+
 // Sum over the workgroup, the same bits in every thread.
 template <typename F>
 __device__ __forceinline__ F row_sum(F v, F* lds) {
@@ -152,15 +155,15 @@ __device__ __forceinline__ uint32_t codes_of(const float s[8], const float w[8],
 // kB: y, r, the weights and gate are bf16; then a workgroup takes rows
 // blockIdx.x, + gridDim.x, ..., and asks for the next row's values as soon as it
 // holds s of its own (else one row: the values of two would not fit).
+// Two chunks are launched with at most 512 threads, four of bf16 too; with room
+// for 1024 the two-chunk float64 form of other types would spill.
 template <int kC, bool kMx, bool kB>
-__global__ __launch_bounds__(kB && kC > 1 ? 512 : 1024) void block_norm_kernel(const NormArgs a) {
+__global__ __launch_bounds__(kC == 2 || (kB && kC > 1) ? 512 : 1024) void block_norm_kernel(const NormArgs a) {
   using F = std::conditional_t<kMx, double, float>;
   constexpr bool kEarly = kB || kC == 1;  // (else too many registers)
   __shared__ F lds[2][2][16];
   const int t = static_cast<int>(threadIdx.x), T = static_cast<int>(blockDim.x);
   const int n8 = a.H / 8;
-  // products of three bf16 values are exact in float32
-  const bool exact = kB || (a.y_bf16 && a.w_bf16);
   Raw8<kB> y[kC], r[kC], g[kC], pw[kC], nw[kC];
   auto load = [&](int row) {
     const size_t base = static_cast<size_t>(row) * n8;
@@ -205,33 +208,36 @@ __global__ __launch_bounds__(kB && kC > 1 ? 512 : 1024) void block_norm_kernel(c
       if (!kEarly && a.r != nullptr) r[c] = get8<kB>(a.r, base + i, a.r_bf16);
       if (!kEarly && a.gate != nullptr) g[c] = get8<kB>(a.gate, (a.gate_rows == 1 ? 0 : base) + i, a.w_bf16);
       if (kC > 1 && a.post_w != nullptr) pw[c] = get8<kB>(a.post_w, i, a.w_bf16);
-      values8(y[c], a.y_bf16, v);
-      if (!kMx || exact) {
+      auto product = [&](auto* o, bool& normal) {
+        values8(y[c], a.y_bf16, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = v[j];
         if (a.post_w != nullptr) {
           values8(pw[c], a.w_bf16, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+          for (int j = 0; j < 8; ++j) o[j] *= w[j], normal &= is_normal(o[j]);
         }
         if (a.gate != nullptr) {
           values8(g[c], a.w_bf16, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+          for (int j = 0; j < 8; ++j) o[j] *= w[j], normal &= is_normal(o[j]);
         }
+      };
+      // In front of codes the products are float64's too: of three bf16 values
+      // float32 has them exactly inside its normal range, and a wave with one
+      // outside (or a zero) takes float64 (2048 x 7168 bf16: always 37.6 us, so 36.5)
+      bool normal = true;
+      if constexpr (kMx && kB) {
+        float f[8];
+        product(f, normal);
+        if (__any(!normal)) {
+          product(p, normal);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = v[j];
+          for (int j = 0; j < 8; ++j) p[j] = f[j];
+        }
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = v[j];
-        if (a.post_w != nullptr) {
-          values8(pw[c], a.w_bf16, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] *= w[j];
-        }
-        if (a.gate != nullptr) {
-          values8(g[c], a.w_bf16, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] *= w[j];
-        }
+        product(p, normal);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0.0f;

@@ -51,3 +51,18 @@ def test_codes_of_very_small_and_large_rows(M, H, t, se, we, eps):
     n = L.mx_empty(M, H)
     L.block_norm(y.cuda(), n=n, pre_w=w.cuda(), eps=eps)
     _codes_are_float64s(n, O.block_norm64(_f(y), eps=eps, pre_w=_f(w))[1])
+
+
+@pytest.mark.parametrize("ye,pe,ge", [(100, 40, -30), (-100, -40, 30), (-60, -30, -40), (-100, -40, 90), (60, 60, 60)])
+@pytest.mark.parametrize("M,H", [(3, 4096), (600, 2304)])
+def test_products_of_bf16_values_outside_float32s_range(M, H, ye, pe, ge):
+    """y * post_w * gate leaves float32's range where y / rms(y) * post_w * gate does not."""
+    rng = np.random.default_rng(abs(ye + 3 * pe) + M)
+    t = lambda e, *s: torch.as_tensor(np.ldexp(rng.standard_normal(s), e)).bfloat16()  # noqa: E731
+    y, post, gate, pre = t(ye, M, H), t(pe, H), t(ge, M, H), t(0, H)
+    s, n = torch.empty((M, H), dtype=torch.bfloat16, device="cuda"), L.mx_empty(M, H)
+    L.block_norm(y.cuda(), r_out=s, n=n, pre_w=pre.cuda(), post_w=post.cuda(), gate=gate.cuda(), eps=0.0)
+    stored = lambda v: torch.as_tensor(v).float().bfloat16().double().numpy()  # noqa: E731
+    sv, nv = O.block_norm64(_f(y), None, _f(post), _f(gate), 1.0, 0.0, _f(pre), stored)
+    assert np.isfinite(stored(sv)).all() and np.array_equal(_f(s), stored(sv))
+    _codes_are_float64s(n, nv)
