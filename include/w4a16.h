@@ -575,11 +575,12 @@ W4A16_API size_t w4a16_mx_gemm_workspace_bytes(int32_t M, w4a16_dtype_t xt, cons
 /*
  * y[M][N] = x[M][K] W^T for a TILED weight of N rows, x float32 or bf16, y
  * float32, or bf16 rounded once, to nearest even.  Weights and rows enter the
- * matrix cores as exact bf16 values (a float32 value as three whose sum it is),
- * sums are float32.  Rows do not affect one another: an infinity or NaN in x[m]
- * reaches y[m] only (an infinity among float32 values as NaN); a weight above
- * bf16's largest reaches its column as an infinity or NaN.  Deterministic: the
- * same inputs give bitwise the same y.  With K = 0, y is zeros.
+ * matrix cores as exact bf16 values (a float32 value as three whose sum it is;
+ * one below 2^-110, where bf16's steps end, to within 2^-134), sums are float32.
+ * Rows do not affect one another: an infinity or NaN in x[m] reaches y[m] only
+ * (an infinity among float32 values as NaN); a weight above bf16's largest
+ * reaches its column as an infinity or NaN.  Deterministic: the same inputs give
+ * bitwise the same y.  With K = 0, y is zeros.
  * Errors: INVALID_ARG (null/misaligned, M < 0, unknown type, y or ws overlapping
  * x, the weights or each other), UNSUPPORTED (layout, rows % 16, the limits above,
  * M * N above 2^33), WORKSPACE, HIP.
@@ -605,8 +606,8 @@ W4A16_API size_t w4a16_mx_swiglu_mlp_workspace_bytes(int32_t M, w4a16_dtype_t xt
 /*
  * w4a16_swiglu_mlp over MXFP4 weights: y = (silu(x Wg^T) * (x Wu^T)) Wd^T, gate
  * and up TILED with I rows of H, down with H rows of I; x and y as in
- * w4a16_mx_gemm.  h = silu(gate) up enters the down product whole with float32
- * x, and to within 2^-16 of each value (two bf16 pieces) with bf16 x.
+ * w4a16_mx_gemm.  h = silu(gate) up enters the down product as a float32 x would
+ * with float32 x, and to within 2^-16 of each value (two bf16 pieces) with bf16 x.
  * Errors as w4a16_mx_gemm, plus UNSUPPORTED if the three shapes do not chain.
  */
 W4A16_API w4a16_status_t w4a16_mx_swiglu_mlp(const void* x, w4a16_dtype_t xt, int32_t M, const w4a16_mx_t* gate,

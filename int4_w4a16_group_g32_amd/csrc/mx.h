@@ -130,7 +130,8 @@ __device__ __forceinline__ void mx_store_h(void* codes, uint8_t* scales, int row
 }
 
 // Four adjacent values as kN bf16 planes of `plane` elements: 8 significant
-// bits each, cut off, the last rounded to nearest (of three it is exact).
+// bits each, cut off, the last rounded to nearest (of three it is exact, down to
+// 2^-110: below, its lowest bits are under bf16's smallest step, 2^-133).
 template <int kN>
 __device__ __forceinline__ void mx_store_pieces(void* planes, size_t at, size_t plane, f32x4 v) {
 #pragma unroll
@@ -161,7 +162,7 @@ __device__ __forceinline__ void mx_store_hidden(void* h, size_t at, size_t plane
 
 // What the activations of a product are.
 enum MxX {
-  kMxXf32 = 0,   // float32, as three bf16 pieces: exact
+  kMxXf32 = 0,   // float32, as three bf16 pieces: exact (from 2^-110 on)
   kMxXf32h = 1,  // float32, as two bf16 pieces: 2^-17 (the intermediate of a bf16 layer)
   kMxXbf16 = 2,
   kMxXfp4 = 3    // MXFP4 rows

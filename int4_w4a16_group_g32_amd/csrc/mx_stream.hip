@@ -14,7 +14,8 @@
 //  - bf16 and float32 rows: codes and scale become exact bf16 values in one
 //    conversion per pair, and v_mfma_f32_16x16x32_bf16 takes codes 8j .. 8j+7 of
 //    every lane as its j-th 32 k, the rows of x in the same order.  float32
-//    values enter as three bf16 pieces whose sum they are exactly.
+//    values enter as three bf16 pieces whose sum they are (exactly from 2^-110 on,
+//    below to within 2^-134).
 //
 // Bound by the weights' bytes.  A workgroup owns the columns of one tile and
 // all of K: its waves take every kW-th step, so nothing is summed across
