@@ -505,8 +505,8 @@ hipError_t start_rows(int bm, const MxTileArgs& a, hipStream_t stream) {
       case 64: return start<0, kGlu, kM, 8 / kM, 1, 4 / kM, kN>(a, stream);
       default:  // 128
         if (a.cols == (kGlu ? 256 : 512)) return start<0, kGlu, 1, 8, 1, 8, 4>(a, stream);
-        if constexpr (!kGlu) return start<0, false, 1, 8, 1, 8, 2>(a, stream);
-        return start<0, kGlu, 2, 4, 1, 4, 4>(a, stream);
+        if constexpr (kGlu) return start<0, true, 2, 4, 1, 4, 4>(a, stream);
+        else return start<0, false, 1, 8, 1, 8, 2>(a, stream);
     }
   } else {
     switch (bm) {

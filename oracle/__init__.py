@@ -34,7 +34,6 @@ from .mx import (  # noqa: F401
     mx_pack,
     mx_quantize64,
     mx_round64,
-    mx_swiglu_mlp64,
     mx_tiled,
     mx_values64,
 )

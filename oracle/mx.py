@@ -8,8 +8,6 @@ from __future__ import annotations
 
 import numpy as np
 
-from .w4a16 import silu64
-
 _MAG = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 
@@ -64,12 +62,6 @@ def mx_tiled(codes, scales):
             c[r // 64, g // 4, r // 16 % 4, 16 * (g % 4) + r % 16] = codes[r, 16 * g:16 * g + 16]
             s[r // 64, g // 4, 16 * (g % 4) + r % 16, r // 16 % 4] = scales[r, g]
     return c, s
-
-
-def mx_swiglu_mlp64(x, gate, up, down, round_h=False):
-    """x and the weights as values (weights [rows][K]); round_h: h as MXFP4 rows."""
-    h = silu64(x @ gate.T) * (x @ up.T)
-    return (mx_round64(h) if round_h else h) @ down.T
 
 
 def block_norm64(y, r=None, post_w=None, gate=None, alpha=1.0, eps=1e-6, pre_w=None, store=None):
