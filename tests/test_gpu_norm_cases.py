@@ -1,11 +1,13 @@
 """block_norm on the GPU: calls that lie beside those of test_gpu_norm.py."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
 
 import int4_w4a16_group_g32_amd as L
 import oracle as O
-from mx_bounds import TORCH
+from mx_bounds import HALF_STEP, TORCH, check
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,38 @@ def test_products_of_bf16_values_outside_float32s_range(M, H, ye, pe, ge):
     sv, nv = O.block_norm64(_f(y), None, _f(post), _f(gate), 1.0, 0.0, _f(pre), stored)
     assert np.isfinite(stored(sv)).all() and np.array_equal(_f(s), stored(sv))
     _codes_are_float64s(n, nv)
+
+
+@pytest.mark.parametrize("yt,rt,wt", [("bf16", "bf16", "bf16"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16"), ("f32", "bf16", "bf16")])
+@pytest.mark.parametrize("M,H", [(3, 96), (300, 2304), (5, 8224)])
+def test_every_combination_of_the_optional_tensors(M, H, yt, rt, wt):
+    """r, post_w, gate, r_out and n, each there or not; n as values and as MXFP4."""
+    rng = np.random.default_rng(M + H)
+    t = lambda ty, *s: torch.as_tensor(rng.standard_normal(s)).to(TORCH[ty]).cuda()  # noqa: E731
+    y, res, pre, post, gates = t(yt, M, H), t(rt, M, H), t(wt, H), t(wt, H), {"channel": t(wt, H), "row": t(wt, M, H)}
+    for has_r, has_post, gate, out in itertools.product((0, 1), (0, 1), (None, "channel", "row"), ("r", "n", "rn", "mx", "rmx")):
+        r, pw, g = res if has_r else None, post if has_post else None, gates.get(gate)
+        st = rt if has_r or "r" in out else yt  # s's type
+        r_out = torch.full((M, H), float("nan"), dtype=TORCH[st], device="cuda") if "r" in out else None
+        n = L.mx_empty(M, H) if "mx" in out else torch.empty((M, H), device="cuda") if "n" in out else None
+        L.block_norm(y, r, r_out, n, pre_w=None if n is None else pre, post_w=pw, gate=g, alpha=0.75)
+        stored = lambda v: torch.as_tensor(v).float().to(TORCH[st]).double().numpy()  # noqa: E731
+        f = lambda v: None if v is None else _f(v)  # noqa: E731
+        s, nv = O.block_norm64(_f(y), f(r), f(pw), f(g), 0.75, 1e-6, _f(pre), stored)
+        what = f"r {has_r} post {has_post} gate {gate} out {out}"
+        if "mx" in out:
+            _codes_are_float64s(n, nv)
+            assert r_out is None or np.array_equal(_f(r_out), stored(s)), what
+            continue
+        part = np.abs(s - (f(r) if has_r else 0.0))
+        b = 2.0 ** -18 * part + 2.0 ** -23 * np.abs(s)
+        step = HALF_STEP[TORCH[st]]
+        if r_out is not None:
+            check(r_out, s, b + step * (np.abs(s) + b) + 1e-37, what)
+        if n is not None:
+            # s may be stored a step off what float64 stores (b and the type's rounding), which moves its mean and itself
+            ds = b + step * (np.abs(s) + b)
+            rms = np.sqrt((stored(s) ** 2).mean(1, keepdims=True) + 1e-6)
+            moved = np.sqrt((ds ** 2).mean(1, keepdims=True)) / rms
+            lim = 2 * ((ds + np.abs(s) * moved) / rms * np.abs(_f(pre))) + (2.0 ** -18 + 2.0 ** -24) * np.abs(nv)
+            check(n, nv, lim / (1 - moved) + 1e-37, what)
