@@ -118,7 +118,10 @@ MxMlpPlan plan_mx_mlp(int M, const w4a16_mx_t* gate, MxX kind) {
   MxMlpPlan p;
   Carve c;
   const size_t n = static_cast<size_t>(M) * gate->rows;
-  // h of bf16 rows keeps 16 bits, well under the rounding of its own operands
+  // h of bf16 rows keeps 16 bits (two pieces), well under the rounding of its own
+  // operands and of a bf16 y: 64 rows, 7168 / 18432, y is 1.66e-3 off float64 with
+  // two pieces and with three, and 1.3e-4 or 0.8e-4 off a float32 composition.  The
+  // third piece would cost 94 -> 108 us there, 870 -> 1083 at 1024 rows.
   p.hkind = kind == kMxXbf16 ? kMxXf32h : kind;
   p.gu = plan_mx_product(M, gate->rows, gate->K, kind, true);
   p.dn = plan_mx_product(M, gate->K, gate->rows, p.hkind, false);
@@ -202,8 +205,9 @@ w4a16_status_t mx_swiglu_mlp(const MxRows& r, int M, const w4a16_mx_t* gate, con
 // and a launch of about 4 us.
 //
 // Up to 16 rows stream.  More rows stream in blocks of 16, each reading the
-// weights (from the L2, mostly) and all of x once a workgroup, while that is
-// shorter than the tiles' longer way: 37 float32 rows, 2304 -> 7168, 15 us
+// weights (a column's row blocks lie on several XCDs, so past the L2 each: 37
+// float32 rows, 2304 -> 7168, read 27.6 MB for 8.8 of weights) and all of x once a
+// workgroup, while that is shorter than the tiles' longer way: 37 float32 rows, 2304 -> 7168, 15 us
 // streamed and 25 in tiles, 7168 -> 18432 85 and 56; 64 bf16 rows, 2304 -> 7168,
 // 13.5 and 18.4, 7168 -> 18432 73 and 32.  The times below, in us, are fitted to
 // such measurements (17 to 128 rows, K 1056 to 7168, N 1040 to 18432).

@@ -28,9 +28,10 @@
 // 7168 / 18432 MLP in 86 us).
 //
 // Measured: four float32 rows through that MLP 43 us (4.9 TB/s of its 211 MB; gate
-// and up alone 5.0), 16 bf16 rows, 7168 -> 4096, 8 us (2 TB/s: one load's way and
-// the sums are most of a workgroup's life), one row, 256 -> 512, 3.5 us of kernel
-// and 7.6 of call.
+// and up alone 5.0), 16 bf16 rows, 7168 -> 4096, 8 us (2 TB/s of weights: each of
+// the 256 workgroups also reads all of x, 59 MB through the L2, and takes seven
+// steps a wave with one load's way before them and the sums after), one row,
+// 256 -> 512, 3.5 us of kernel and 7.6 of call.
 #include "mx.h"
 
 namespace w4 {

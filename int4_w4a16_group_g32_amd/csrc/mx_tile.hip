@@ -24,8 +24,10 @@
 // and a stage's barrier); MXFP4 rows the same product 37 us (3.3 PFLOP/s, 29 %),
 // where a stage's chain of code loads, staging and LDS reads, at two waves a SIMD,
 // is longer than its 64 products a wave; 1024 MXFP4 rows through the 7168 / 18432
-// MLP 243 us (3.35 PFLOP/s).  64 bf16 rows through it 91 us, 2.3 TB/s of weights:
-// each workgroup's start, the sums' planes (12 us) and the expansion.
+// MLP 246 us (3.3 PFLOP/s; the instruction alone issues at 8).  64 bf16 rows through
+// it 93 us, 2.3 TB/s of weights: each workgroup's start, the sums' planes
+// (12 us) and the expansion.  The tiles of 64 float32 rows spill a few registers
+// (gate and up 7, a product alone 3).
 #include "mx.h"
 
 #include <cmath>

@@ -9,7 +9,13 @@
 // and everything between the loads and stores are float32; where n goes to
 // 4-bit codes they are float64, since a code's borders turn a last-bit
 // difference into half a step: the codes then do not depend on the order of the
-// sums (the vector units' float64 work stays under the memory's time).
+// sums.
+//
+// Measured, 2048 x 7168 with a gate a row: bf16 to bf16 33.1 us (4.4 TB/s; a copy
+// 4.76), to MXFP4 36.5 (3.4 TB/s: fewer bytes and the same barriers, so the
+// float64 work is what is left over); float32 62.5 and 65.2; bf16 on a float32
+// stream to MXFP4 60.2.  Above H = 8192 the forms that are not all bf16 spill
+// (1024 threads leave 128 registers): 1024 x 16384 float32 143 us, to MXFP4 201.
 #include "mx.h"
 
 #include <type_traits>
