@@ -282,9 +282,12 @@ def _ready(t, name: str, dtype, shape, dev: int):
         _on_device(**{name: t})
 
 
-def _device_of(t) -> int:
+def _device_of(t, name: str = "y") -> int:
     """The current device, of which `t` must be."""
-    d = t.get_device()
+    try:
+        d = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     return d if d >= 0 and d == _current_device() else -2  # (no tensor is of device -2)
 
 
@@ -338,9 +341,12 @@ class MxMatrix:
             nc, ns = tiles * 4096, tiles * 256
         else:
             nc, ns = rows * (K // 2), rows * (K // 32)
-        if (c.dtype is _U8 and s.dtype is _U8 and c.numel() == nc and s.numel() == ns and c.is_contiguous()
-                and s.is_contiguous() and c.get_device() == dev and s.get_device() == dev):
-            return
+        try:
+            if (c.dtype is _U8 and s.dtype is _U8 and c.numel() == nc and s.numel() == ns and c.is_contiguous()
+                    and s.is_contiguous() and c.get_device() == dev and s.get_device() == dev):
+                return
+        except AttributeError:  # (no tensor)
+            pass
         _need(c, f"{name}.codes", torch.uint8)
         _need(s, f"{name}.scales", torch.uint8)
         if (c.numel(), s.numel()) != (nc, ns):
@@ -728,7 +734,7 @@ def _mx_io(y, M: int, N: int, ws, dev: int) -> int:
     """y float32 or bfloat16 [M][N], ws bytes; returns y's type code."""
     yt = _dtype_code(y)
     _ready(y, "y", y.dtype, (M, N), dev)
-    _ready(ws, "ws", _U8, ws.shape, dev)
+    _ready(ws, "ws", _U8, getattr(ws, "shape", None), dev)
     return yt
 
 

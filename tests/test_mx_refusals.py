@@ -3,6 +3,7 @@ past the limits (nothing is enqueued: these pointers are not device memory)."""
 import ctypes
 
 import pytest
+import torch
 
 import int4_w4a16_group_g32_amd as L
 
@@ -43,3 +44,27 @@ def test_products_of_more_values_than_the_limit_have_no_workspace_size(lib, M, r
         assert lib.w4a16_mx_gemm(p(0x300000), xt, M, r(w), p(0x500000), L.F32, p(0x600000), 1 << 40, None) == L.ERR_UNSUPPORTED
     assert lib.w4a16_mx_gemm_a4_workspace_bytes(M, r(w)) == 0
     assert lib.w4a16_mx_gemm_a4(r(x), r(w), p(0x500000), L.F32, p(0x600000), 1 << 40, None) == L.ERR_UNSUPPORTED
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on device 0."""
+
+    def get_device(self):
+        return 0
+
+
+def test_what_is_no_tensor_is_a_type_error(lib, monkeypatch):
+    """Outputs, workspaces and a matrix's parts, as in the other calls."""
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
+    monkeypatch.setattr(L, "_stream_of", lambda *a: pytest.fail("the library was reached"))
+    z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t).as_subclass(_OnDevice)  # noqa: E731
+    w = L.MxMatrix(z(8192, t=torch.uint8), z(512, t=torch.uint8), 128, 128, L.MX_TILED)
+    x, y, ws = z(2, 128), z(2, 128), z(256, t=torch.uint8)
+    for bad in (L.MxMatrix(None, w.scales, 128, 128, L.MX_TILED), L.MxMatrix(w.codes, None, 128, 128, L.MX_TILED)):
+        with pytest.raises(TypeError):
+            L.mx_gemm(x, bad, y, ws)
+    for a, b in ((None, ws), (y, None)):
+        with pytest.raises(TypeError):
+            L.mx_gemm(x, w, a, b)
+        with pytest.raises(TypeError):
+            L.mx_swiglu_mlp(x, w, w, w, a, b)
