@@ -703,14 +703,19 @@ def mx_dequantize(m: MxMatrix, out: torch.Tensor, stream=None):
 
 
 def mx_quantize_to_weight(w: torch.Tensor, stream=None) -> MxMatrix:
-    """Quantize device weights [K][N] and prepack them (TILED)."""
+    """Quantize device weights [K][N] and prepack them (TILED).  With a stream, the weight is made there: the
+    current one uses it once it has waited for that."""
     K, N = w.shape
     if stream is not None:
         _stream(stream)  # (of the current device)
     with torch.cuda.stream(stream):  # the rows, freed on return, are that stream's memory
         rows = mx_empty(N, K, MX_ROWS, w.device)
         mx_quantize_weight(w, rows, stream)
-        return mx_prepack(rows, mx_empty(N, K, MX_TILED, w.device), stream)
+        out = mx_prepack(rows, mx_empty(N, K, MX_TILED, w.device), stream)
+    if stream is not None:  # freed later, its memory is that stream's again when the current one is done with it
+        for t in (out.codes, out.scales):
+            t.record_stream(torch.cuda.current_stream())
+    return out
 
 
 def mx_gemm_workspace_bytes(M: int, xt: int, w: MxMatrix) -> int:

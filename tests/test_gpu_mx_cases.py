@@ -143,3 +143,25 @@ def test_quantised_rows_and_weights_that_were_not_finite(M):
         want = torch.zeros((M, N), dtype=torch.bool)
         want[:, 9], want[bad_rows] = True, True
         assert torch.equal(nan, want)
+
+
+def test_weights_made_on_another_stream_and_freed_while_in_use():
+    """Their memory is that stream's: the next weights made there are not put over them before the current
+    stream's product, still waiting behind other work, has read them."""
+    torch.manual_seed(5)
+    a, b = torch.randn((4096, 4096), device="cuda"), torch.randn((4096, 4096), device="cuda")
+    x, busy = torch.randn((4, 4096), device="cuda"), torch.randn((4096, 4096), device="cuda")
+    want = _gemm(x, L.mx_quantize_to_weight(a), 4096, "f32")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ws = L.new_workspace(L.mx_gemm_workspace_bytes(4, L.F32, L.mx_quantize_to_weight(a)))
+    y = torch.empty_like(want)
+    w = L.mx_quantize_to_weight(a, side)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        torch.mm(busy, busy, out=b)  # some 40 ms
+    L.mx_gemm(x, w, y, ws)
+    del w
+    other = [L.mx_quantize_to_weight(busy, side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and len(other) == 3
