@@ -853,12 +853,18 @@ def new_workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
 
 
 def quantize_to_weight(w: torch.Tensor, stream=None) -> Weight:
-    """Quantize float32 device weights [E][K][N] or [K][N] and prepack them (GROUPED)."""
+    """Quantize float32 device weights [E][K][N] or [K][N] and prepack them (GROUPED).  With a stream, the weight is
+    made there: the current one uses it once it has waited for that."""
     E = 1 if w.dim() == 2 else w.shape[0]
     K, N = w.shape[-2], w.shape[-1]
-    qw = torch.empty((E, K // 8, N), dtype=torch.int32, device=w.device)
-    sc = torch.empty((E, K // GROUP, N), dtype=torch.float32, device=w.device)
-    quantize(w, qw, sc, stream)
-    canon = Weight(qw, sc, K, N, E, LAYOUT_CANONICAL)
-    dst = torch.empty_like(qw)
-    return prepack(canon, dst, stream)
+    if stream is not None:
+        _stream(stream)  # (of the current device)
+    with torch.cuda.stream(stream):  # the canonical codes, freed on return, are that stream's memory
+        qw = torch.empty((E, K // 8, N), dtype=torch.int32, device=w.device)
+        sc = torch.empty((E, K // GROUP, N), dtype=torch.float32, device=w.device)
+        quantize(w, qw, sc, stream)
+        out = prepack(Weight(qw, sc, K, N, E, LAYOUT_CANONICAL), torch.empty_like(qw), stream)
+    if stream is not None:  # freed later, its memory is that stream's again when the current one is done with it
+        for t in (out.qw, out.scales):
+            t.record_stream(torch.cuda.current_stream())
+    return out
